@@ -1,0 +1,411 @@
+"""Workloads of the microscaled 4-bit operators and of the adapter's dropout.
+
+Four operators, in the forms a QLoRA user runs them:
+
+  codec    MXFP4 quantisation of a matrix and its dequantisation
+  mx_fwd   the QLoRA linear's forward over an MXFP4 base (decode and prefill)
+  mx_bwd   its backward (dX, dA, dB)
+  dropout  counter-based dropout: element-wise, and a training step of the
+           NF4 linear with dropout on the adapter's input
+
+``run`` computes them with elementary torch operations, or, where ``own`` is
+set, with this repository's kernels.  ``exact`` states them in 64 bits.
+"""
+
+import statistics
+
+import torch
+
+own = False
+
+GROUP = 8                                   # elements per generator call
+M0, M1 = 0xD2511F53, 0xCD9E8D57             # Philox4x32 multipliers
+W0, W1 = 0x9E3779B9, 0xBB67AE85             # Philox key increments
+ROUNDS = 7
+MASK32 = 0xFFFFFFFF
+
+
+# ------------------------------------------------------------------ the cases
+def listed():
+    return [
+        # one token's activations, quantised on their own
+        dict(name="codec-token", op="codec", rows=1, cols=4096, dtype="bf16"),
+        # a bulk tile of a 70B-shaped layer's weight, as a conversion pass sees it
+        dict(name="codec-tile", op="codec", rows=4096, cols=8192, dtype="bf16"),
+        # decode of one token through a 70B-shaped q/o projection
+        dict(name="fwd-decode-1", op="mx_fwd", M=1, N=8192, K=8192, r=64, p=0.0, want_H=False),
+        # a small decode batch through the gate projection, r = 16
+        dict(name="fwd-decode-13", op="mx_fwd", M=13, N=28672, K=8192, r=16, p=0.0, want_H=False),
+        # prefill of 4096 tokens through the q/o projection
+        dict(name="fwd-prefill", op="mx_fwd", M=4096, N=8192, K=8192, r=64, p=0.0, want_H=False),
+        # a ragged training batch through a 7B-shaped gate projection, adapter dropout on
+        dict(name="fwd-train-ragged", op="mx_fwd", M=777, N=18944, K=3584, r=16, p=0.1, want_H=True),
+        # backward of a full training batch through the q/o projection
+        dict(name="bwd-train", op="mx_bwd", M=4096, N=8192, K=8192, r=64, p=0.05),
+        # backward of a short ragged batch through a 7B-shaped k/v projection, no dropout
+        dict(name="bwd-ragged", op="mx_bwd", M=333, N=512, K=3584, r=8, p=0.0),
+        # dropout of an activation matrix
+        dict(name="dropout-tile", op="dropout", n=4096 * 8192, dtype="bf16", p=0.1),
+        # dropout of one odd-sized fp32 vector
+        dict(name="dropout-odd", op="dropout", n=4099, dtype="f32", p=0.5),
+        # forward and backward of the 4096 x 4096 NF4 projection with adapter dropout
+        dict(name="nf4-step", op="nf4_step", M=2048, N=4096, K=4096, r=16, p=0.1),
+        # the same for a handful of tokens and a narrow projection
+        dict(name="nf4-step-small", op="nf4_step", M=61, N=512, K=3584, r=24, p=0.25),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    x = lo * (hi / lo) ** rng.random()
+    return max(lo, min(hi, int(round(x))))
+
+
+def draw(rng):
+    op = rng.choice(["codec", "codec", "mx_fwd", "mx_fwd", "mx_fwd", "mx_bwd", "mx_bwd", "dropout", "dropout",
+                     "nf4_step"])
+    if op == "codec":
+        cols = _log_int(rng, 1, 28672)
+        rows = _log_int(rng, 1, max(1, min(28672, (4096 * 8192) // cols)))
+        return dict(op=op, rows=rows, cols=cols, dtype=rng.choice(["bf16", "f32"]))
+    if op == "dropout":
+        return dict(op=op, n=_log_int(rng, 1, 4096 * 8192), dtype=rng.choice(["bf16", "f32"]),
+                    p=rng.choice([0.0, 0.05, 0.1, 0.25, 0.5, 0.9]))
+    N = 64 * _log_int(rng, 1, 300 if op != "nf4_step" else 128)
+    K = 64 * _log_int(rng, 1, 128)
+    M = _log_int(rng, 1, 4096 if op != "nf4_step" else 2048)
+    M = max(1, min(M, (4096 * 8192 * 4096) // (N * K)))
+    r = rng.choice([1, 4, 8, 13, 16, 24, 32, 48, 64])
+    p = rng.choice([0.0, 0.05, 0.1, 0.25, 0.5])
+    if op == "mx_fwd":
+        if rng.random() < 0.2:
+            return dict(op=op, M=M, N=N, K=K, r=0, p=0.0, want_H=False)   # base alone
+        return dict(op=op, M=M, N=N, K=K, r=r, p=p, want_H=bool(rng.random() < 0.5))
+    return dict(op=op, M=M, N=N, K=K, r=r, p=p)
+
+
+def work(case):
+    op = case["op"]
+    if op == "codec":
+        n = case["rows"] * case["cols"]
+        # the matrix in, its codes and scales out, the bf16 values out
+        return {"bytes": n * (2 if case["dtype"] == "bf16" else 4) + n * 17 // 32 + 2 * n, "flops": 0}
+    if op == "dropout":
+        return {"bytes": case["n"] * (4 if case["dtype"] == "bf16" else 8), "flops": case["n"]}
+    M, N, K, r = case["M"], case["N"], case["K"], case["r"]
+    wb = N * K * 17 // 32 if op != "nf4_step" else N * K // 2 + N * K // 64
+    low = 2 * M * r * (N + K)
+    if op == "mx_fwd":
+        h = 4 * M * r if case["want_H"] else 0
+        return {"bytes": 2 * M * (N + K) + wb + 2 * r * (N + K) + h, "flops": 2 * M * N * K + low}
+    if op == "mx_bwd":
+        return {"bytes": 2 * M * N + 4 * M * K + wb + 4 * M * r + 4 * r * (N + K),
+                "flops": 2 * M * N * K + 2 * low}
+    return {"bytes": 4 * M * (N + K) + wb + 4 * M * r + 4 * r * (N + K), "flops": 4 * M * N * K + 3 * low}
+
+
+# ------------------------------------------------------------------ plain forms
+def _mx_encode(x):
+    """MXFP4 of a matrix: codes (uint8, one a cell) and scale bytes, rows padded to 256 columns."""
+    rows, cols = x.shape
+    pad = (cols + 255) // 256 * 256
+    v = torch.zeros((rows, pad), dtype=torch.float32, device=x.device)
+    v[:, :cols] = x.float()
+    v = v.view(rows, pad // 32, 32)
+    amax = v.abs().amax(dim=2)
+    e = torch.frexp(amax).exponent.to(torch.int32) - 3          # floor(log2 amax) - 2
+    e = torch.where(amax == 0, torch.full_like(e, -127), e.clamp(min=-127))
+    m = torch.ldexp(v.abs(), -e[:, :, None])
+    code = ((m > 0.25).to(torch.uint8) + (m >= 0.75).to(torch.uint8) + (m > 1.25).to(torch.uint8)
+            + (m >= 1.75).to(torch.uint8) + (m > 2.5).to(torch.uint8) + (m >= 3.5).to(torch.uint8)
+            + (m > 5.0).to(torch.uint8))
+    code = code | (torch.signbit(v).to(torch.uint8) << 3)
+    return code.view(rows, pad), (e + 127).to(torch.uint8)
+
+
+def _mx_decode(code, scale, cols):
+    """fp32 values of unpacked codes and scale bytes."""
+    level = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float32,
+                         device=code.device)
+    rows, pad = code.shape
+    v = level[code.to(torch.int64)].view(rows, pad // 32, 32)
+    return torch.ldexp(v, scale.to(torch.int32)[:, :, None] - 127).view(rows, pad)[:, :cols]
+
+
+def _pack(code):
+    """Two codes a byte, low nibble first."""
+    c = code.view(code.shape[0], -1, 2)
+    return (c[:, :, 0] | (c[:, :, 1] << 4)).contiguous()
+
+
+def _unpack(packed):
+    return torch.stack((packed & 15, packed >> 4), dim=2).view(packed.shape[0], -1)
+
+
+def _threshold(p):
+    return min(65535, int(p * 65536 + 0.5))
+
+
+def _keep(n, p, seed, offset, device):
+    """Truth values of the n kept elements: 8 sixteen-bit fields of one Philox4x32-7 call for each 8 elements."""
+    g = torch.arange((n + GROUP - 1) // GROUP, dtype=torch.int64, device=device)
+    c = [g & MASK32, g >> 32, torch.full_like(g, offset & MASK32), torch.full_like(g, offset >> 32)]
+    k0, k1 = seed & MASK32, seed >> 32
+    for _ in range(ROUNDS):
+        p0, p1 = c[0] * M0, c[2] * M1                          # modulo 2^64, in two's complement
+        c = [((p1 >> 32) & MASK32) ^ c[1] ^ k0, p1 & MASK32, ((p0 >> 32) & MASK32) ^ c[3] ^ k1, p0 & MASK32]
+        k0, k1 = (k0 + W0) & MASK32, (k1 + W1) & MASK32
+    f = torch.stack([h for w in c for h in (w & 0xFFFF, w >> 16)], dim=1).view(-1)[:n]
+    return f >= _threshold(p)
+
+
+def _scale(p):
+    """1 / (1 - p) for the p that the 16-bit threshold stands for."""
+    return 65536.0 / (65536 - _threshold(p))
+
+
+def _nf4_levels():
+    """The NF4 table: normal quantiles, 7 rows below zero and 8 above, ending at -1 and 1."""
+    q = statistics.NormalDist().inv_cdf
+    top = 1.0 - 31.0 / 960.0
+    pos = [q(0.5 + (top - 0.5) * i / 8) for i in range(9)]
+    neg = [q(0.5 + (top - 0.5) * i / 7) for i in range(8)]
+    return [-x / neg[7] for x in neg[:0:-1]] + [0.0] + [x / pos[8] for x in pos[1:]]
+
+
+def _nf4_values(codes, absmax_q, scale2, N, K):
+    """bf16 weight values (held in fp32) of packed NF4 codes with double-quantised scales."""
+    table = torch.tensor(_nf4_levels(), dtype=torch.float32, device=codes.device)
+    q = torch.stack((codes & 15, codes >> 4), dim=1).view(-1)
+    a = absmax_q.float() * scale2.repeat_interleave(256)[:absmax_q.numel()]
+    return (table[q.to(torch.int64)].view(-1, 64) * a[:, None]).to(torch.bfloat16).float().view(N, K)
+
+
+def _dropped(x, p, seed, offset):
+    """x (fp32) with its dropped elements zero; the factor 1/(1-p) is left to the caller."""
+    if p == 0.0:
+        return x
+    return torch.where(_keep(x.numel(), p, seed, offset, x.device).view(x.shape), x, torch.zeros((), device=x.device))
+
+
+def _plain_fwd(X, What, A, B, s, case, rng):
+    """(Y, H) of the linear over base values What and base input X[0]; the adapter reads X[1]."""
+    Y = X[0] @ What.t()
+    H = None
+    if A is not None:
+        H = (_dropped(X[1], case["p"], *rng) @ A.float().t()) * _scale(case["p"])
+        Y = Y + (H @ B.float().t()) * s
+    return Y.to(torch.bfloat16), H
+
+
+def _plain_bwd(G, X, H, What, A, B, s, case, rng):
+    c = _scale(case["p"])
+    dH = (G @ B.float()) * s
+    dB = (G.t() @ H) * s
+    dA = (dH.t() @ _dropped(X, case["p"], *rng)) * c
+    dX = G @ What + _dropped(dH @ A.float(), case["p"], *rng) * c
+    return dX.to(torch.bfloat16), dA.to(torch.bfloat16), dB.to(torch.bfloat16)
+
+
+# ------------------------------------------------------------------ inputs
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    op = case["op"]
+    st = {"case": case, "rng": ((0x5DEECE66D1234567 ^ (seed * 0x9E3779B1)) % (1 << 64), (seed * 7 + 1) % (1 << 64))}
+
+    def normal(shape, std, dtype=torch.bfloat16):
+        return (torch.randn(shape, generator=gen, device=dev) * std).to(dtype)
+
+    if op in ("codec", "dropout"):
+        dt = torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+        shape = (case["rows"], case["cols"]) if op == "codec" else (case["n"],)
+        x = normal(shape, 1.0, torch.float32)
+        if op == "codec":   # activations: some channels far larger than the rest
+            x = x * torch.exp(torch.randn((1, case["cols"]), generator=gen, device=dev))
+        st["x"] = x.to(dt)
+        if own:
+            from bit_nf4_quantized_08_amd import lib
+            if op == "dropout":
+                st["drop"] = lib.Dropout(case["p"], *st["rng"])
+                st["out"] = torch.empty_like(st["x"])
+            else:
+                st["q"] = lib.MXMatrix.empty(case["rows"], case["cols"], dev)
+                st["out"] = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        return st
+
+    M, N, K, r = case["M"], case["N"], case["K"], case["r"]
+    st["alpha"] = 2.0 * r
+    W = normal((N, K), 0.02, torch.float32)
+    if op == "nf4_step":
+        blocks = W.view(-1, 64)
+        absmax = blocks.abs().amax(dim=1)
+        lv = _nf4_levels()
+        mid = torch.tensor([(a + b) / 2 for a, b in zip(lv, lv[1:])], dtype=torch.float32, device=dev)
+        code = torch.bucketize((blocks / absmax[:, None]).contiguous(), mid).to(torch.uint8)
+        st["codes"] = _pack(code).view(-1)
+        nb = absmax.numel()
+        padded = torch.zeros((nb + 255) // 256 * 256, dtype=torch.float32, device=dev)
+        padded[:nb] = absmax
+        st["scale2"] = padded.view(-1, 256).amax(dim=1) / 255
+        st["absmax_q"] = (torch.ceil(padded.view(-1, 256) / st["scale2"][:, None] - 0.5).clamp(0, 255)
+                          .to(torch.uint8).view(-1)[:nb].contiguous())
+    else:
+        code, st["scales"] = _mx_encode(W)
+        st["codes"] = _pack(code)
+    del W
+    st["X"] = normal((M, K), 1.0)
+    st["A"] = normal((r, K), 0.01) if r else None
+    st["B"] = normal((N, r), 0.01) if r else None
+    if op != "mx_fwd":
+        st["G"] = normal((M, N), 1.0)
+    if op == "mx_bwd":   # what the forward left
+        st["H"] = ((_dropped(st["X"].float(), case["p"], *st["rng"]) @ st["A"].float().t()) * _scale(case["p"])).contiguous()
+    if own:
+        from bit_nf4_quantized_08_amd import lib
+        st["drop"] = lib.Dropout(case["p"], *st["rng"]) if case["p"] > 0.0 else None
+        if op == "nf4_step":
+            st["drop"] = lib.Dropout(case["p"], *st["rng"])
+            st["w"] = lib.NF4Weight(st["codes"], None, st["absmax_q"], st["scale2"], N, K)
+            st["ws"] = lib.workspace(lib.QN_OP_FWD_DROPOUT, M, N, K, r, dev)
+            st["ws_b"] = lib.workspace(lib.QN_OP_BWD, M, N, K, r, dev)
+        else:
+            st["w"] = lib.MXMatrix(st["codes"], st["scales"], N, K)
+            st["ws"] = lib.mx_workspace(lib.QN_OP_FWD if op == "mx_fwd" else lib.QN_OP_BWD, M, N, K, r, dev)
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        if op != "mx_bwd":
+            st["Y"] = torch.empty((M, N), **bf)
+            st["Hout"] = (torch.empty((M, r), dtype=torch.float32, device=dev)
+                          if op == "nf4_step" or case["want_H"] else None)
+        if op != "mx_fwd":
+            st["grads"] = (torch.empty((M, K), **bf), torch.empty((r, K), **bf), torch.empty((N, r), **bf))
+    return st
+
+
+# ------------------------------------------------------------------ one pass
+def run(st):
+    case = st["case"]
+    op = case["op"]
+    if own:
+        from bit_nf4_quantized_08_amd import lib
+        if op == "codec":
+            lib.mxfp4_quantize(st["x"], out=st["q"])
+            return lib.mxfp4_dequant(st["q"], out=st["out"])
+        if op == "dropout":
+            return lib.dropout(st["x"], st["drop"], out=st["out"])
+        if op == "mx_fwd":
+            return lib.qlora_mx_linear_fwd(st["X"], st["w"], st["A"], st["B"], st["alpha"], drop=st["drop"],
+                                           Y=st["Y"], H=st["Hout"], ws=st["ws"])
+        if op == "mx_bwd":
+            return lib.qlora_mx_linear_bwd(st["G"], st["X"], st["w"], st["A"], st["B"], st["alpha"],
+                                           drop=st["drop"], H=st["H"], out=st["grads"], ws=st["ws"])
+        Y, H = lib.qlora_linear_fwd_dropout(st["X"], st["w"], st["A"], st["B"], st["alpha"], st["drop"],
+                                            Y=st["Y"], H=st["Hout"], ws=st["ws"])
+        return (Y, H) + tuple(lib.qlora_linear_bwd_dropout(st["G"], st["X"], st["w"], st["A"], st["B"], st["alpha"],
+                                                           st["drop"], H=H, out=st["grads"], ws=st["ws_b"]))
+    if op == "codec":
+        code, scale = _mx_encode(st["x"])
+        return _mx_decode(code, scale, case["cols"]).to(torch.bfloat16)
+    if op == "dropout":
+        x = st["x"]
+        return (_dropped(x.float(), case["p"], *st["rng"]) * _scale(case["p"])).to(x.dtype)
+    N, K, A, B = case["N"], case["K"], st["A"], st["B"]
+    s = st["alpha"] / case["r"] if case["r"] else 0.0
+    X = st["X"].float()
+    if op == "nf4_step":
+        What = _nf4_values(st["codes"], st["absmax_q"], st["scale2"], N, K)
+        Y, H = _plain_fwd((X, X), What, A, B, s, case, st["rng"])
+        return (Y, H) + _plain_bwd(st["G"].float(), X, H, What, A, B, s, case, st["rng"])
+    What = _mx_decode(_unpack(st["codes"]), st["scales"], K)
+    if op == "mx_bwd":
+        return _plain_bwd(st["G"].float(), X, st["H"], What, A, B, s, case, st["rng"])
+    Y, H = _plain_fwd((_mx_decode(*_mx_encode(st["X"]), K), X), What, A, B, s, case, st["rng"])
+    return (Y, H) if case["want_H"] else Y
+
+
+# ------------------------------------------------------------------ definitions in 64 bits
+def _exact_mx(x):
+    """Values of MXFP4(x) in fp64, from the definition: a grid per binade, rounded half to even."""
+    rows, cols = x.shape
+    nb = (cols + 31) // 32
+    v = torch.nn.functional.pad(x.double(), (0, 32 * nb - cols)).view(rows, nb, 32)
+    top = v.abs().amax(dim=2, keepdim=True)
+    e = torch.floor(torch.log2(torch.where(top > 0, top, torch.ones_like(top))))
+    unit = torch.exp2((e - 2).clamp(min=-127.0))
+    y = v.abs() / unit
+    step = torch.where(y < 2, 0.5, torch.where(y < 4, 1.0, 2.0)).double()
+    y = torch.minimum(torch.round(y / step) * step, torch.full_like(y, 6.0))
+    return (torch.sign(v) * y * unit).view(rows, 32 * nb)[:, :cols]
+
+
+def _exact_weight_mx(packed, scales, K):
+    c = torch.stack((packed % 16, packed // 16), dim=2).view(packed.shape[0], -1).long()
+    ex, man = (c % 8) // 2, c % 2
+    mag = torch.where(ex == 0, man * 0.5, (1.0 + 0.5 * man) * torch.exp2(ex.double() - 1))
+    v = torch.where(c >= 8, -mag, mag).view(packed.shape[0], -1, 32) * torch.exp2(scales.double() - 127)[:, :, None]
+    return v.view(packed.shape[0], -1)[:, :K]
+
+
+def _exact_keep(n, p, seed, offset, device):
+    """The kept elements as 0.0 / 1.0, the 32 x 32 bit products formed from 16-bit halves."""
+    def mul(a, b):
+        al, ah, bl, bh = a % 65536, a // 65536, b % 65536, b // 65536
+        low = al * bl
+        mid = ah * bl + low // 65536
+        mid2 = al * bh + mid % 65536
+        return ah * bh + mid // 65536 + mid2 // 65536, (mid2 % 65536) * 65536 + low % 65536
+
+    two32 = 1 << 32
+    g = torch.arange(-(-n // GROUP), device=device, dtype=torch.int64)
+    x0, x1 = g % two32, g // two32
+    x2, x3 = torch.zeros_like(g) + offset % two32, torch.zeros_like(g) + offset // two32
+    for i in range(ROUNDS):
+        h0, l0 = mul(x0, M0)
+        h1, l1 = mul(x2, M1)
+        x0, x1, x2, x3 = (h1 ^ x1 ^ ((seed % two32 + i * W0) % two32), l1,
+                          h0 ^ x3 ^ ((seed // two32 + i * W1) % two32), l0)
+    out = torch.empty((g.numel(), GROUP), dtype=torch.float64, device=device)
+    for w, x in enumerate((x0, x1, x2, x3)):
+        out[:, 2 * w] = (x % 65536 >= _threshold(p)).double()
+        out[:, 2 * w + 1] = (x // 65536 >= _threshold(p)).double()
+    return out.view(-1)[:n]
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    op = case["op"]
+    if op == "codec":
+        return _exact_mx(st["x"])
+    p, rng = case["p"], st["rng"]
+    c = 1.0 / (1.0 - _threshold(p) / 65536.0)
+    if op == "dropout":
+        x = st["x"].double()
+        return x * _exact_keep(x.numel(), p, *rng, x.device) * c
+    N, K, r = case["N"], case["K"], case["r"]
+    X = st["X"].double()
+    keep = _exact_keep(X.numel(), p, *rng, X.device).view(X.shape) * c
+    if op == "nf4_step":
+        q = torch.stack((st["codes"] % 16, st["codes"] // 16), dim=1).view(-1).long()
+        lv = torch.tensor(_nf4_levels(), dtype=torch.float64, device=X.device).float()
+        a = st["absmax_q"].float() * st["scale2"].repeat_interleave(256)[:st["absmax_q"].numel()]
+        # the base is defined as bf16(fl32(level * scale))
+        What = (lv[q].view(-1, 64) * a[:, None]).bfloat16().double().view(N, K)
+        base_in = X
+    else:
+        What = _exact_weight_mx(st["codes"], st["scales"], K)
+        base_in = _exact_mx(st["X"])
+    if r:
+        A, B, s = st["A"].double(), st["B"].double(), st["alpha"] / r
+        H = (keep * X) @ A.t()
+    out = ()
+    if op != "mx_bwd":
+        Y = base_in @ What.t()
+        if r:
+            Y = Y + s * (H @ B.t())
+        if op == "mx_fwd":
+            return (Y, H) if case["want_H"] else Y
+        out = (Y, H)
+    else:
+        H = st["H"].double()
+    G = st["G"].double()
+    dH = s * (G @ B)
+    return out + (G @ What + keep * (dH @ A), dH.t() @ (keep * X), s * (G.t() @ H))
