@@ -141,6 +141,15 @@ def _unpack(packed):
     return torch.stack((packed & 15, packed >> 4), dim=2).view(packed.shape[0], -1)
 
 
+def _by_chunk(scale):
+    """Scale bytes [rows, blocks] in the kernels' order: [chunk of 8 blocks][row][8]."""
+    return scale.view(scale.shape[0], -1, 8).permute(1, 0, 2).contiguous()
+
+
+def _by_row(scale):
+    return scale.permute(1, 0, 2).reshape(scale.shape[1], -1)
+
+
 def _threshold(p):
     return min(65535, int(p * 65536 + 0.5))
 
@@ -250,7 +259,8 @@ def prepare(case, seed):
         st["absmax_q"] = (torch.ceil(padded.view(-1, 256) / st["scale2"][:, None] - 0.5).clamp(0, 255)
                           .to(torch.uint8).view(-1)[:nb].contiguous())
     else:
-        code, st["scales"] = _mx_encode(W)
+        code, scale = _mx_encode(W)
+        st["scales"] = _by_chunk(scale)
         st["codes"] = _pack(code)
     del W
     st["X"] = normal((M, K), 1.0)
@@ -315,7 +325,7 @@ def run(st):
         What = _nf4_values(st["codes"], st["absmax_q"], st["scale2"], N, K)
         Y, H = _plain_fwd((X, X), What, A, B, s, case, st["rng"])
         return (Y, H) + _plain_bwd(st["G"].float(), X, H, What, A, B, s, case, st["rng"])
-    What = _mx_decode(_unpack(st["codes"]), st["scales"], K)
+    What = _mx_decode(_unpack(st["codes"]), _by_row(st["scales"]), K)
     if op == "mx_bwd":
         return _plain_bwd(st["G"].float(), X, st["H"], What, A, B, s, case, st["rng"])
     Y, H = _plain_fwd((_mx_decode(*_mx_encode(st["X"]), K), X), What, A, B, s, case, st["rng"])
@@ -340,8 +350,9 @@ def _exact_mx(x):
 def _exact_weight_mx(packed, scales, K):
     c = torch.stack((packed % 16, packed // 16), dim=2).view(packed.shape[0], -1).long()
     ex, man = (c % 8) // 2, c % 2
+    ebits = scales.transpose(0, 1).reshape(packed.shape[0], -1)
     mag = torch.where(ex == 0, man * 0.5, (1.0 + 0.5 * man) * torch.exp2(ex.double() - 1))
-    v = torch.where(c >= 8, -mag, mag).view(packed.shape[0], -1, 32) * torch.exp2(scales.double() - 127)[:, :, None]
+    v = torch.where(c >= 8, -mag, mag).view(packed.shape[0], -1, 32) * torch.exp2(ebits.double() - 127)[:, :, None]
     return v.view(packed.shape[0], -1)[:, :K]
 
 
