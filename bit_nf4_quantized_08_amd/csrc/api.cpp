@@ -100,6 +100,38 @@ int adam_consts(const qn_adamw_config &h, qn::AdamConsts &c) {
   return QN_OK;
 }
 
+// Dropout of a call: thr and the scale from p (drop null: none).
+int drop_args(const qn_dropout_config *d, qn::DropArgs &out) {
+  out = qn::kNoDrop;
+  if (!d) return QN_OK;
+  if (!(d->p >= 0.0f && d->p < 1.0f)) return QN_ERR_VALUE;
+  if (!aligned(d->offset_dev, 8)) return QN_ERR_ALIGN;
+  out.thr = std::min<uint32_t>(65535u, (uint32_t)std::floor((double)d->p * 65536.0 + 0.5));
+  out.c = (float)(65536.0 / (65536.0 - (double)out.thr));
+  out.seed = d->seed;
+  out.offset = d->offset;
+  out.offset_dev = d->offset_dev;
+  return QN_OK;
+}
+
+int check_mx(const qn_mx_matrix *W) {
+  if (!W || !W->codes || !W->scales) return QN_ERR_NULL;
+  if (W->rows <= 0 || W->cols <= 0 || W->cols > kMaxElems || W->rows > INT32_MAX / qn::mx_chunks(W->cols))
+    return QN_ERR_SHAPE;
+  if (!aligned(W->codes, 16) || !aligned(W->scales, 8)) return QN_ERR_ALIGN;
+  return QN_OK;
+}
+
+bool mx_shapes_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
+  if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > QN_MAX_RANK) return false;
+  if (K % 64 != 0 || N % 64 != 0) return false;
+  // Tile rows are addressed with 32-bit byte offsets (256 rows of X, dY, Y or
+  // dX; all of W's codes).
+  if (K > (int64_t)1 << 22 || N > (int64_t)1 << 22) return false;
+  if (N * 128 * qn::mx_chunks(K) > (int64_t)INT32_MAX) return false;
+  return M <= INT32_MAX / 64 && M <= INT32_MAX / qn::mx_chunks(K);
+}
+
 }  // namespace
 
 extern "C" {
@@ -154,6 +186,38 @@ int nf4_dequant(const qn_nf4_weight *W, void *out, int out_dtype, void *stream) 
   if (!aligned(out, 16)) return QN_ERR_ALIGN;
   if (!qn::codec_tables_ok()) return QN_ERR_VALUE;
   return hip_status(qn::launch_dequant(*W, out, out_dtype == QN_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int qn_dropout(const void *x, int dtype, int64_t n, const qn_dropout_config *drop, void *y, void *stream) {
+  if (!x || !y || !drop) return QN_ERR_NULL;
+  if (dtype != QN_F32 && dtype != QN_BF16) return QN_ERR_DTYPE;
+  if (n <= 0 || n > kMaxElems) return QN_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(y, 16)) return QN_ERR_ALIGN;
+  qn::DropArgs d;
+  const int st = drop_args(drop, d);
+  if (st != QN_OK) return st;
+  return hip_status(qn::launch_dropout(x, dtype == QN_BF16, n, d, y, static_cast<hipStream_t>(stream)));
+}
+
+int qn_mxfp4_quantize(const void *X, int x_dtype, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales,
+                      void *stream) {
+  if (!X) return QN_ERR_NULL;
+  const qn_mx_matrix W{codes, scales, rows, cols};
+  const int st = check_mx(&W);
+  if (st != QN_OK) return st;
+  if (x_dtype != QN_F32 && x_dtype != QN_BF16) return QN_ERR_DTYPE;
+  if (!aligned(X, 16)) return QN_ERR_ALIGN;
+  return hip_status(qn::launch_mx_quantize(X, x_dtype == QN_BF16, rows, cols, codes, scales,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int qn_mxfp4_dequant(const qn_mx_matrix *W, void *out, int out_dtype, void *stream) {
+  const int st = check_mx(W);
+  if (st != QN_OK) return st;
+  if (!out) return QN_ERR_NULL;
+  if (out_dtype != QN_F32 && out_dtype != QN_BF16) return QN_ERR_DTYPE;
+  if (!aligned(out, 16)) return QN_ERR_ALIGN;
+  return hip_status(qn::launch_mx_dequant(*W, out, out_dtype == QN_BF16, static_cast<hipStream_t>(stream)));
 }
 
 int qlora_merge(const qn_nf4_weight *W, const void *A, const void *B, int64_t r, float alpha, void *out,
@@ -224,6 +288,7 @@ size_t qlora_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t r) 
   if (M > kMaxElems / K || M > kMaxElems / N) return 0;
   if (op == QN_OP_FWD) return qn::fwd_workspace(M, N, K, r);
   if (op == QN_OP_BWD) return qn::bwd_workspace(M, N, K, r);
+  if (op == QN_OP_FWD_DROPOUT) return qn::fwd_dropout_workspace(M, N, K, r);
   return 0;
 }
 
@@ -252,6 +317,38 @@ int qlora_linear_fwd(const void *X, int64_t M, const qn_nf4_weight *W, const voi
   a.H_out = H_out;
   a.ws = workspace; a.ws_bytes = ws_bytes;
   return hip_status(qn::run_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int qlora_linear_fwd_dropout(const void *X, int64_t M, const qn_nf4_weight *W, const void *A, const void *B,
+                             int64_t r, float alpha, const qn_dropout_config *drop, void *Y, float *H_out,
+                             void *workspace, size_t ws_bytes, void *stream) {
+  int st = check_weight(W);
+  if (st != QN_OK) return st;
+  if (!X || !A || !B || !Y || !drop) return QN_ERR_NULL;
+  st = check_linear_shapes(M, W, r, alpha);
+  if (st != QN_OK) return st;
+  if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(Y, 16)) return QN_ERR_ALIGN;
+  if (H_out && !aligned(H_out, 4)) return QN_ERR_ALIGN;
+  qn::DropArgs d;
+  st = drop_args(drop, d);
+  if (st != QN_OK) return st;
+  const size_t need = qn::fwd_dropout_workspace(M, W->N, W->K, r);
+  if (!workspace || ws_bytes < need) return QN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return QN_ERR_ALIGN;
+  if (!qn::codec_tables_ok()) return QN_ERR_VALUE;
+  qn::FwdArgs a{};
+  a.X = static_cast<const uint16_t *>(X);
+  a.M = M; a.N = W->N; a.K = W->K; a.r = r;
+  a.codes = W->codes;
+  a.sc = qn::ScaleSrc{W->absmax, W->absmax_q, W->scale2, W->quant_type};
+  a.A = static_cast<const uint16_t *>(A);
+  a.B = static_cast<const uint16_t *>(B);
+  a.s = alpha / (float)r;
+  a.Y = static_cast<uint16_t *>(Y);
+  a.H_out = H_out;
+  a.ws = workspace; a.ws_bytes = ws_bytes;
+  a.drop = d;
+  return hip_status(qn::run_fwd_dropout(a, static_cast<hipStream_t>(stream)));
 }
 
 size_t qlora_workspace_size_grouped(int n, const qlora_fwd_problem *problems) {
@@ -330,9 +427,10 @@ int qlora_linear_fwd_noalloc(const void *X, int64_t M, const qn_nf4_weight *W, c
   return hip_status(qn::run_fwd(a, static_cast<hipStream_t>(stream)));
 }
 
-int qlora_linear_bwd(const void *dY, const void *X, const float *H, int64_t M, const qn_nf4_weight *W,
-                     const void *A, const void *B, int64_t r, float alpha, void *dX, void *dA, void *dB,
-                     void *workspace, size_t ws_bytes, void *stream) {
+// qlora_linear_bwd and its dropout form (drop null: none).
+static int linear_bwd(const void *dY, const void *X, const float *H, int64_t M, const qn_nf4_weight *W, const void *A,
+                      const void *B, int64_t r, float alpha, const qn_dropout_config *drop, void *dX, void *dA,
+                      void *dB, void *workspace, size_t ws_bytes, void *stream) {
   int st = check_weight(W);
   if (st != QN_OK) return st;
   if (!dY || !X || !A || !B || !dA || !dB) return QN_ERR_NULL;
@@ -341,6 +439,9 @@ int qlora_linear_bwd(const void *dY, const void *X, const float *H, int64_t M, c
   if (!aligned(dY, 16) || !aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dA, 16) ||
       !aligned(dB, 16) || (dX && !aligned(dX, 16)) || (H && !aligned(H, 4)))
     return QN_ERR_ALIGN;
+  qn::DropArgs d;
+  st = drop_args(drop, d);
+  if (st != QN_OK) return st;
   const size_t need = qn::bwd_workspace(M, W->N, W->K, r);
   if (!workspace || ws_bytes < need) return QN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QN_ERR_ALIGN;
@@ -359,6 +460,93 @@ int qlora_linear_bwd(const void *dY, const void *X, const float *H, int64_t M, c
   a.dA = static_cast<uint16_t *>(dA);
   a.dB = static_cast<uint16_t *>(dB);
   a.ws = workspace; a.ws_bytes = ws_bytes;
+  a.drop = d;
+  return hip_status(qn::run_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int qlora_linear_bwd(const void *dY, const void *X, const float *H, int64_t M, const qn_nf4_weight *W,
+                     const void *A, const void *B, int64_t r, float alpha, void *dX, void *dA, void *dB,
+                     void *workspace, size_t ws_bytes, void *stream) {
+  return linear_bwd(dY, X, H, M, W, A, B, r, alpha, nullptr, dX, dA, dB, workspace, ws_bytes, stream);
+}
+
+int qlora_linear_bwd_dropout(const void *dY, const void *X, const float *H, int64_t M, const qn_nf4_weight *W,
+                             const void *A, const void *B, int64_t r, float alpha, const qn_dropout_config *drop,
+                             void *dX, void *dA, void *dB, void *workspace, size_t ws_bytes, void *stream) {
+  if (!drop) return QN_ERR_NULL;
+  return linear_bwd(dY, X, H, M, W, A, B, r, alpha, drop, dX, dA, dB, workspace, ws_bytes, stream);
+}
+
+size_t qlora_mx_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t r) {
+  if (!mx_shapes_ok(M, N, K, r)) return 0;
+  if (op == QN_OP_FWD) return qn::mx_fwd_workspace(M, N, K, r);
+  if (op == QN_OP_BWD) return std::max<size_t>(256, qn::bwd_workspace(M, N, K, r) + qn::mx_dx_part_bytes(M, N, K));
+  return 0;
+}
+
+int qlora_mx_linear_fwd(const void *X, int64_t M, const qn_mx_matrix *W, const void *A, const void *B, int64_t r,
+                        float alpha, const qn_dropout_config *drop, void *Y, float *H_out, void *workspace,
+                        size_t ws_bytes, void *stream) {
+  int st = check_mx(W);
+  if (st != QN_OK) return st;
+  if (!X || !Y) return QN_ERR_NULL;
+  if (!mx_shapes_ok(M, W->rows, W->cols, r)) return QN_ERR_SHAPE;
+  qn::DropArgs d = qn::kNoDrop;
+  if (r > 0) {
+    if (!A || !B) return QN_ERR_NULL;
+    if (!std::isfinite(alpha)) return QN_ERR_VALUE;
+    st = drop_args(drop, d);
+    if (st != QN_OK) return st;
+  } else if (A || B || H_out) {
+    return QN_ERR_SHAPE;
+  }
+  if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(Y, 16) || !aligned(H_out, 4))
+    return QN_ERR_ALIGN;
+  if (!workspace || ws_bytes < qn::mx_fwd_workspace(M, W->rows, W->cols, r)) return QN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return QN_ERR_ALIGN;
+  const qn::MxFwdArgs a{static_cast<const uint16_t *>(X), M, W->rows, W->cols, r, W->codes, W->scales,
+                        static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B),
+                        r > 0 ? alpha / (float)r : 0.0f, static_cast<uint16_t *>(Y), H_out, workspace, d};
+  return hip_status(qn::run_mx_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int qlora_mx_linear_bwd(const void *dY, const void *X, const float *H, int64_t M, const qn_mx_matrix *W,
+                        const void *A, const void *B, int64_t r, float alpha, const qn_dropout_config *drop, void *dX,
+                        void *dA, void *dB, void *workspace, size_t ws_bytes, void *stream) {
+  int st = check_mx(W);
+  if (st != QN_OK) return st;
+  if (!dY) return QN_ERR_NULL;
+  if (!mx_shapes_ok(M, W->rows, W->cols, r)) return QN_ERR_SHAPE;
+  qn::DropArgs d = qn::kNoDrop;
+  if (r > 0) {
+    if (!X || !A || !B || !dA || !dB) return QN_ERR_NULL;
+    if (!std::isfinite(alpha)) return QN_ERR_VALUE;
+    st = drop_args(drop, d);
+    if (st != QN_OK) return st;
+  } else {
+    if (A || B || H || dA || dB) return QN_ERR_SHAPE;
+    if (!dX) return QN_ERR_NULL;
+  }
+  if (!aligned(dY, 16) || !aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dX, 16) ||
+      !aligned(dA, 16) || !aligned(dB, 16) || !aligned(H, 4))
+    return QN_ERR_ALIGN;
+  if (!workspace || ws_bytes < qlora_mx_workspace_size(QN_OP_BWD, M, W->rows, W->cols, r)) return QN_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return QN_ERR_ALIGN;
+  qn::BwdArgs a{};
+  a.dY = static_cast<const uint16_t *>(dY);
+  a.X = static_cast<const uint16_t *>(X);
+  a.H = H;
+  a.M = M; a.N = W->rows; a.K = W->cols; a.r = r;
+  a.codes = W->codes;
+  a.mx_scales = W->scales;
+  a.A = static_cast<const uint16_t *>(A);
+  a.B = static_cast<const uint16_t *>(B);
+  a.s = r > 0 ? alpha / (float)r : 0.0f;
+  a.dX = static_cast<uint16_t *>(dX);
+  a.dA = static_cast<uint16_t *>(dA);
+  a.dB = static_cast<uint16_t *>(dB);
+  a.ws = workspace; a.ws_bytes = ws_bytes;
+  a.drop = d;
   return hip_status(qn::run_bwd(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -586,6 +586,13 @@ size_t fwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
   return c.off;
 }
 
+size_t fwd_dropout_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
+  Carve c(nullptr);
+  c.take<uint16_t>(M * align_up(r, 8));
+  c.take<char>((int64_t)lowrank_part_bytes(M, K, r));
+  return c.off;
+}
+
 // Arguments of the forward's MFMA path: the low-rank product H = X A^T
 // (written unscaled to H_out, and as bf16(s H) to the workspace) and the tile
 // GEMM that takes bf16(s H) B^T as its extra contraction step.
@@ -597,6 +604,7 @@ static void fwd_mfma_args(const FwdArgs &a, LowRankArgs &la, QGemmArgs &g) {
   la = LowRankArgs{};
   la.L = a.X; la.ldl = a.K; la.M = a.M; la.Kc = a.K;
   la.P = a.A; la.ldp = a.K; la.R = a.r; la.scale = a.s;
+  la.drop = a.drop;
   la.out_f32 = a.H_out; la.out_b = sH; la.ldb = rp; la.out_t = nullptr; la.Mp = a.M; la.part = part;
   g = QGemmArgs{};
   g.L = a.X; g.ldl = a.K; g.M = a.M; g.Nout = a.N; g.Kc = a.K;
@@ -697,6 +705,14 @@ hipError_t run_fwd(const FwdArgs &a, hipStream_t st) {
   return launch_qgemm_fwd(g, st);
 }
 
+hipError_t run_fwd_dropout(const FwdArgs &a, hipStream_t st) {
+  LowRankArgs la;
+  QGemmArgs g;
+  fwd_mfma_args(a, la, g);
+  QN_TRY(launch_lowrank(la, st));
+  return launch_qgemm_fwd(g, st);
+}
+
 hipError_t run_fwd_group(const FwdArgs *a, int n, hipStream_t st) {
   LowRankArgs la[QN_MAX_GROUP];
   QGemmArgs g[4][QN_MAX_GROUP];   // [2 * (4-bit type) + (double-quantised scales?)][problem]
@@ -733,8 +749,10 @@ hipError_t run_fwd_group(const FwdArgs *a, int n, hipStream_t st) {
 
 // ---------------------------------------------------------------- backward
 
+// r = 0 (the MXFP4 linear without an adapter) has dX only.
 size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
   Carve c(nullptr);
+  if (r == 0) return 0;
   const int64_t rp = align_up(r, 32);
   const int64_t Mp = align_up(M, BK);
   c.take<uint16_t>(rp * N);                 // B^T
@@ -749,6 +767,11 @@ size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
 }
 
 hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
+  if (a.r == 0) {
+    MxDxArgs x{a.dY, a.M, a.N, a.K, a.codes, a.mx_scales, nullptr, 0, nullptr, 0, kNoDrop, a.dX,
+               static_cast<float *>(a.ws), 0};
+    return a.dX ? launch_mx_dx(x, st) : hipSuccess;
+  }
   Carve c(a.ws);
   const int64_t rp = align_up(a.r, 32);
   const int64_t Mp = align_up(a.M, BK);
@@ -777,7 +800,7 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     ld.P = Bt; ld.ldp = a.N; ld.R = a.r; ld.scale = a.s;
     ld.out_b = dHb; ld.ldb = rp; ld.out_t = dHt; ld.ldt_rows = rp; ld.Mp = Mp; ld.part = dhpart;
     lh.L = a.X; lh.ldl = a.K; lh.M = a.M; lh.Kc = a.K;
-    lh.P = a.A; lh.ldp = a.K; lh.R = a.r; lh.scale = a.s;
+    lh.P = a.A; lh.ldp = a.K; lh.R = a.r; lh.scale = a.s; lh.drop = a.drop;
     lh.out_t = sHt; lh.ldt_rows = rp; lh.Mp = Mp; lh.part = hpart;
     QN_TRY(launch_lowrank2(ld, a.H ? nullptr : &lh, st));
   }
@@ -788,17 +811,22 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     cb.Lt = sHt; cb.Mp = Mp; cb.Q = a.dY; cb.ldq = a.N; cb.M = a.M; cb.Ncols = a.N; cb.R = a.r;
     cb.part = bpart; cb.out = a.dB; cb.transpose = true;
     ca.Lt = dHt; ca.Mp = Mp; ca.Q = a.X; ca.ldq = a.K; ca.M = a.M; ca.Ncols = a.K; ca.R = a.r;
-    ca.part = apart; ca.out = a.dA; ca.transpose = false;
+    ca.part = apart; ca.out = a.dA; ca.transpose = false; ca.drop = a.drop;
     QN_TRY(launch_colred2(cb, &ca, st, QN_TRACE_GEMM_DB));
   }
   // dX [M, K] = dY [M, N] * W_hat [N, K] + dH [M, r] * A [r, K]
+  if (a.dX && a.mx_scales) {
+    MxDxArgs x{a.dY, a.M, a.N, a.K, a.codes, a.mx_scales, dHb, rp, a.A, a.r, a.drop, a.dX,
+               reinterpret_cast<float *>(c.take<char>((int64_t)mx_dx_part_bytes(a.M, a.N, a.K))), 0};
+    return launch_mx_dx(x, st);
+  }
   if (a.dX) {
     QGemmArgs g{};
     g.L = a.dY; g.ldl = a.N; g.M = a.M; g.Nout = a.K; g.Kc = a.N;
     g.codes = a.codes; g.absmax = a.sc.absmax; g.absmax_q = a.sc.absmax_q; g.scale2 = a.sc.scale2;
     g.qtype = a.sc.qtype;
     g.L2 = dHb; g.ldl2 = rp; g.R2 = a.A; g.ldr2 = a.K; g.r = a.r;
-    g.out = a.dX; g.ldo = a.K;
+    g.out = a.dX; g.ldo = a.K; g.drop = a.drop;
     QN_TRY(launch_qgemm_dx(g, st));
   }
   return hipSuccess;

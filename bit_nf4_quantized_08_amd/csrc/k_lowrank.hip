@@ -24,11 +24,17 @@
 // columns), bf16 scaled and transposed (zero-padded to ldt_rows rows and Mp
 // columns).  One launch carries up to QN_MAX_GROUP independent products
 // (blockIdx.y selects one).
+//
+// Dropout of L (the adapter's input): a 16-byte piece of L is one call of the
+// generator of qn_philox.h, so each lane masks the pieces it loaded, in
+// registers, before they go to LDS; the kept values stay unscaled bf16 and the
+// factor 1/(1-p) is applied to the fp32 sums, so dropout adds no rounding.
 
 #include <algorithm>
 
 #include "qn_device.h"
 #include "qn_internal.h"
+#include "qn_philox.h"
 
 namespace qn {
 namespace {
@@ -61,7 +67,9 @@ struct LowRankGroup {
   LowRankArgs p[QN_MAX_GROUP];
 };
 
-template <int RT>   // 32-column tiles of the factor: R <= 32 * RT
+// RT: 32-column tiles of the factor, R <= 32 * RT.  DROP: some product of the
+// launch drops elements of its L.
+template <int RT, bool DROP>
 __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup grp) {
   __shared__ __attribute__((aligned(16))) uint8_t ps[2][32 * RT * LR_PITCH];
   __shared__ __attribute__((aligned(16))) uint8_t xs[LR_THREADS / 64][32 * 128];   // each wave's L slab
@@ -96,6 +104,16 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
     xrd[i] = (uint32_t)(lr * 128 + 16 * ((4 * lh + i) ^ ((lr >> 1) & 7)));
   }
   uint8_t *xslab = xs[wave];
+  // Generator call of load i of step c: its eight elements' flat index / 8.
+  DropKey dk{};
+  uint64_t dg[4] = {};
+  const bool dropping = DROP && a.drop.thr != 0;
+  if constexpr (DROP) {
+    if (dropping) dk = drop_key(a.drop);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dg[i] = (uint64_t)(m0 + 32 * wave + 8 * i + (lane >> 3)) * (uint64_t)(a.Kc / 8) + (uint64_t)(lane & 7);
+  }
   // P: thread t moves 16-byte unit (t & 7) of rows t / 8 + 32 i, i < RT (rows
   // past R read zeros).
   const rsrc_t rp = make_rsrc(a.P, a.R * a.ldp * 2);
@@ -147,6 +165,17 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
 #pragma unroll
       for (int d = 0; d < LR_DEPTH; ++d) {
         const uint8_t *pb = ps[d & 1];
+        if constexpr (DROP) {
+          if (dropping) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+              philox7(dg[i] + (uint64_t)(c0 + cb + d) * (LR_CK / 8), dk, w);
+              xr[d][i] &= u32x4{keep_mask2(w[0], dk.thr2), keep_mask2(w[1], dk.thr2), keep_mask2(w[2], dk.thr2),
+                                keep_mask2(w[3], dk.thr2)};
+            }
+          }
+        }
         // The wave's slab through its LDS region (its own rows only: LDS
         // operations of one wave complete in order, no barrier needed).
 #pragma unroll
@@ -222,7 +251,7 @@ __global__ __launch_bounds__(256) void lowrank_finish_kernel(LowRankGroup grp) {
 #pragma unroll
     for (int s = 0; s < LR_MAX_SPLITS; ++s)
       if (s < S) v += pv[i][s];
-    tile[r][j] = in[i] ? v : 0.0f;
+    tile[r][j] = in[i] ? v * a.drop.c : 0.0f;   // c = 1 without dropout
   }
   __syncthreads();
   for (int idx = tid; idx < FIN_ROWS * 64; idx += 256) {
@@ -260,18 +289,25 @@ hipError_t launch_lowrank_n(const LowRankArgs *a, int n, hipStream_t st) {
   if (n < 1 || n > QN_MAX_GROUP) return hipErrorInvalidValue;
   LowRankGroup grp{};
   int64_t wgs = 0, fin = 0, R = 0;
+  bool drop = false;
   for (int i = 0; i < n; ++i) {
     grp.p[i] = a[i];
     grp.p[i].splits = lowrank_splits(a[i].M, a[i].Kc);
     wgs = std::max<int64_t>(wgs, (a[i].M + LR_BM - 1) / LR_BM * grp.p[i].splits);
     fin = std::max<int64_t>(fin, (lowrank_rows(a[i]) + FIN_ROWS - 1) / FIN_ROWS);
     R = std::max(R, a[i].R);
+    drop = drop || a[i].drop.thr != 0;
   }
   {
     TraceScope tr(QN_TRACE_LOWRANK, st);
     const dim3 grid((unsigned)wgs, (unsigned)n);
-    if (R <= 32) hipLaunchKernelGGL(lowrank_part_kernel<1>, grid, dim3(LR_THREADS), 0, st, grp);
-    else hipLaunchKernelGGL(lowrank_part_kernel<2>, grid, dim3(LR_THREADS), 0, st, grp);
+    if (drop) {
+      if (R <= 32) hipLaunchKernelGGL((lowrank_part_kernel<1, true>), grid, dim3(LR_THREADS), 0, st, grp);
+      else hipLaunchKernelGGL((lowrank_part_kernel<2, true>), grid, dim3(LR_THREADS), 0, st, grp);
+    } else {
+      if (R <= 32) hipLaunchKernelGGL((lowrank_part_kernel<1, false>), grid, dim3(LR_THREADS), 0, st, grp);
+      else hipLaunchKernelGGL((lowrank_part_kernel<2, false>), grid, dim3(LR_THREADS), 0, st, grp);
+    }
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -305,6 +341,11 @@ hipError_t launch_lowrank(const LowRankArgs &a, hipStream_t st) { return launch_
 // reads).  Per-split partial sums go to `part`; a second kernel adds the
 // splits in order and rounds to bf16.  Like the low-rank product, one launch
 // can carry two independent reductions over the same rows (blockIdx.z).
+//
+// Dropout of Q (dA's X): the four lanes of a quad hold the eight columns of one
+// generator call, two each.  Of four rows, lane j of the quad runs the call of
+// row j, and a 4 x 4 transpose within the quad (DPP) hands every lane its own
+// word of all four rows; the sum is scaled by 1/(1-p) when it is rounded.
 namespace qn {
 namespace {
 
@@ -313,7 +354,22 @@ constexpr int CR_COLS = 128;
 constexpr int CR_RB = 128;        // rows per split
 constexpr int CR_PAIRS = CR_RB / 2;
 
-template <int R>
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_perm(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+// w[i] of lane j of a quad <- w[j] of lane i.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
+  const bool odd = lane & 1, hi = lane & 2;
+  uint32_t x = quad_perm<0xB1>(odd ? w[0] : w[1]), y = quad_perm<0xB1>(odd ? w[2] : w[3]);
+  if (odd) { w[0] = x; w[2] = y; } else { w[1] = x; w[3] = y; }
+  x = quad_perm<0x4E>(hi ? w[0] : w[2]);
+  y = quad_perm<0x4E>(hi ? w[1] : w[3]);
+  if (hi) { w[0] = x; w[1] = y; } else { w[2] = x; w[3] = y; }
+}
+
+template <int R, bool DROP>
 __global__ __launch_bounds__(CR_THREADS) void colred_kernel(ColRedArgs a0, ColRedArgs a1) {
   constexpr int RJ = R < 16 ? R : 16;            // rows of the output reduced per pass
   __shared__ uint32_t lt[CR_PAIRS * R];          // (Lt[j][2p], Lt[j][2p+1]) at [p][j]
@@ -361,6 +417,26 @@ __global__ __launch_bounds__(CR_THREADS) void colred_kernel(ColRedArgs a0, ColRe
     lt[p * R + j] = (j < a.R && mb + 2 * p < a.Mp) ? ltv[i] : 0u;
   }
   __syncthreads();
+
+  if constexpr (DROP) {
+    if (a.drop.thr) {
+      const DropKey dk = drop_key(a.drop);
+      const uint64_t call0 = (uint64_t)(c >> 3), pitch = (uint64_t)(a.ldq / 8);
+#pragma unroll
+      for (int u = 0; u < U; u += 2) {
+        // Row j of the four: row j & 1 of pair wave + 4 (u + j / 2).
+        const int j = lane & 3;
+        const uint64_t row = (uint64_t)mb + (uint64_t)(2 * (wave + 4 * (u + (j >> 1))) + (j & 1));
+        uint32_t w[4];
+        philox7(row * pitch + call0, dk, w);
+        quad_transpose(w, lane);
+        q[u][0] &= keep_mask2(w[0], dk.thr2);
+        q[u][1] &= keep_mask2(w[1], dk.thr2);
+        q[u + 1][0] &= keep_mask2(w[2], dk.thr2);
+        q[u + 1][1] &= keep_mask2(w[3], dk.thr2);
+      }
+    }
+  }
 
   float acc0[R], acc1[R];
 #pragma unroll
@@ -432,7 +508,15 @@ __global__ __launch_bounds__(256) void colred_reduce_kernel(ColRedArgs a0, ColRe
     for (int q = 0; q < BATCH; ++q)
       if (s0 + q < splits) v += x[q];
   }
-  a.out[a.transpose ? col * a.R + j : idx] = f32_to_bf16(v);
+  a.out[a.transpose ? col * a.R + j : idx] = f32_to_bf16(v * a.drop.c);   // c = 1 without dropout
+}
+
+template <bool DROP>
+void launch_colred_rank(const ColRedArgs &a, const ColRedArgs &a1, int64_t R, dim3 grid, hipStream_t st) {
+  if (R <= 8) hipLaunchKernelGGL((colred_kernel<8, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
+  else if (R <= 16) hipLaunchKernelGGL((colred_kernel<16, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
+  else if (R <= 32) hipLaunchKernelGGL((colred_kernel<32, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
+  else hipLaunchKernelGGL((colred_kernel<64, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
 }
 
 }  // namespace
@@ -447,10 +531,8 @@ hipError_t launch_colred2(const ColRedArgs &a, const ColRedArgs *b, hipStream_t 
   const dim3 grid((unsigned)((ncols + CR_COLS - 1) / CR_COLS), (unsigned)splits, b ? 2u : 1u);
   {
     TraceScope tr(trace_kind, st);
-    if (R <= 8) hipLaunchKernelGGL(colred_kernel<8>, grid, dim3(CR_THREADS), 0, st, a, a1);
-    else if (R <= 16) hipLaunchKernelGGL(colred_kernel<16>, grid, dim3(CR_THREADS), 0, st, a, a1);
-    else if (R <= 32) hipLaunchKernelGGL(colred_kernel<32>, grid, dim3(CR_THREADS), 0, st, a, a1);
-    else hipLaunchKernelGGL(colred_kernel<64>, grid, dim3(CR_THREADS), 0, st, a, a1);
+    if (a.drop.thr || a1.drop.thr) launch_colred_rank<true>(a, a1, R, grid, st);
+    else launch_colred_rank<false>(a, a1, R, grid, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

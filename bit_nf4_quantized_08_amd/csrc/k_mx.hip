@@ -1,0 +1,897 @@
+// MXFP4 on gfx950: quantisation, dequantisation and the QLoRA linear's forward
+// over an MXFP4 base.
+//
+// The format (32 elements of E2M1 under one power of two) is what
+// v_mfma_scale_f32_*_f8f6f4 multiplies: lane operands are 32 consecutive
+// elements of one row, 16 bytes, with the block's scale byte beside them, so
+// codes go from memory to the matrix cores without any expansion.  A product
+// of two codes is exact and every sum is fp32.
+//
+// Kernels:
+//   mx_quantize_kernel   fp32 or bf16 rows -> codes and scales (bound by memory)
+//   mx_dequant_kernel    codes and scales -> fp32 or bf16 (bound by memory)
+//   mx_gemm_kernel       tiles of mx(X) W^T with the adapter term (bound by the
+//                        matrix cores and the clock they sustain), optionally
+//                        over a part of K with fp32 partial sums
+//   mx_decode_kernel     M <= 16: streams the weights (bound by memory); its
+//                        last workgroups form the adapter's H partials
+//   mx_finish_kernel     adds partial sums and the adapter term
+
+#include <algorithm>
+
+#include "qn_philox.h"
+#include "qn_tile.h"
+
+namespace qn {
+namespace {
+
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+#define QN_TRY(x)                      \
+  do {                                 \
+    hipError_t e_ = (x);               \
+    if (e_ != hipSuccess) return e_;   \
+  } while (0)
+
+// n / d for n < 2^31 by one multiply: q = (mulhi(n, m) + n) >> s.
+struct FastDiv {
+  uint32_t m, s, d;
+};
+FastDiv fast_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return FastDiv{(uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s, d};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, FastDiv f) { return (__umulhi(n, f.m) + n) >> f.s; }
+
+// ------------------------------------------------------------------ codec
+// Unit u of a matrix: 8 consecutive columns of one row, 32 units per 256-column
+// chunk, chunks of a row together.  A lane owns one unit, a quad of lanes one
+// block: the block's largest magnitude is an integer maximum of the absolute
+// bit patterns (two DPP steps), whose exponent field gives the scale byte
+// directly; the hardware conversion rounds x 2^-e to E2M1 (nearest even,
+// saturating), the same rule bit for bit, subnormal inputs included.  Each
+// thread takes kUnits units a workgroup apart, loads first.
+constexpr int kThreads = 256;
+constexpr int kUnits = 4;
+
+// dword t of v (a vector of four dwords per register quad).
+template <int N>
+__device__ __forceinline__ uint32_t dw(const u32x4 (&v)[N], int t) {
+  const uint32_t w[4] = {v[t >> 2].x, v[t >> 2].y, v[t >> 2].z, v[t >> 2].w};
+  return w[t & 3];
+}
+
+// Largest absolute bit pattern of a unit: bf16 pairs packed (result in 16 bits)
+// or fp32.
+template <bool BF16>
+__device__ __forceinline__ uint32_t unit_amax(const u32x4 (&x)[BF16 ? 1 : 2]) {
+  if constexpr (BF16) {
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, dw(x, t) & 0x7FFF7FFFu));
+    return m.x > m.y ? m.x : m.y;
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) m = max(m, dw(x, t) & 0x7FFFFFFFu);
+    return m;
+  }
+}
+
+// Scale byte of a block from its largest absolute bit pattern: the exponent
+// field less 2, at least 0; 255 for a block that is not finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  const uint32_t e = amax >> (BF16 ? 7 : 23);
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// The unit's eight codes (one dword) under a scale byte.
+template <bool BF16>
+__device__ __forceinline__ uint32_t unit_codes(const u32x4 (&x)[BF16 ? 1 : 2], uint32_t byte) {
+  const float sc = as_f32(byte << 23);   // the conversion reads the exponent field; 0 stands for 2^-127
+  uint32_t c = 0;
+  if constexpr (BF16) {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 0)), sc, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 1)), sc, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 2)), sc, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 3)), sc, 3);
+  } else {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 0)), as_f32(dw(x, 1)), sc, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 2)), as_f32(dw(x, 3)), sc, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 4)), as_f32(dw(x, 5)), sc, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 6)), as_f32(dw(x, 7)), sc, 3);
+  }
+  return byte == 255u ? 0u : c;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+// VEC: cols is a multiple of 8, so that a unit is aligned and whole.
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint8_t *__restrict__ x, uint32_t rows,
+                                                               int64_t cols, FastDiv cd, uint32_t chunks,
+                                                               uint8_t *__restrict__ codes,
+                                                               uint8_t *__restrict__ scales) {
+  constexpr int V = BF16 ? 1 : 2, ES = BF16 ? 2 : 4;
+  const int tid = threadIdx.x;
+  u32x4 v[kUnits][V];
+  uint32_t ch[kUnits], row[kUnits];
+  const uint32_t c0 = blockIdx.x * (kThreads / 32 * kUnits) + (tid >> 5);
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t c = c0 + i * (kThreads / 32);
+    row[i] = div_by(c, cd);
+    ch[i] = c - row[i] * cd.d;
+    const int64_t col = (int64_t)ch[i] * 256 + 8 * (tid & 31);
+    const uint8_t *p = x + ((int64_t)row[i] * cols + col) * ES;
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[i][q] = u32x4{0, 0, 0, 0};
+    if (c < chunks) {
+      if constexpr (VEC) {
+        if (col < cols)
+#pragma unroll
+          for (int q = 0; q < V; ++q) v[i][q] = reinterpret_cast<const u32x4 *>(p)[q];
+      } else {
+        uint32_t e[4 * V] = {};
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (col + t >= cols) break;
+          if constexpr (BF16) e[t >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[t] << (16 * (t & 1));
+          else e[t] = reinterpret_cast<const uint32_t *>(p)[t];
+        }
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[i][q] = u32x4{e[4 * q], e[4 * q + 1], e[4 * q + 2], e[4 * q + 3]};
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    uint32_t m = unit_amax<BF16>(v[i]);
+    m = max(m, dpp<0xB1>(m));
+    m = max(m, dpp<0x4E>(m));
+    const uint32_t b = scale_byte<BF16>(m);
+    const uint32_t c = c0 + i * (kThreads / 32);
+    if (c < chunks) {
+      reinterpret_cast<uint32_t *>(codes)[(int64_t)c * 32 + (tid & 31)] = unit_codes<BF16>(v[i], b);
+      if ((tid & 3) == 0) scales[((int64_t)ch[i] * rows + row[i]) * 8 + ((tid & 31) >> 2)] = (uint8_t)b;
+    }
+  }
+}
+
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(kThreads) void mx_dequant_kernel(const uint8_t *__restrict__ codes,
+                                                              const uint8_t *__restrict__ scales, uint32_t rows,
+                                                              int64_t cols, FastDiv cd, uint32_t chunks,
+                                                              uint8_t *__restrict__ out) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const int tid = threadIdx.x;
+  uint32_t cw[kUnits], sb[kUnits], ch[kUnits], row[kUnits];
+  const uint32_t c0 = blockIdx.x * (kThreads / 32 * kUnits) + (tid >> 5);
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t c = c0 + i * (kThreads / 32);
+    row[i] = div_by(c, cd);
+    ch[i] = c - row[i] * cd.d;
+    cw[i] = sb[i] = 0;
+    if (c < chunks) {
+      cw[i] = reinterpret_cast<const uint32_t *>(codes)[(int64_t)c * 32 + (tid & 31)];
+      sb[i] = scales[((int64_t)ch[i] * rows + row[i]) * 8 + ((tid & 31) >> 2)];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t c = c0 + i * (kThreads / 32);
+    const int64_t col = (int64_t)ch[i] * 256 + 8 * (tid & 31);
+    if (c >= chunks || col >= cols) continue;
+    const float sc = as_f32(sb[i] << 23);
+    uint8_t *p = out + ((int64_t)row[i] * cols + col) * ES;
+    uint32_t o[BF16 ? 4 : 8];
+    if constexpr (BF16) {
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[i], sc, 0));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[i], sc, 1));
+      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[i], sc, 2));
+      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[i], sc, 3));
+      if (sb[i] == 255u) o[0] = o[1] = o[2] = o[3] = 0x7FC07FC0u;
+    } else {
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], sc, 0);
+      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], sc, 1);
+      const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], sc, 2);
+      const f32x2 f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], sc, 3);
+      const float w[8] = {a.x, a.y, b.x, b.y, e.x, e.y, f.x, f.y};
+#pragma unroll
+      for (int t = 0; t < 8; ++t) o[t] = sb[i] == 255u ? 0x7FC00000u : as_u32(w[t]);
+    }
+    if constexpr (VEC) {
+      reinterpret_cast<u32x4 *>(p)[0] = u32x4{o[0], o[1], o[2], o[3]};
+      if constexpr (!BF16) reinterpret_cast<u32x4 *>(p)[1] = u32x4{o[4], o[5], o[6], o[7]};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        if (col + t >= cols) break;
+        if constexpr (BF16) reinterpret_cast<uint16_t *>(p)[t] = (uint16_t)(o[t >> 1] >> (16 * (t & 1)));
+        else reinterpret_cast<uint32_t *>(p)[t] = o[t];
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ tiles
+// out[M, N] = X^ W^T over steps of one 256-column chunk (128 bytes of codes per
+// row).  A workgroup of WR x WC waves computes a 32 TM WR x 32 TN WC tile; a
+// wave multiplies TM x TN tiles of 32 x 32 with v_mfma_scale_f32_32x32x64: in
+// sub-step j (0..3) lane half h of a row supplies block 4h + j of the chunk for
+// both operands, so that one dword per row half (blocks 4h .. 4h + 3) holds
+// the scale bytes of all four sub-steps, picked by the instruction's byte
+// select.
+// Codes reach LDS by direct loads, one step ahead in the other of two stages,
+// 16-byte piece k of row r at slot k ^ ((r >> 1) & 7): a fragment read takes
+// one piece of 16 consecutive rows, which then fall on 16 distinct groups of
+// four banks (rows are 128 bytes apart, two rows to a turn of the 64 banks).
+// Scales go straight to registers, one step ahead: 32 rows of a chunk are 256
+// contiguous bytes.
+// The adapter term bf16(s H) B^T (r <= 64) follows as bf16 MFMAs into the same
+// accumulators, its fragments read from global memory (H is small, B is read
+// once per tile column).
+struct MxGemmArgs {
+  const uint8_t *xc, *xs;    // X^: codes [M, 128 C], scales [C][M][8]
+  const uint8_t *wc, *ws;    // W: [N, 128 C], [C][N][8]
+  int64_t M, N, C;
+  const uint16_t *sH;        // bf16 [M, 64], zero beyond r, or null
+  const uint16_t *B;         // bf16 [N, r]
+  int64_t r;
+  uint16_t *out;             // bf16 [M, N] (splits == 1)
+  float *part;               // fp32 [splits][M][N]
+  int tiles_m, tiles_n, group_m, splits;
+};
+
+template <int TM, int TN, int WR, int WC, bool PART>
+__global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void mx_gemm_kernel(MxGemmArgs a) {
+  constexpr int NW = WR * WC, BM = 32 * TM * WR, BN = 32 * TN * WC;
+  constexpr int XL = BM / 8 / NW, WL = BN / 8 / NW;   // direct loads (8 rows each) per wave and step
+  static_assert(XL * 8 * NW == BM && WL * 8 * NW == BN, "stage loads");
+  constexpr int kPitch = 32 * TN + 8;                 // bf16 per row of a store block
+  __shared__ __attribute__((aligned(16))) uint8_t xs0[BM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t xs1[BM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t ws0[BN * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t ws1[BN * 128];
+  static_assert(NW * 32 * kPitch * 2 <= 2 * BM * 128 + 2 * BN * 128, "store blocks fit the stages");
+
+  int tm, tn;
+  xcd_tile((int)blockIdx.x, a.tiles_m, a.tiles_n, a.group_m, tm, tn);
+  const int split = (int)blockIdx.y;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave % WR, wc = wave / WR;
+  const int C = (int)a.C, s0 = C * split / a.splits, s1 = C * (split + 1) / a.splits;
+  const int64_t pitch = 128 * a.C;
+
+  const rsrc_t rx = make_rsrc_u(a.xc + m0 * pitch, (a.M - m0) * pitch);
+  const rsrc_t rw = make_rsrc_u(a.wc + n0 * pitch, (a.N - n0) * pitch);
+  // Direct load g covers rows 8g .. 8g + 7: lane l fills slot l & 7 of row
+  // 8g + l / 8 with piece (l & 7) ^ ((row >> 1) & 7) of that row.
+  auto load_off = [&](int g) {
+    const int row = 8 * g + (lane >> 3);
+    return (uint32_t)(row * pitch + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  };
+  uint32_t xo[XL], wo[WL];
+#pragma unroll
+  for (int i = 0; i < XL; ++i) xo[i] = load_off(wave * XL + i);
+#pragma unroll
+  for (int i = 0; i < WL; ++i) wo[i] = load_off(wave * WL + i);
+  auto issue = [&](uint8_t *xd, uint8_t *wd, int s) {
+    const uint32_t xb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(xd)) + wave * XL * 1024;
+    const uint32_t wb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(wd)) + wave * WL * 1024;
+#pragma unroll
+    for (int i = 0; i < XL; ++i) load_lds16(rx, xb + i * 1024, xo[i], s * 128);
+#pragma unroll
+    for (int i = 0; i < WL; ++i) load_lds16(rw, wb + i * 1024, wo[i], s * 128);
+  };
+  // Scale dwords of step s: rows lr of each 32-row tile, blocks 4 lh .. +3.
+  struct Scales {
+    uint32_t a[TM], b[TN];
+  };
+  const int64_t xrow = m0 + wr * 32 * TM, wrow = n0 + wc * 32 * TN;
+  auto load_scales = [&](Scales &t, int s) {
+    const rsrc_t ra = make_rsrc_u(a.xs + ((int64_t)s * a.M + xrow) * 8, (a.M - xrow) * 8);
+    const rsrc_t rb = make_rsrc_u(a.ws + ((int64_t)s * a.N + wrow) * 8, (a.N - wrow) * 8);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) t.a[i] = __builtin_amdgcn_raw_buffer_load_b32(ra, (uint32_t)((32 * i + lr) * 8 + 4 * lh), 0, 0);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) t.b[i] = __builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)((32 * i + lr) * 8 + 4 * lh), 0, 0);
+  };
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  uint32_t fo[4];   // LDS offset of sub-step j's piece in row lr of a tile
+#pragma unroll
+  for (int j = 0; j < 4; ++j) fo[j] = (uint32_t)(lr * 128 + 16 * ((4 * lh + j) ^ ((lr >> 1) & 7)));
+  auto frag = [&](const uint8_t *p) {
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
+    return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+  };
+  auto multiply = [&](const uint8_t *xc, const uint8_t *wc_, const Scales &t) {
+    const uint8_t *xp = xc + wr * 32 * TM * 128, *wp = wc_ + wc * 32 * TN * 128;
+    auto sub = [&](auto J) {
+      constexpr int j = decltype(J)::value;
+      i32x8 fa[TM], fb[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) fa[i] = frag(xp + i * 32 * 128 + fo[j]);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) fb[i] = frag(wp + i * 32 * 128 + fo[j]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int k = 0; k < TN; ++k)
+          acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[k], acc[i][k], 4, 4, j, (int)t.a[i], j,
+                                                                      (int)t.b[k]);
+    };
+    sub(std::integral_constant<int, 0>{});
+    sub(std::integral_constant<int, 1>{});
+    sub(std::integral_constant<int, 2>{});
+    sub(std::integral_constant<int, 3>{});
+  };
+
+  Scales t0, t1;
+  issue(xs0, ws0, s0);
+  load_scales(t0, s0);
+  stage_barrier();
+  // Stage (s - s0) & 1 holds step s; the other is filled meanwhile (it was last
+  // read before the previous barrier).  Past the end the last step is reloaded.
+  for (int s = s0; s < s1; s += 2) {
+    issue(xs1, ws1, min(s + 1, s1 - 1));
+    load_scales(t1, min(s + 1, s1 - 1));
+    multiply(xs0, ws0, t0);
+    stage_barrier();
+    if (s + 1 >= s1) break;
+    issue(xs0, ws0, min(s + 2, s1 - 1));
+    load_scales(t0, min(s + 2, s1 - 1));
+    multiply(xs1, ws1, t1);
+    stage_barrier();
+  }
+
+  if constexpr (PART) {
+    float *part = a.part + (int64_t)split * a.M * a.N;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int64_t n = wrow + 32 * j + lr;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t m = xrow + 32 * i + 8 * (e >> 2) + 4 * lh + (e & 3);
+          if (m < a.M && n < a.N) part[m * a.N + n] = acc[i][j][e];
+        }
+      }
+    return;
+  }
+
+  if (a.sH) {
+    // Sub-step c: lane half h supplies ranks 16 c + 8 h .. + 7 of its row.
+    const rsrc_t rh = make_rsrc_u(a.sH + xrow * 64, (a.M - xrow) * 128);
+    const rsrc_t rb = make_rsrc_u(a.B + wrow * a.r, (a.N - wrow) * a.r * 2);
+    const int steps = (int)(a.r + 15) / 16;
+    const bool vec = (a.r & 7) == 0;
+    for (int c = 0; c < steps; ++c) {
+      u32x4 ha[TM], hb[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        ha[i] = __builtin_amdgcn_raw_buffer_load_b128(rh, (uint32_t)((32 * i + lr) * 128 + 32 * c + 16 * lh), 0, 0);
+      const int j0 = 16 * c + 8 * lh;
+      if (vec) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+          hb[i] = __builtin_amdgcn_raw_buffer_load_b128(
+              rb, j0 < a.r ? (uint32_t)(((32 * i + lr) * a.r + j0) * 2) : kOutOfRange, 0, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t o = (uint32_t)(((32 * i + lr) * a.r + j0 + 2 * q) * 2);
+            const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(rb, j0 + 2 * q < a.r ? o : kOutOfRange, 0, 0);
+            const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(rb, j0 + 2 * q + 1 < a.r ? o + 2 : kOutOfRange, 0, 0);
+            w[q] = (lo & 0xFFFFu) | hi << 16;
+          }
+          hb[i] = u32x4{w[0], w[1], w[2], w[3]};
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int k = 0; k < TN; ++k)
+          acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, ha[i]),
+                                                              __builtin_bit_cast(bf16x8, hb[k]), acc[i][k], 0, 0, 0);
+    }
+  }
+
+  // Store through LDS (the stages are no longer read): each wave turns its
+  // 32 x 32 TN blocks into whole 16-byte pieces of rows.  Rows at or beyond M
+  // fall outside the buffer; N is a multiple of 64, so pieces are whole.
+  constexpr int kBlock = 32 * kPitch;   // bf16
+  constexpr int kPerStage = BM * 64 / kBlock;
+  static_assert(kPerStage >= 1, "a store block fits a stage");
+  uint16_t *blk;
+  {
+    // Blocks are laid over xs0, xs1, ws0, ws1 in turn.
+    constexpr int wper = BN * 64 / kBlock;
+    uint8_t *p = wave < kPerStage ? xs0 + wave * kBlock * 2
+                 : wave < 2 * kPerStage ? xs1 + (wave - kPerStage) * kBlock * 2
+                 : wave < 2 * kPerStage + wper ? ws0 + (wave - 2 * kPerStage) * kBlock * 2
+                                               : ws1 + (wave - 2 * kPerStage - wper) * kBlock * 2;
+    static_assert(2 * kPerStage + 2 * wper >= NW, "store blocks");
+    blk = reinterpret_cast<uint16_t *>(p);
+  }
+  const rsrc_t rout = make_rsrc_u(a.out + m0 * a.N, (a.M - m0) * a.N * 2);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        blk[(8 * (e >> 2) + 4 * lh + (e & 3)) * kPitch + j * 32 + lr] = f32_to_bf16(acc[i][j][e]);
+    constexpr int kPieces = 4 * TN, kRows = 64 / kPieces;   // pieces per row, rows per store
+#pragma unroll
+    for (int q = 0; q < 32 / kRows; ++q) {
+      const int row = kRows * q + lane / kPieces, c8 = 8 * (lane % kPieces);
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(&blk[row * kPitch + c8]);
+      const int64_t lrow = wr * 32 * TM + 32 * i + row, n = wrow + c8;
+      __builtin_amdgcn_raw_buffer_store_b128(v, rout, n < a.N ? (uint32_t)((lrow * a.N + n) * 2) : kOutOfRange, 0, 0);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ few rows
+// M <= 16.  A wave owns 16 weight rows x 1024 columns: eight sub-steps of
+// v_mfma_scale_f32_16x16x128 with the weights as the first operand (lane: row
+// lane % 16, block lane / 16 of the sub-step's four, 64 contiguous bytes of a
+// row per load) and the 16 rows of X^ as the second.  All eight loads of a
+// group of rows are in flight before the first is used, the next group's
+// before this group is multiplied.  X^ is quantised by the wave itself, in
+// LDS, block by block (a lane per block: the rows that exist, not sixteen),
+// while its first weight loads are on their way.
+// A workgroup's 8 waves cover nk (a power of two) column segments of 8 / nk
+// row groups; partial sums meet in LDS, so that K up to 8192 leaves one sum.
+constexpr int DW = 8;                 // waves
+constexpr int DSEG = 1024;            // columns per wave
+constexpr int DSUB = DSEG / 128;      // sub-steps
+constexpr int HSEG = 256;             // columns per wave of the H partials
+
+struct MxDecodeArgs {
+  const uint16_t *X;
+  int64_t M, N, K, C;
+  const uint8_t *wc, *ws;
+  const uint16_t *A;
+  int64_t r;
+  DropArgs drop;
+  float *y_part;       // [ksplits][M][N]
+  float *h_part;       // [hsplits][M][64]
+  uint16_t *out;       // written instead of y_part when non-null (no adapter, one split)
+  int nk, ksplits, row_blocks, hsplits, groups;   // groups: 16-row groups per wave
+};
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+
+// H partials: workgroup b of them takes 16 ranks of A and 8 x HSEG columns.
+__device__ void decode_h(const MxDecodeArgs &a, int b, float (*red)[256]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, kb = lane >> 4;
+  const int jt = b / a.hsplits, hs = b % a.hsplits, j = 16 * jt + l16;
+  const int64_t k0 = (int64_t)hs * (DW * HSEG) + wave * HSEG + 8 * kb;
+  const rsrc_t ra = make_rsrc_u(a.A, a.r * a.K * 2), rx = make_rsrc_u(a.X, a.M * a.K * 2);
+  u32x4 av[HSEG / 32], xv[HSEG / 32];
+#pragma unroll
+  for (int i = 0; i < HSEG / 32; ++i) {
+    const int64_t k = k0 + 32 * i;
+    av[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, j < a.r && k < a.K ? (uint32_t)((j * a.K + k) * 2) : kOutOfRange, 0, 0);
+    xv[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, l16 < a.M && k < a.K ? (uint32_t)((l16 * a.K + k) * 2) : kOutOfRange, 0, 0);
+  }
+  if (a.drop.thr) {
+    const DropKey dk = drop_key(a.drop);
+#pragma unroll
+    for (int i = 0; i < HSEG / 32; ++i) {
+      uint32_t w[4];
+      philox7((uint64_t)l16 * (uint64_t)(a.K / 8) + (uint64_t)((k0 + 32 * i) >> 3), dk, w);
+      xv[i] &= u32x4{keep_mask2(w[0], dk.thr2), keep_mask2(w[1], dk.thr2), keep_mask2(w[2], dk.thr2),
+                     keep_mask2(w[3], dk.thr2)};
+    }
+  }
+  f32x4 acc = zero4();
+#pragma unroll
+  for (int i = 0; i < HSEG / 32; ++i)
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[i]), __builtin_bit_cast(bf16x8, xv[i]),
+                                                  acc, 0, 0, 0);
+  // acc[e]: rank 16 jt + 4 kb + e, row l16.
+#pragma unroll
+  for (int e = 0; e < 4; ++e) red[wave][l16 * 16 + 4 * kb + e] = acc[e];
+  __syncthreads();
+  if (tid < 256) {
+    const int m = tid >> 4, jj = tid & 15;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < DW; ++w) v += red[w][tid];
+    if (m < a.M) a.h_part[((int64_t)hs * a.M + m) * 64 + 16 * jt + jj] = v;
+  }
+}
+
+template <int G>   // row groups per wave
+__global__ __launch_bounds__(64 * DW) void mx_decode_kernel(MxDecodeArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t xq[DW][16 * DSEG / 2];   // a wave's X^: piece (m, block) of 16 bytes
+  __shared__ __attribute__((aligned(16))) uint8_t xe[DW][16 * 32];         // its scale bytes, [m][block % 4][block / 4]
+  // The partial sums [DW][G * 256] take the place of the wave's own X^, which
+  // is in registers by then.
+  static_assert(G * 1024 <= 16 * DSEG / 2, "partial sums fit");
+  auto red = [&](int w) { return reinterpret_cast<float *>(xq[w]); };
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, kb = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int hb = (int)blockIdx.x - a.row_blocks * a.ksplits;
+  if (hb >= 0) {
+    decode_h(a, hb, reinterpret_cast<float (*)[256]>(&xq[0][0]));
+    return;
+  }
+  const int rb = (int)blockIdx.x % a.row_blocks, ks = (int)blockIdx.x / a.row_blocks;
+  const int seg = wave & (a.nk - 1), rg = wave / a.nk, ng = DW / a.nk;
+  const int64_t k0 = ((int64_t)ks * a.nk + seg) * DSEG;
+  const int64_t pitch = 128 * a.C;
+  const int64_t n0 = ((int64_t)rb * ng + rg) * (16 * G);     // first row of the wave
+  const int subs = (int)min((int64_t)DSUB, max((int64_t)0, (256 * a.C - k0) / 128));   // sub-steps that exist (even)
+
+  // Weights: row n0 + 16 g + l16, piece 4 i + kb of the segment.
+  const rsrc_t rw = make_rsrc_u(a.wc + n0 * pitch + k0 / 2, (a.N - n0) * pitch - k0 / 2);
+  uint32_t wv[2][DSUB][4];
+  u32x2 wsv[2][DSUB / 2];
+  auto load_w = [&](int buf, int g) {
+    const bool in = n0 + 16 * g + l16 < a.N;
+#pragma unroll
+    for (int i = 0; i < DSUB; ++i) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
+          rw, in && i < subs ? (uint32_t)((16 * g + l16) * pitch + 64 * i + 16 * kb) : kOutOfRange, 0, 0);
+      wv[buf][i][0] = v.x; wv[buf][i][1] = v.y; wv[buf][i][2] = v.z; wv[buf][i][3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < DSUB / 2; ++i) {
+      const int64_t c = k0 / 256 + i;
+      const rsrc_t rs = make_rsrc_u(a.ws + (c < a.C ? c * a.N * 8 : 0), c < a.C ? a.N * 8 : 0);
+      wsv[buf][i] = __builtin_amdgcn_raw_buffer_load_b64(rs, in ? (uint32_t)((n0 + 16 * g + l16) * 8) : kOutOfRange, 0, 0);
+    }
+  };
+  load_w(0, 0);
+
+  // X^ of the wave's segment: lane t takes block t & 31 of rows t >> 5, + 2, ...
+  {
+    const int b = lane & 31;
+    const int64_t k = k0 + 32 * b;
+    for (int m = lane >> 5; m < (int)a.M; m += 2) {
+      u32x4 v[4];
+      const rsrc_t rx = make_rsrc_u(a.X, a.M * a.K * 2);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = __builtin_amdgcn_raw_buffer_load_b128(rx, k < a.K ? (uint32_t)((m * a.K + k + 8 * q) * 2) : kOutOfRange, 0, 0);
+      uint32_t am = 0;
+      uint32_t c[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const u32x4 u[1] = {v[q]};
+        am = max(am, unit_amax<true>(u));
+      }
+      const uint32_t byte = scale_byte<true>(am);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const u32x4 u[1] = {v[q]};
+        c[q] = unit_codes<true>(u, byte);
+      }
+      *reinterpret_cast<u32x4 *>(&xq[wave][(m * 32 + b) * 16]) = u32x4{c[0], c[1], c[2], c[3]};
+      xe[wave][m * 32 + (b & 3) * 8 + (b >> 2)] = (uint8_t)byte;
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  // Fragments: row l16 (rows at or beyond M hold whatever LDS held: their
+  // products land in columns of the result that are never stored).
+  i32x8 xf[DSUB];
+#pragma unroll
+  for (int i = 0; i < DSUB; ++i) {
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(&xq[wave][(l16 * 32 + 4 * i + kb) * 16]);
+    xf[i] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+  }
+  const u32x2 xsc = *reinterpret_cast<const u32x2 *>(&xe[wave][l16 * 32 + kb * 8]);
+
+  f32x4 acc[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    if (g + 1 < G) load_w((g + 1) & 1, g + 1);
+    acc[g] = zero4();
+    auto sub = [&](auto I) {
+      constexpr int i = decltype(I)::value;
+      const uint32_t(&w)[4] = wv[g & 1][i];
+      const i32x8 wf = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+      const uint32_t sw = ((i & 1) ? wsv[g & 1][i >> 1].y : wsv[g & 1][i >> 1].x) >> (8 * kb);
+      const uint32_t sx = (i < 4) ? xsc.x : xsc.y;
+      // Sub-steps past the segment's end hold zero codes under scale byte 0,
+      // and X^ there was quantised from zeros.
+      acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[g], 4, 4, 0, (int)sw, i & 3, (int)sx);
+    };
+    sub(std::integral_constant<int, 0>{}); sub(std::integral_constant<int, 1>{});
+    sub(std::integral_constant<int, 2>{}); sub(std::integral_constant<int, 3>{});
+    sub(std::integral_constant<int, 4>{}); sub(std::integral_constant<int, 5>{});
+    sub(std::integral_constant<int, 6>{}); sub(std::integral_constant<int, 7>{});
+  }
+  // acc[g][e]: weight row 16 g + 4 kb + e, row l16 of X.
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red(wave)[g * 256 + l16 * 16 + 4 * kb + e] = acc[g][e];
+  __syncthreads();
+  // Element idx of a row group set: (group set q, g, m, row in 16).
+  for (int idx = tid; idx < ng * G * 256; idx += 64 * DW) {
+    const int q = idx / (G * 256), in = idx % (G * 256);
+    float v = 0.0f;
+    for (int w = 0; w < a.nk; ++w) v += red(q * a.nk + w)[in];
+    const int64_t n = ((int64_t)rb * ng + q) * (16 * G) + 16 * (in >> 8) + (in & 15);
+    const int m = (in >> 4) & 15;
+    if (m < a.M && n < a.N) {
+      if (a.out) a.out[m * a.N + n] = f32_to_bf16(v);
+      else a.y_part[((int64_t)ks * a.M + m) * a.N + n] = v;
+    }
+  }
+}
+
+// Y = sum of the partial products + s H B^T, H = c * (sum of its partials);
+// also writes H.  A workgroup owns 64 columns and 16 rows; thread t column
+// t & 63, rows (t >> 6) + 4 i.  H stays in fp32.
+struct MxFinishArgs {
+  const float *part;   // [splits][M][N]
+  int splits;
+  const float *hp;     // [hsplits][M][ldh] unscaled, or null
+  int hsplits, ldh;
+  int64_t M, N, r;
+  const uint16_t *B;
+  float s, c;
+  uint16_t *out;
+  float *H_out;
+};
+
+__global__ __launch_bounds__(256) void mx_finish_kernel(MxFinishArgs a) {
+  __shared__ float h[16][65];
+  __shared__ float bt[64][65];
+  const int tid = threadIdx.x;
+  const int64_t m0 = (int64_t)blockIdx.y * 16, n = (int64_t)blockIdx.x * 64 + (tid & 63);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = 0.0f;
+  for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + (tid >> 6) + 4 * i;
+      if (m < a.M) v[i] += a.part[((int64_t)s * a.M + m) * a.N + n];
+    }
+  if (a.hp) {
+    for (int i = tid; i < 16 * 64; i += 256) {
+      const int64_t m = m0 + (i >> 6);
+      const int j = i & 63;
+      float x = 0.0f;
+      if (m < a.M && j < a.r)
+        for (int s = 0; s < a.hsplits; ++s) x += a.hp[((int64_t)s * a.M + m) * a.ldh + j];
+      x *= a.c;
+      h[i >> 6][j] = x;
+      if (a.H_out && blockIdx.x == 0 && m < a.M && j < a.r) a.H_out[m * a.r + j] = x;
+    }
+    const int r = (int)a.r;
+    for (int i = tid; i < 64 * r; i += 256) bt[i / r][i % r] = bf16_to_f32(a.B[(int64_t)blockIdx.x * 64 * r + i]);
+    __syncthreads();
+    for (int j = 0; j < r; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += (a.s * h[(tid >> 6) + 4 * i][j]) * bt[tid & 63][j];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = m0 + (tid >> 6) + 4 * i;
+    if (m < a.M) a.out[m * a.N + n] = f32_to_bf16(v[i]);
+  }
+}
+
+// ------------------------------------------------------------------ plans
+struct Carve {
+  char *base;
+  size_t off = 0;
+  explicit Carve(void *p) : base(static_cast<char *>(p)) {}
+  template <typename T>
+  T *take(int64_t count) {
+    T *p = reinterpret_cast<T *>(base ? base + off : nullptr);
+    off += (size_t)align_up(count * (int64_t)sizeof(T), 256);
+    return p;
+  }
+};
+
+constexpr int64_t kDecodeRows = 16;
+
+struct DecodePlan {
+  int nk, ksplits, row_blocks, hsplits, hblocks, groups;
+};
+DecodePlan decode_plan(int64_t N, int64_t K, int64_t r) {
+  DecodePlan p;
+  const int64_t segs = cdiv(K, DSEG);
+  p.nk = 1;
+  while (p.nk < DW && p.nk < segs) p.nk *= 2;
+  p.ksplits = (int)cdiv(segs, p.nk);
+  // Row groups per wave: one while that leaves workgroups waiting for few
+  // rounds, then two or four (X^ is quantised once per wave, whatever it owns).
+  const int64_t wgs = cdiv(N, 16 * (DW / p.nk)) * p.ksplits;
+  p.groups = wgs <= 2 * device_cus() ? 1 : (wgs <= 4 * device_cus() ? 2 : 4);
+  p.row_blocks = (int)cdiv(N, (int64_t)16 * p.groups * (DW / p.nk));
+  p.hsplits = (int)cdiv(K, DW * HSEG);
+  p.hblocks = r ? (int)cdiv(r, 16) * p.hsplits : 0;
+  return p;
+}
+
+struct GemmPlan {
+  int bm, bn, splits;
+};
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t C) {
+  const int64_t cus = device_cus();
+  const int64_t big = cdiv(M, 256) * cdiv(N, 256);
+  if (big * 2 > cus) return GemmPlan{256, 256, 1};
+  const int64_t mid = cdiv(M, 128) * cdiv(N, 128);
+  int splits = 1;
+  while (splits < 8 && mid * splits * 2 <= 2 * cus && C / (splits * 2) >= 2) splits *= 2;
+  return GemmPlan{128, 128, splits};
+}
+
+struct FwdPieces {
+  float *y_part, *h_part;                // decode, or the split tiles
+  uint8_t *xc, *xs;                      // X^
+  uint16_t *sH;
+  float *hf, *lr_part;
+  size_t bytes;
+};
+FwdPieces fwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r) {
+  FwdPieces p{};
+  Carve c(ws);
+  if (M <= kDecodeRows) {
+    const DecodePlan d = decode_plan(N, K, r);
+    p.y_part = c.take<float>((int64_t)d.ksplits * M * N);
+    if (r) p.h_part = c.take<float>((int64_t)d.hsplits * M * 64);
+  } else {
+    const int64_t C = mx_chunks(K);
+    const GemmPlan g = gemm_plan(M, N, C);
+    p.xc = c.take<uint8_t>(M * 128 * C);
+    p.xs = c.take<uint8_t>(M * 8 * C);
+    if (g.splits > 1) p.y_part = c.take<float>((int64_t)g.splits * M * N);
+    if (r) {
+      if (g.splits > 1) p.hf = c.take<float>(M * r);
+      else p.sH = c.take<uint16_t>(M * 64);
+      p.lr_part = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
+    }
+  }
+  p.bytes = std::max<size_t>(c.off, 256);
+  return p;
+}
+
+template <int TM, int TN, int WR, int WC, bool PART>
+hipError_t launch_tiles(MxGemmArgs g, hipStream_t st) {
+  constexpr int BM = 32 * TM * WR, BN = 32 * TN * WC;
+  g.tiles_m = (int)cdiv(g.M, BM);
+  g.tiles_n = (int)cdiv(g.N, BN);
+  // An XCD runs about 1/8 of the tiles, at most a 32-CU round at a time: a
+  // square-ish patch of them shares the most.
+  g.group_m = std::max(1, std::min(g.tiles_m, 4));
+  const int64_t T = (int64_t)g.tiles_m * g.tiles_n;
+  if (T > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)T, (unsigned)g.splits), block(64 * WR * WC);
+  TraceScope tr(QN_TRACE_MX_GEMM, st);
+  hipLaunchKernelGGL((mx_gemm_kernel<TM, TN, WR, WC, PART>), grid, block, 0, st, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_finish(const MxFinishArgs &f, hipStream_t st) {
+  const dim3 grid((unsigned)(f.N / 64), (unsigned)cdiv(f.M, 16));
+  hipLaunchKernelGGL(mx_finish_kernel, grid, dim3(256), 0, st, f);
+  return hipGetLastError();
+}
+
+hipError_t run_decode(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
+  const DecodePlan p = decode_plan(a.N, a.K, a.r);
+  const bool direct = a.r == 0 && p.ksplits == 1;
+  MxDecodeArgs d{a.X, a.M, a.N, a.K, mx_chunks(a.K), a.codes, a.scales, a.A, a.r, a.drop, w.y_part, w.h_part,
+                 direct ? a.Y : nullptr, p.nk, p.ksplits, p.row_blocks, p.hsplits, p.groups};
+  const dim3 grid((unsigned)(p.row_blocks * p.ksplits + p.hblocks)), block(64 * DW);
+  {
+    TraceScope tr(QN_TRACE_MX_GEMV, st);
+    if (p.groups == 1) hipLaunchKernelGGL(mx_decode_kernel<1>, grid, block, 0, st, d);
+    else if (p.groups == 2) hipLaunchKernelGGL(mx_decode_kernel<2>, grid, block, 0, st, d);
+    else hipLaunchKernelGGL(mx_decode_kernel<4>, grid, block, 0, st, d);
+  }
+  QN_TRY(hipGetLastError());
+  if (direct) return hipSuccess;
+  return launch_finish(MxFinishArgs{w.y_part, p.ksplits, a.r ? w.h_part : nullptr, p.hsplits, 64, a.M, a.N, a.r, a.B,
+                                    a.s, a.drop.c, a.Y, a.H_out}, st);
+}
+
+template <bool Q>
+hipError_t launch_codec(const void *x, int bf16, int64_t rows, int64_t cols, const uint8_t *ci, const uint8_t *si,
+                        uint8_t *co, uint8_t *so, void *out, hipStream_t st) {
+  const int64_t C = mx_chunks(cols), chunks = rows * C;
+  const FastDiv cd = fast_div((uint32_t)C);
+  const dim3 grid((unsigned)cdiv(chunks, kThreads / 32 * kUnits)), block(kThreads);
+  const bool vec = cols % 8 == 0;
+  const auto *xb = static_cast<const uint8_t *>(x);
+  auto *ob = static_cast<uint8_t *>(out);
+  const uint32_t R = (uint32_t)rows, n = (uint32_t)chunks;
+#define QN_CODEC(B, V)                                                                                          \
+  do {                                                                                                          \
+    if constexpr (Q) hipLaunchKernelGGL((mx_quantize_kernel<B, V>), grid, block, 0, st, xb, R, cols, cd, n, co, so); \
+    else hipLaunchKernelGGL((mx_dequant_kernel<B, V>), grid, block, 0, st, ci, si, R, cols, cd, n, ob);         \
+  } while (0)
+  if (bf16) {
+    if (vec) QN_CODEC(true, true);
+    else QN_CODEC(true, false);
+  } else {
+    if (vec) QN_CODEC(false, true);
+    else QN_CODEC(false, false);
+  }
+#undef QN_CODEC
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void *x, int is_bf16, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales,
+                              hipStream_t st) {
+  TraceScope tr(QN_TRACE_MX_QUANTIZE, st);
+  return launch_codec<true>(x, is_bf16, rows, cols, nullptr, nullptr, codes, scales, nullptr, st);
+}
+
+hipError_t launch_mx_dequant(const qn_mx_matrix &W, void *out, int out_bf16, hipStream_t st) {
+  TraceScope tr(QN_TRACE_MX_DEQUANT, st);
+  return launch_codec<false>(nullptr, out_bf16, W.rows, W.cols, W.codes, W.scales, nullptr, nullptr, out, st);
+}
+
+size_t mx_fwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r) { return fwd_pieces(nullptr, M, N, K, r).bytes; }
+
+hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
+  const FwdPieces w = fwd_pieces(a.ws, a.M, a.N, a.K, a.r);
+  if (a.M <= kDecodeRows) return run_decode(a, w, st);
+  const int64_t C = mx_chunks(a.K);
+  const GemmPlan p = gemm_plan(a.M, a.N, C);
+  QN_TRY(launch_mx_quantize(a.X, 1, a.M, a.K, w.xc, w.xs, st));
+  if (a.r) {
+    LowRankArgs l{};
+    l.L = a.X; l.ldl = a.K; l.M = a.M; l.Kc = a.K;
+    l.P = a.A; l.ldp = a.K; l.R = a.r; l.scale = a.s; l.drop = a.drop;
+    l.Mp = a.M; l.part = w.lr_part;
+    if (p.splits > 1) {
+      l.out_f32 = a.H_out ? a.H_out : w.hf;
+    } else {
+      l.out_f32 = a.H_out;
+      l.out_b = w.sH;
+      l.ldb = 64;
+    }
+    QN_TRY(launch_lowrank(l, st));
+  }
+  MxGemmArgs g{w.xc, w.xs, a.codes, a.scales, a.M, a.N, C, a.r ? w.sH : nullptr, a.B, a.r, a.Y, w.y_part,
+               0, 0, 0, p.splits};
+  if (p.bm == 256) return launch_tiles<2, 4, 4, 2, false>(g, st);
+  if (p.splits == 1) return launch_tiles<2, 2, 2, 2, false>(g, st);
+  QN_TRY((launch_tiles<2, 2, 2, 2, true>(g, st)));
+  // The low-rank product's H already carries the dropout's factor.
+  return launch_finish(MxFinishArgs{w.y_part, p.splits, a.r ? (a.H_out ? a.H_out : w.hf) : nullptr, 1, (int)a.r, a.M,
+                                    a.N, a.r, a.B, a.s, 1.0f, a.Y, nullptr}, st);
+}
+
+}  // namespace qn

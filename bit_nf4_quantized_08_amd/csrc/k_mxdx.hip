@@ -1,0 +1,378 @@
+// dX of the MXFP4 linear on gfx950: dX[M, K] = G[M, N] bf16(W[N, K]) + c keep *
+// (dH[M, r] A[r, K]).
+//
+// The contraction runs down the weight's rows, across its blocks, so the
+// block scales cannot ride on the matrix instruction: each 64-row step
+// expands a 64 x 256 patch of codes to bf16 (exact, v_cvt_scalef32_pk_bf16_fp4)
+// into LDS as it lies, and the fragments, which need eight consecutive
+// contraction rows of one column, come back through the transposing LDS read
+// (ds_read_b64_tr_b16: 16 lanes point at 4 rows x 16 columns and receive 16
+// columns x 4 rows).  Bound by the bf16 matrix rate and by LDS reads, which
+// take about three quarters of the MFMAs' time at 256 x 256.
+//
+// A workgroup of 8 waves owns a (32 TM WR) x 256 tile of dX: one chunk of the
+// weight's columns, so a step's scale bytes are 512 contiguous bytes.  Step s
+// multiplies stage s & 1 while G of step s + 1 goes to the other stage by
+// direct-to-LDS loads and the codes of step s + 1, loaded during step s - 1, are
+// expanded into it.
+//
+// Expanded stage: row n (pitch 576 bytes: four rows of a transposing read fall
+// on different banks), 16-byte units of 8 columns.  Thread (n, ch) expands one
+// block, columns 32 ch .. +31, as four units q = 0..3; unit (ch, q) sits at slot
+// 8 q + ch, so that the eight lanes of a write cycle store 128 contiguous
+// bytes.  A wave's columns are the units ch = UW wc .. + UW - 1 for all q (UW =
+// 8 / WC): 32 UW consecutive columns of dX.  "Tile column" x of a wave is unit
+// (q, u) = (x / 8 / UW, x / 8 % UW).
+//
+// G's stage is swizzled in 16-byte pieces as in the forward: piece k of row r
+// at slot k ^ ((r >> 1) & 7).  Contraction order: in sub-step c of a step, lane
+// half h supplies rows 32 h + 8 c .. + 7 of both operands.
+
+#include <algorithm>
+
+#include "qn_philox.h"
+#include "qn_tile.h"
+
+namespace qn {
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+constexpr int kRowPitch = 576;           // bytes per expanded row
+constexpr int kWStage = 64 * kRowPitch;  // bytes per expanded stage
+
+template <int TM, int TN, int WR, int WC, bool DROP, bool PART>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
+  static_assert(WR * WC == 8 && TN * WC == 8, "8 waves over 256 columns");
+  constexpr int BM = 32 * TM * WR, UW = 8 / WC;
+  constexpr int GL = BM / 64;   // direct loads (8 rows each) per wave and step
+  static_assert(GL >= 1, "stage loads");
+  constexpr int kPitch = 32 * TN + 8;   // bf16 per row of a store block
+  __shared__ __attribute__((aligned(16))) uint8_t gs0[BM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t gs1[BM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t ws0[kWStage];
+  __shared__ __attribute__((aligned(16))) uint8_t ws1[kWStage];
+
+  int tm, tn;
+  xcd_tile((int)blockIdx.x, tiles_m, tiles_n, group_m, tm, tn);
+  const int split = (int)blockIdx.y;
+  const int64_t m0 = (int64_t)tm * BM, k0 = (int64_t)tn * 256;
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave % WR, wc = wave / WR;
+  const int steps = (int)(a.N / 64), s0 = (int)((int64_t)steps * split / a.splits),
+            s1 = (int)((int64_t)steps * (split + 1) / a.splits);
+
+  // G: load g covers rows 8g .. 8g + 7, 64 columns (128 bytes).
+  const rsrc_t rg = make_rsrc_u(a.G + m0 * a.N, (a.M - m0) * a.N * 2);
+  uint32_t go[GL];
+#pragma unroll
+  for (int i = 0; i < GL; ++i) {
+    const int row = 8 * (wave * GL + i) + (lane >> 3);
+    go[i] = (uint32_t)(row * a.N * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  }
+  auto issue_g = [&](uint8_t *dst, int s) {
+    const uint32_t b = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(dst)) + wave * GL * 1024;
+#pragma unroll
+    for (int i = 0; i < GL; ++i) load_lds16(rg, b + i * 1024, go[i], s * 128);
+  };
+  // W: thread (n, ch) of a step.
+  const int64_t C = (a.K + 255) / 256, pitch = 128 * C;
+  const int wn = tid >> 3, ch = tid & 7;
+  const rsrc_t rw = make_rsrc_u(a.codes + tn * 128, a.N * pitch - tn * 128);
+  const rsrc_t rs = make_rsrc_u(a.scales + (int64_t)tn * a.N * 8, a.N * 8);
+  const uint32_t wo = (uint32_t)(wn * pitch + 16 * ch);
+  struct Set {
+    u32x4 code;
+    uint32_t sb;
+  };
+  auto load_w = [&](Set &t, int s) {
+    t.code = __builtin_amdgcn_raw_buffer_load_b128(rw, wo, (int)(s * 64 * pitch), 0);
+    t.sb = __builtin_amdgcn_raw_buffer_load_b8(rs, (uint32_t)tid, s * 512, 0);
+  };
+  uint32_t wst = (uint32_t)(wn * kRowPitch + 16 * ch);
+  auto expand = [&](const Set &t, uint8_t *dst) {
+    const float sc = as_f32(t.sb << 23);
+    const uint32_t cw[4] = {t.code.x, t.code.y, t.code.z, t.code.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      u32x4 o;
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 0));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 1));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 2));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 3));
+      if (t.sb == 255u) o = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+      *reinterpret_cast<u32x4 *>(dst + wst + 128 * q) = o;
+    }
+  };
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  // Fragments.  G: row lr of a tile, piece 4 lh + c.  W: 16 tile columns per
+  // group of 16 lanes; a lane points at row (lane % 16) / 4, columns 4 (lane % 4).
+  uint32_t fg[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) fg[c] = (uint32_t)((wr * 32 * TM + lr) * 128 + 16 * ((4 * lh + c) ^ ((lr >> 1) & 7)));
+  uint32_t fw[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int g16 = 2 * j + ((lane >> 4) & 1), q = 2 * g16 / UW, u = 2 * g16 % UW;
+    const int scol = 64 * q + 8 * (UW * wc + u);
+    fw[j] = (uint32_t)((32 * lh + ((lane & 15) >> 2)) * kRowPitch + (scol + 4 * (lane & 3)) * 2);
+  }
+  auto read_g = [&](const uint8_t *gst, int i, int c) {
+    return *reinterpret_cast<const bf16x8 *>(gst + fg[c] + i * 32 * 128);
+  };
+  auto read_w = [&](const uint8_t *wst_, int j, int c) {
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+    const uint32_t b = lds_offset(wst_) + fw[j] + c * 8 * kRowPitch;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)b);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)(b + 4 * kRowPitch));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(bf16x8, (s16x8){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+  };
+  auto multiply = [&](const uint8_t *gst, const uint8_t *wst_) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      bf16x8 fa[TM], fb[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) fa[i] = read_g(gst, i, c);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) fb[j] = read_w(wst_, j, c);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  const int last = s1 - 1;
+  Set t0, t1;
+  load_w(t0, s0);
+  issue_g(gs0, s0);
+  load_w(t1, min(s0 + 1, last));
+  expand(t0, ws0);
+  stage_barrier();
+  // Step s: stage (s - s0) & 1; past the end the last step is loaded again.
+  for (int s = s0; s < s1; s += 2) {
+    issue_g(gs1, min(s + 1, last));
+    load_w(t0, min(s + 2, last));
+    expand(t1, ws1);
+    multiply(gs0, ws0);
+    stage_barrier();
+    if (s + 1 >= s1) break;
+    issue_g(gs0, min(s + 2, last));
+    load_w(t1, min(s + 3, last));
+    expand(t0, ws0);
+    multiply(gs1, ws1);
+    stage_barrier();
+  }
+
+  const int64_t row0 = m0 + wr * 32 * TM, colw = k0 + 32 * UW * wc;   // the wave's first row and column
+  // dX column (from k0) of the wave's tile column x.
+  auto col_of = [&](int x) {
+    const int un = x >> 3, q = un / UW, u = un % UW;
+    return 32 * (UW * wc + u) + 8 * q + (x & 7);
+  };
+  if constexpr (PART) {
+    float *part = a.part + (int64_t)split * a.M * a.K;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int64_t k = k0 + col_of(32 * j + lr);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t m = row0 + 32 * i + 8 * (e >> 2) + 4 * lh + (e & 3);
+          if (m < a.M && k < a.K) part[m * a.K + k] = acc[i][j][e];
+        }
+      }
+    return;
+  }
+
+  // Adapter term: A as an expanded stage (rows j < r, zero beyond), dH's
+  // fragments from global memory.  Every wave has passed the last barrier, so
+  // ws0 is free.
+  if (a.r) {
+    {
+      const rsrc_t ra = make_rsrc_u(a.A, a.r * a.K * 2);
+      const int64_t col = k0 + 32 * ch;
+      u32x4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = __builtin_amdgcn_raw_buffer_load_b128(
+            ra, wn < a.r && col < a.K ? (uint32_t)((wn * a.K + col + 8 * q) * 2) : kOutOfRange, 0, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<u32x4 *>(ws0 + wst + 128 * q) = v[q];
+    }
+    const rsrc_t rh = make_rsrc_u(a.dHb + row0 * a.ldh, (a.M - row0) * a.ldh * 2);
+    bf16x8 fa[TM][4];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int j = 32 * lh + 8 * c;
+        fa[i][c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  rh, j < a.ldh ? (uint32_t)(((32 * i + lr) * a.ldh + j) * 2) : kOutOfRange, 0, 0));
+      }
+    __syncthreads();
+    if constexpr (DROP) {
+      const DropKey dk = drop_key(a.drop);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          f32x16 t;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[e] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i][c], read_w(ws0, j, c), t, 0, 0, 0);
+          add_dropped(acc[i][j], t, dk, a.drop.c, row0 + 32 * i, a.K, lane,
+                      [&](int x) { return k0 + col_of(32 * j + x); });
+        }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const bf16x8 fb = read_w(ws0, j, c);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i][c], fb, acc[i][j], 0, 0, 0);
+        }
+    }
+  }
+
+  // Store through LDS: each wave turns its 32-row blocks into whole 16-byte
+  // pieces of dX's rows.  ws1 (the stages of G too) is no longer read; ws0 may
+  // still be (adapter), so the blocks lie in ws1, gs0 and gs1.
+  constexpr int kBlock = 32 * kPitch * 2;   // bytes
+  constexpr int kInW = kWStage / kBlock, kInG = BM * 128 / kBlock;
+  static_assert(kInW + 2 * kInG >= 8, "store blocks fit");
+  uint16_t *blk = reinterpret_cast<uint16_t *>(wave < kInW ? ws1 + wave * kBlock
+                                               : wave < kInW + kInG ? gs0 + (wave - kInW) * kBlock
+                                                                    : gs1 + (wave - kInW - kInG) * kBlock);
+  const rsrc_t rout = make_rsrc_u(a.dX + m0 * a.K, (a.M - m0) * a.K * 2);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        blk[(8 * (e >> 2) + 4 * lh + (e & 3)) * kPitch + j * 32 + lr] = f32_to_bf16(acc[i][j][e]);
+    constexpr int kPieces = 4 * TN, kRows = 64 / kPieces;   // pieces per row, rows per store
+#pragma unroll
+    for (int p = 0; p < 32 / kRows; ++p) {
+      const int row = kRows * p + lane / kPieces, t = lane % kPieces, q = t & 3, u = t >> 2;
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(&blk[row * kPitch + 8 * (UW * q + u)]);
+      const int64_t lrow = wr * 32 * TM + 32 * i + row, k = colw + 8 * t;
+      __builtin_amdgcn_raw_buffer_store_b128(v, rout, k < a.K ? (uint32_t)((lrow * a.K + k) * 2) : kOutOfRange, 0, 0);
+    }
+  }
+}
+
+// dX = bf16(sum of the splits' partial products + the adapter term), one thread
+// per 8 columns (one generator call).
+__global__ __launch_bounds__(256) void mx_dx_finish_kernel(MxDxArgs a) {
+  const int64_t per = a.K / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * per) return;
+  const int64_t m = i / per, k = 8 * (i % per);
+  float v[8], t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = t[e] = 0.0f;
+  for (int s = 0; s < a.splits; ++s) {
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part + ((int64_t)s * a.M + m) * a.K + k);
+    const f32x4 x = p[0], y = p[1];
+    const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += z[e];
+  }
+  for (int64_t j = 0; j < a.r; ++j) {
+    const float h = bf16_to_f32(a.dHb[m * a.ldh + j]);
+    const u32x4 x = *reinterpret_cast<const u32x4 *>(a.A + j * a.K + k);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t[2 * e] += h * bf16_lo(w[e]);
+      t[2 * e + 1] += h * bf16_hi(w[e]);
+    }
+  }
+  uint32_t keep = 0xFFu;
+  if (a.drop.thr) {
+    const DropKey dk = drop_key(a.drop);
+    uint32_t w[4];
+    philox7((uint64_t)i, dk, w);
+    keep = keep_bits8(w, dk.thr2);
+  }
+  if (a.r)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (keep >> e & 1u) v[e] += a.drop.c * t[e];
+  u32x4 o;
+  o.x = pack_bf16x2(v[0], v[1]); o.y = pack_bf16x2(v[2], v[3]);
+  o.z = pack_bf16x2(v[4], v[5]); o.w = pack_bf16x2(v[6], v[7]);
+  *reinterpret_cast<u32x4 *>(a.dX + m * a.K + k) = o;
+}
+
+// 256 x 256 tiles when they fill half the GPU or more, else 64 x 256 tiles, cut
+// over the contraction until they do (at least four steps per cut).
+struct DxPlan {
+  bool big;
+  int splits;
+};
+DxPlan dx_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t cus = device_cus(), cols = cdiv(K, 256);
+  if (cdiv(M, 256) * cols * 2 > cus) return DxPlan{true, 1};
+  const int64_t t = cdiv(M, 64) * cols;
+  int splits = 1;
+  while (splits < 8 && t * splits * 2 <= cus && N / 64 / (splits * 2) >= 4) splits *= 2;
+  return DxPlan{false, splits};
+}
+
+template <int TM, int TN, int WR, int WC>
+hipError_t launch_tiles(const MxDxArgs &a, hipStream_t st) {
+  const int tiles_m = (int)cdiv(a.M, 32 * TM * WR), tiles_n = (int)cdiv(a.K, 256);
+  const int64_t T = (int64_t)tiles_m * tiles_n;
+  if (T > INT32_MAX) return hipErrorInvalidValue;
+  const int gm = std::max(1, std::min(tiles_m, 4));
+  const dim3 grid((unsigned)T, (unsigned)a.splits), block(512);
+  TraceScope tr(QN_TRACE_MX_DX, st);
+  if constexpr (TM == 1) {
+    if (a.splits > 1) {
+      hipLaunchKernelGGL((mx_dx_kernel<TM, TN, WR, WC, false, true>), grid, block, 0, st, a, tiles_m, tiles_n, gm);
+      return hipGetLastError();
+    }
+  }
+  if (a.drop.thr)
+    hipLaunchKernelGGL((mx_dx_kernel<TM, TN, WR, WC, true, false>), grid, block, 0, st, a, tiles_m, tiles_n, gm);
+  else
+    hipLaunchKernelGGL((mx_dx_kernel<TM, TN, WR, WC, false, false>), grid, block, 0, st, a, tiles_m, tiles_n, gm);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t mx_dx_part_bytes(int64_t M, int64_t N, int64_t K) {
+  const DxPlan p = dx_plan(M, N, K);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)K * sizeof(float) : 0;
+}
+
+hipError_t launch_mx_dx(const MxDxArgs &in, hipStream_t st) {
+  MxDxArgs a = in;
+  const DxPlan p = dx_plan(a.M, a.N, a.K);
+  a.splits = p.splits;
+  if (p.big) return launch_tiles<2, 4, 4, 2>(a, st);
+  const hipError_t e = launch_tiles<1, 2, 2, 4>(a, st);
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(mx_dx_finish_kernel, dim3((unsigned)cdiv(a.M * (a.K / 8), 256)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace qn

@@ -32,6 +32,10 @@
 // its right operand (B or A, zero beyond r) through the weight stage, into
 // the same accumulators before the bf16 store.
 //
+// dX with dropout on the adapter's input needs c keep(m, n) times the adapter
+// term alone, so that step then multiplies into a zeroed 32 x 32 tile at a time
+// and adds the kept elements to the accumulators (add_dropped).
+//
 // Weight layouts:
 //   NK (forward): output column n reads weight row n, contraction along K; a
 //      producer lane dequantises 32 consecutive codes of one row (16 bytes).
@@ -53,6 +57,7 @@
 
 #include "qn_device.h"
 #include "qn_internal.h"
+#include "qn_philox.h"
 
 namespace qn {
 namespace {
@@ -457,7 +462,7 @@ __device__ __forceinline__ void lds_barrier() {
 // Exactly one workgroup (2 waves per SIMD) fits a CU, so tell the compiler
 // that higher occupancy is not reachable: it may then keep a whole step's
 // operands in registers instead of re-reading them one by one.
-template <bool KN, bool DQ, bool EPI_NK, bool Q4>
+template <bool KN, bool DQ, bool EPI_NK, bool Q4, bool DROP = false>
 __global__ __launch_bounds__(kThreads, 1) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void qgemm_kernel(QGemmGroup grp, Code16 cb) {
   // The problem this workgroup belongs to (a grouped launch runs several
@@ -755,11 +760,31 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
     const int xi = (int)(steps % 3);
     const uint16_t *xa = xi == 0 ? xs0 : (xi == 1 ? xs1 : xs2);
     const uint16_t *wa = (steps & 1) ? ws1 : ws0;
+    if constexpr (DROP) {
+      const DropKey dk = drop_key(a.drop);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      Frag f;
-      read_f(f, xa, wa, c);
-      mma(f);
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          f32x16 t;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[e] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const bf16x8 af = *reinterpret_cast<const bf16x8 *>(&xa[aoff[c] + i * 32 * BK]);
+            const bf16x8 bf = *reinterpret_cast<const bf16x8 *>(&wa[rb + j * 32 * LD + (KN ? (bpos[j] ^ (8 * c)) : 8 * c)]);
+            t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af, bf, t, 0, 0, 0);
+          }
+          add_dropped(acc[i][j], t, dk, a.drop.c, m0 + wave_u * WM + 32 * i, a.Nout, lane,
+                      [&](int x) { return n0 + kn_col(32 * j + x); });
+        }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        Frag f;
+        read_f(f, xa, wa, c);
+        mma(f);
+      }
     }
     lds_barrier();   // pairs with the producers' last barrier
   }
@@ -831,7 +856,7 @@ constexpr int BM2 = 256, BN2 = 256;
 constexpr int R_TILE2 = BN2 * LD;
 constexpr int XSTAGE2 = BM2 * BK;
 
-template <bool DQ, bool Q4, bool KN>
+template <bool DQ, bool Q4, bool KN, bool DROP = false>
 __global__ __launch_bounds__(kThreads2, 1) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void qgemm2_kernel(QGemmGroup grp, Code16 cb) {
   static_assert(!(KN && Q4), "four-step scales are for row-major weights");
@@ -1185,7 +1210,25 @@ void qgemm2_kernel(QGemmGroup grp, Code16 cb) {
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
   lds_barrier();
-  {
+  if constexpr (DROP) {
+    const DropKey dk = drop_key(a.drop);
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        f32x16 t;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) t[e] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bf16x8 af = *reinterpret_cast<const bf16x8 *>(&xa[aoff[c] + i * 32 * BK]);
+          const bf16x8 bf = *reinterpret_cast<const bf16x8 *>(&wa[rb + j * 32 * LD + (KN ? (bpos[j] ^ (8 * c)) : 8 * c)]);
+          t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af, bf, t, 0, 0, 0);
+        }
+        add_dropped(acc[i][j], t, dk, a.drop.c, m0 + rg * WM + 32 * i, a.Nout, lane,
+                    [&](int x) { return n0 + kn_col(128 * cg + 32 * j + x); });
+      }
+  } else {
     Frag f;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -1603,6 +1646,17 @@ hipError_t launch_tiling(const QGemmArgs *in, int n, bool wide, int wide_kind, h
   grp.n = n;
   const dim3 grid((unsigned)total);
   if constexpr (KN) {
+    if (in[0].drop.thr) {   // dX with dropout on the adapter's input (one problem)
+      const Code16 cb = code16(in[0].qtype);
+      if (wide) {
+        if (dq) hipLaunchKernelGGL((qgemm2_kernel<true, false, true, true>), grid, dim3(kThreads2), 0, st, grp, cb);
+        else hipLaunchKernelGGL((qgemm2_kernel<false, false, true, true>), grid, dim3(kThreads2), 0, st, grp, cb);
+      } else {
+        if (dq) hipLaunchKernelGGL((qgemm_kernel<true, true, EPI_NK, false, true>), grid, dim3(kThreads), 0, st, grp, cb);
+        else hipLaunchKernelGGL((qgemm_kernel<true, false, EPI_NK, false, true>), grid, dim3(kThreads), 0, st, grp, cb);
+      }
+      return hipGetLastError();
+    }
     if (wide) {   // dX: the 8-wave 256 x 256 tiling
       if (dq) hipLaunchKernelGGL((qgemm2_kernel<true, false, true>), grid, dim3(kThreads2), 0, st, grp, code16(in[0].qtype));
       else hipLaunchKernelGGL((qgemm2_kernel<false, false, true>), grid, dim3(kThreads2), 0, st, grp, code16(in[0].qtype));

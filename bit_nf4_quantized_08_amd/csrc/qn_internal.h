@@ -107,6 +107,16 @@ struct Code16 {
 };
 Code16 code16(int qtype = QN_NF4);
 
+// Counter-based dropout (qn_philox.h): thr = 0 means none.
+struct DropArgs {
+  uint32_t thr;
+  float c;                     // 1 / (1 - thr / 65536); 1 without dropout
+  uint64_t seed, offset;
+  const uint64_t *offset_dev;  // added to offset on the device, or null
+};
+constexpr DropArgs kNoDrop{0u, 1.0f, 0u, 0u, nullptr};
+hipError_t launch_dropout(const void *x, int is_bf16, int64_t n, const DropArgs &d, void *y, hipStream_t s);
+
 // Dequant-GEMM (k_qgemm.hip).  out[M, Nout] (bf16) =
 //   sum_k L[m, k] * W_hat(k, n)  +  sum_{j<r} L2[m, j] * R2(j, n)
 // where W_hat(k, n) = bf16(fl32(table[q] * scale)) of weight element
@@ -131,6 +141,7 @@ struct QGemmArgs {
   uint16_t *out;
   int64_t ldo;
   int tiles_m, tiles_n, group_m;
+  DropArgs drop;   // dX only: thr > 0 adds c keep(m, n) * (adapter term), keep over [M, Nout]
 };
 hipError_t launch_qgemm_fwd(const QGemmArgs &a, hipStream_t s);
 hipError_t launch_qgemm_dx(const QGemmArgs &a, hipStream_t s);
@@ -170,6 +181,7 @@ struct LowRankArgs {
   int64_t ldt_rows, Mp;
   float *part;
   int splits;   // set by the launcher
+  DropArgs drop = kNoDrop;   // thr > 0: L is read as keep * L and C scaled by c
 };
 int lowrank_splits(int64_t M, int64_t Kc);
 size_t lowrank_part_bytes(int64_t M, int64_t Kc, int64_t R);
@@ -191,6 +203,7 @@ struct ColRedArgs {
   float *part;
   uint16_t *out;
   bool transpose;
+  DropArgs drop = kNoDrop;   // thr > 0: Q is read as keep * Q and the sum scaled by c
 };
 int colred_splits(int64_t M);
 hipError_t launch_colred(const ColRedArgs &a, hipStream_t s, int trace_kind);
@@ -211,9 +224,13 @@ struct FwdArgs {
   float *H_out;          // fp32 [M,r] or null
   void *ws;
   size_t ws_bytes;
+  DropArgs drop = kNoDrop;   // run_fwd_dropout only
 };
 size_t fwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r);
 hipError_t run_fwd(const FwdArgs &a, hipStream_t s);
+// The forward with dropout on the adapter's input: the MFMA path for every M.
+size_t fwd_dropout_workspace(int64_t M, int64_t N, int64_t K, int64_t r);
+hipError_t run_fwd_dropout(const FwdArgs &a, hipStream_t s);
 // Several forwards: decode-path problems (M <= 8) as in run_fwd, the others
 // with one low-rank launch and one dequant-GEMM launch per scale source.  Each
 // problem's workspace is a[g].ws (carved by the caller).
@@ -237,8 +254,45 @@ struct BwdArgs {
   uint16_t *dB;          // bf16 [N,r]
   void *ws;
   size_t ws_bytes;
+  DropArgs drop = kNoDrop;
+  const uint8_t *mx_scales = nullptr;   // non-null: the base is MXFP4 (codes, mx_scales)
 };
 size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r);
 hipError_t run_bwd(const BwdArgs &a, hipStream_t s);
+
+// ---- MXFP4 (k_mx.hip, k_mxdx.hip).  Layouts as qn_mx_matrix.
+inline int64_t mx_chunks(int64_t cols) { return (cols + QN_MX_CHUNK - 1) / QN_MX_CHUNK; }
+hipError_t launch_mx_quantize(const void *x, int is_bf16, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales,
+                              hipStream_t s);
+hipError_t launch_mx_dequant(const qn_mx_matrix &W, void *out, int out_bf16, hipStream_t s);
+struct MxFwdArgs {
+  const uint16_t *X;       // bf16 [M, K]
+  int64_t M, N, K, r;      // r = 0: no adapter
+  const uint8_t *codes, *scales;
+  const uint16_t *A, *B;
+  float s;
+  uint16_t *Y;
+  float *H_out;
+  void *ws;
+  DropArgs drop;
+};
+size_t mx_fwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r);
+hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t s);
+// dX[M, K] = G[M, N] bf16(W[N, K]) + c keep * (dHb[M, ldh] A[r, K]); r = 0: no adapter term.
+struct MxDxArgs {
+  const uint16_t *G;
+  int64_t M, N, K;
+  const uint8_t *codes, *scales;
+  const uint16_t *dHb;
+  int64_t ldh;
+  const uint16_t *A;
+  int64_t r;
+  DropArgs drop;
+  uint16_t *dX;
+  float *part;             // mx_dx_part_bytes(M, N, K) of workspace
+  int splits;              // set by the launcher
+};
+size_t mx_dx_part_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_dx(const MxDxArgs &a, hipStream_t s);
 
 }  // namespace qn

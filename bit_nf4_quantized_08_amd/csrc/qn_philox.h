@@ -1,0 +1,111 @@
+// Counter-based dropout, device side (gfx950).
+//
+// Element i of a tensor (row-major) is field i % 8 of generator call i / 8:
+// Philox4x32 with 7 rounds (J. Salmon, M. Moraes, R. Dror, D. Shaw, "Parallel
+// random numbers: as easy as 1, 2, 3", SC 2011: the smallest round count that
+// passed all their tests; the usual 10 leave a margin that a dropout mask does
+// not use), counter (call index, offset) and key (seed), gives four 32-bit
+// words, read as eight 16-bit fields, low half first.  The element is kept
+// when its field is at least thr = round(65536 p).  One call serves the eight
+// elements of a 16-byte bf16 load, so the mask costs 14 32 x 32 -> 64 bit
+// multiplies for eight elements and is never stored: the backward forms it
+// again from the same (seed, offset).
+#pragma once
+
+#include "qn_device.h"
+#include "qn_internal.h"
+
+namespace qn {
+
+struct DropKey {
+  uint32_t k0, k1, o0, o1;
+  uint32_t thr2;   // thr - 1 in both halves (thr >= 1)
+};
+
+// Wave-uniform; reads the caller's device-side offset, if any.
+__device__ __forceinline__ DropKey drop_key(const DropArgs &d) {
+  uint64_t off = d.offset;
+  if (d.offset_dev) off += *d.offset_dev;
+  DropKey k;
+  k.k0 = (uint32_t)d.seed;
+  k.k1 = (uint32_t)(d.seed >> 32);
+  k.o0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)off);
+  k.o1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(off >> 32));
+  k.thr2 = (d.thr - 1u) * 0x10001u;
+  return k;
+}
+
+// The four words of generator call g.
+__device__ __forceinline__ void philox7(uint64_t g, const DropKey &k, uint32_t (&w)[4]) {
+  uint32_t c0 = (uint32_t)g, c1 = (uint32_t)(g >> 32), c2 = k.o0, c3 = k.o1, k0 = k.k0, k1 = k.k1;
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)p1;
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)p0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  w[0] = c0; w[1] = c1; w[2] = c2; w[3] = c3;
+}
+
+// Two fields -> 0xFFFF in the half of each kept element, 0 in the other's.
+__device__ __forceinline__ uint32_t keep_mask2(uint32_t w, uint32_t thr2) {
+  const u16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w), __builtin_bit_cast(u16x2, thr2));
+  const u16x2 one = {1, 1}, zero = {0, 0};
+  return __builtin_bit_cast(uint32_t, (u16x2)(zero - __builtin_elementwise_min(d, one)));
+}
+
+// Bit t set when element t of the call's eight is kept.
+__device__ __forceinline__ uint32_t keep_bits8(const uint32_t (&w)[4], uint32_t thr2) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t m = keep_mask2(w[t], thr2);
+    b |= (m & 1u) << (2 * t) | ((m >> 16) & 1u) << (2 * t + 1);
+  }
+  return b;
+}
+
+// acc += c keep * t for one 32 x 32 tile of dX's adapter term (a lane's element
+// e is row 8 (e / 4) + 4 (lane / 32) + e % 4, column lane % 32): rows row0 .. +31
+// of a tensor of ncols columns, tile columns x .. x + 7 (x a multiple of 8)
+// its columns col(x) .. col(x) + 7, one generator call.  Lane (lr, lh) runs the
+// calls of row lr, x = 16 lh and 16 lh + 8, which puts the 32 x 32 mask in the
+// wave row by row; an element's lane mask is then two rows' words, read out of
+// their lanes into a scalar pair.  Elements that are not kept add nothing,
+// whatever t holds.  The key passes through an empty asm per tile and the tile
+// is fenced: hoisted out of the adapter step or run ahead of each other, the
+// tiles' generator calls would spill the accumulators.
+template <typename Col>
+__device__ __forceinline__ void add_dropped(f32x16 &acc, const f32x16 &t, DropKey dk, float c, int64_t row0,
+                                            int64_t ncols, int lane, Col &&col) {
+  const int lr = lane & 31, lh = lane >> 5;
+  uint32_t half = 0;
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" : "+s"(dk.k0), "+s"(dk.o0), "+v"(row0));
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int64_t n = col(16 * lh + 8 * q);
+    uint32_t w[4];
+    philox7((uint64_t)(row0 + lr) * (uint64_t)(ncols / 8) + (uint64_t)(n >> 3), dk, w);
+    half |= keep_bits8(w, dk.thr2) << (8 * q);
+  }
+  // The row's 32 bits: low 16 in lane lr, high 16 in lane lr + 32.
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int ra = 8 * (e >> 2) + (e & 3), rb = ra + 4;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)half, ra) |
+                        (uint32_t)__builtin_amdgcn_readlane((int)half, ra + 32) << 16;
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)half, rb) |
+                        (uint32_t)__builtin_amdgcn_readlane((int)half, rb + 32) << 16;
+    const uint64_t mask = ((uint64_t)hi << 32) | lo;
+    const float v = __builtin_fmaf(c, t[e], acc[e]);
+    acc[e] = __builtin_amdgcn_inverse_ballot_w64(mask) ? v : acc[e];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+}  // namespace qn

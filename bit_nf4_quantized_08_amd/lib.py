@@ -6,7 +6,10 @@ device pointers, sizes and torch's current HIP stream to the C ABI declared in
 in the library's HIP kernels; there is no CPU or PyTorch fallback.
 
 Names follow the C ABI: ``nf4_quantize``, ``nf4_double_quant``, ``nf4_dequant``,
-``qlora_linear_fwd``, ``qlora_linear_bwd``, plus ``qn_codebook``.
+``qlora_linear_fwd``, ``qlora_linear_bwd``, ``qn_codebook``; dropout on the
+adapter's input (``Dropout``, ``dropout``, ``qlora_linear_fwd_dropout``,
+``qlora_linear_bwd_dropout``); and the microscaled base (``mxfp4_quantize``,
+``mxfp4_dequant``, ``qlora_mx_linear_fwd``, ``qlora_mx_linear_bwd``).
 """
 
 import ctypes
@@ -25,12 +28,13 @@ QN_OK = 0
 QN_F32, QN_BF16 = 0, 1
 QN_NF4, QN_FP4 = 0, 1
 QUANT_TYPES = {"nf4": QN_NF4, "fp4": QN_FP4}
-QN_OP_FWD, QN_OP_BWD = 0, 1
+QN_OP_FWD, QN_OP_BWD, QN_OP_FWD_DROPOUT = 0, 1, 2
 QN_ERR_SCRATCH = 8
 QN_ERR_MEMORY = 9
 QN_NOALLOC_SCRATCH_BYTES = 16 << 20
 QN_BLOCK, QN_GROUP, QN_MAX_RANK, QN_MAX_GROUP = 64, 256, 64, 8
 QN_ADAMW_MULTI = 32
+QN_MX_BLOCK, QN_MX_CHUNK = 32, 256
 
 _lib = None
 
@@ -85,6 +89,18 @@ class AdamWTensorStruct(ctypes.Structure):
                 ("u_step", ctypes.c_void_p)]
 
 
+class DropoutStruct(ctypes.Structure):
+    """qn_dropout_config."""
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_dev", ctypes.c_void_p)]
+
+
+class MXMatrixStruct(ctypes.Structure):
+    """qn_mx_matrix."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
 def load():
     """Load the shared library (once).  Raises if it has not been built."""
     global _lib
@@ -114,6 +130,18 @@ def load():
         "qlora_linear_fwd_noalloc": (i32, [vp, i64, ctypes.POINTER(NF4WeightStruct), vp, vp, i64, f32, vp, vp, vp]),
         "qlora_linear_bwd": (i32, [vp, vp, vp, i64, ctypes.POINTER(NF4WeightStruct), vp, vp, i64, f32, vp, vp,
                                    vp, vp, ctypes.c_size_t, vp]),
+        "qn_dropout": (i32, [vp, i32, i64, ctypes.POINTER(DropoutStruct), vp, vp]),
+        "qlora_linear_fwd_dropout": (i32, [vp, i64, ctypes.POINTER(NF4WeightStruct), vp, vp, i64, f32,
+                                           ctypes.POINTER(DropoutStruct), vp, vp, vp, ctypes.c_size_t, vp]),
+        "qlora_linear_bwd_dropout": (i32, [vp, vp, vp, i64, ctypes.POINTER(NF4WeightStruct), vp, vp, i64, f32,
+                                           ctypes.POINTER(DropoutStruct), vp, vp, vp, vp, ctypes.c_size_t, vp]),
+        "qn_mxfp4_quantize": (i32, [vp, i32, i64, i64, vp, vp, vp]),
+        "qn_mxfp4_dequant": (i32, [ctypes.POINTER(MXMatrixStruct), vp, i32, vp]),
+        "qlora_mx_workspace_size": (ctypes.c_size_t, [i32, i64, i64, i64, i64]),
+        "qlora_mx_linear_fwd": (i32, [vp, i64, ctypes.POINTER(MXMatrixStruct), vp, vp, i64, f32,
+                                      ctypes.POINTER(DropoutStruct), vp, vp, vp, ctypes.c_size_t, vp]),
+        "qlora_mx_linear_bwd": (i32, [vp, vp, vp, i64, ctypes.POINTER(MXMatrixStruct), vp, vp, i64, f32,
+                                      ctypes.POINTER(DropoutStruct), vp, vp, vp, vp, ctypes.c_size_t, vp]),
         "qn_status_string": (ctypes.c_char_p, [i32]),
         "qn_trace_enable": (i32, [i32]),
         "qn_set_gemm_variant": (i32, [i32]),
@@ -133,7 +161,8 @@ def exported_symbols():
             "qlora_workspace_size",
             "qlora_linear_fwd", "qlora_linear_fwd_noalloc", "qlora_workspace_size_grouped",
             "qlora_linear_fwd_grouped", "qlora_linear_bwd", "qn_status_string", "qn_version", "qn_set_gemm_variant", "qn_trace_enable",
-            "qn_trace_read"]
+            "qn_trace_read", "qn_dropout", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout", "qn_mxfp4_quantize",
+            "qn_mxfp4_dequant", "qlora_mx_workspace_size", "qlora_mx_linear_fwd", "qlora_mx_linear_bwd"]
 
 
 def status_string(status):
@@ -517,8 +546,291 @@ def qlora_linear_bwd(dY, X, w: NF4Weight, A, B, alpha, want_dX=True, use_double_
     return dX, dA, dB
 
 
+# ------------------------------------------------- dropout and the MXFP4 base
+def _one_device(*tensors):
+    """The one GPU all given tensors (None skipped) lie on."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop()
+
+
+def _launch(device, fn, *args):
+    """Call fn(*args, stream) with the tensors' device current, on its current stream."""
+    torch = _torch()
+    with torch.cuda.device(device):
+        _check(fn, getattr(load(), fn)(*args, _stream()))
+
+
+@dataclass
+class Dropout:
+    """qn_dropout_config: probability, seed, and the offset that picks the mask
+    within a seed.  ``offset_dev`` (optional, a one-element int64 GPU tensor) is
+    added to the offset when the kernels run: advance it between the replays of
+    a captured graph, and keep it unchanged from a forward to its backward."""
+    p: float
+    seed: int
+    offset: int = 0
+    offset_dev: Optional[object] = None
+
+    def struct(self):
+        torch = _torch()
+        for name in ("seed", "offset"):
+            if not 0 <= int(getattr(self, name)) < 1 << 64:
+                raise ValueError(f"{name} must be in [0, 2^64)")
+        if self.offset_dev is not None:
+            _need(self.offset_dev, "offset_dev", torch.int64)
+            if self.offset_dev.numel() != 1:
+                raise ValueError("offset_dev must hold one element")
+        return DropoutStruct(float(self.p), int(self.seed), int(self.offset),
+                             self.offset_dev.data_ptr() if self.offset_dev is not None else 0)
+
+
+def _drop_ref(drop):
+    return ctypes.byref(drop.struct()) if drop is not None else None
+
+
+def _drop_dev(drop):
+    return drop.offset_dev if drop is not None else None
+
+
+def dropout(x, drop: Dropout, out=None):
+    """qn_dropout of a contiguous fp32 or bf16 tensor of any shape; ``out`` may be
+    ``x``.  Applied to a gradient with the same ``drop`` it is the backward."""
+    torch = _torch()
+    _need(x, "x")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be float32 or bfloat16")
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out, "out", x.dtype)
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    dev = _one_device(x, out, drop.offset_dev)
+    dt = QN_BF16 if x.dtype == torch.bfloat16 else QN_F32
+    _launch(dev, "qn_dropout", _ptr(x), dt, x.numel(), _drop_ref(drop), _ptr(out))
+    return out
+
+
+@dataclass
+class MXMatrix:
+    """A matrix [rows, cols] in MXFP4 form (device tensors)."""
+    codes: "object"                 # uint8 [rows, 128 C], C = ceil(cols / 256)
+    scales: "object"                # uint8 [C, rows, 8]
+    rows: int
+    cols: int
+
+    @staticmethod
+    def empty(rows, cols, device="cuda"):
+        """Storage of a matrix, not yet written (mxfp4_quantize's ``out``)."""
+        torch = _torch()
+        C = -(-cols // QN_MX_CHUNK)
+        return MXMatrix(torch.empty((rows, 128 * C), dtype=torch.uint8, device=device),
+                        torch.empty((C, rows, 8), dtype=torch.uint8, device=device), int(rows), int(cols))
+
+    @property
+    def N(self):
+        return self.rows
+
+    @property
+    def K(self):
+        return self.cols
+
+    def struct(self):
+        torch = _torch()
+        _need(self.codes, "codes", torch.uint8)
+        _need(self.scales, "scales", torch.uint8)
+        C = -(-self.cols // QN_MX_CHUNK)
+        if self.codes.numel() != self.rows * 128 * C or self.scales.numel() != self.rows * 8 * C:
+            raise ValueError("codes must be [rows, 128 C] and scales [C, rows, 8] with C = ceil(cols / 256)")
+        return MXMatrixStruct(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+
+
+def mxfp4_quantize(X, out: Optional[MXMatrix] = None):
+    """qn_mxfp4_quantize of a 2-D fp32 or bf16 device tensor -> MXMatrix."""
+    torch = _torch()
+    _need(X, "X", ndim=2)
+    if X.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("X must be float32 or bfloat16")
+    rows, cols = X.shape
+    if out is None:
+        out = MXMatrix.empty(rows, cols, X.device)
+    if (out.rows, out.cols) != (rows, cols):
+        raise ValueError("out must have X's shape")
+    st = out.struct()
+    dev = _one_device(X, out.codes, out.scales)
+    dt = QN_BF16 if X.dtype == torch.bfloat16 else QN_F32
+    _launch(dev, "qn_mxfp4_quantize", _ptr(X), dt, rows, cols, _ptr(out.codes), _ptr(out.scales))
+    return out
+
+
+def mxfp4_dequant(w: MXMatrix, out_dtype="bf16", out=None):
+    """The values an MXMatrix stands for, [rows, cols] bf16 (or fp32); a given
+    ``out`` decides the type."""
+    torch = _torch()
+    types = {"bf16": torch.bfloat16, "f32": torch.float32}
+    if out is None:
+        out = torch.empty((w.rows, w.cols), dtype=types[out_dtype], device=w.codes.device)
+    _need(out, "out", ndim=2)
+    if out.dtype not in types.values() or tuple(out.shape) != (w.rows, w.cols):
+        raise ValueError("out must be a float32 or bfloat16 [rows, cols] tensor")
+    st = w.struct()
+    dev = _one_device(w.codes, w.scales, out)
+    dt = QN_BF16 if out.dtype == torch.bfloat16 else QN_F32
+    _launch(dev, "qn_mxfp4_dequant", ctypes.byref(st), _ptr(out), dt)
+    return out
+
+
+def mx_workspace_size(op, M, N, K, r):
+    return int(load().qlora_mx_workspace_size(op, M, N, K, r))
+
+
+def mx_workspace(op, M, N, K, r, device="cuda"):
+    """Workspace of the MXFP4 linear for op QN_OP_FWD or QN_OP_BWD (r = 0: no adapter)."""
+    torch = _torch()
+    nbytes = mx_workspace_size(op, M, N, K, r)
+    if nbytes == 0:
+        raise QNError("qlora_mx_workspace_size", 2)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _linear_args(X, w, A, B, H, other=None, other_name=None):
+    """Check a linear's operands; (M, K, r).  A and B are both None for r = 0."""
+    torch = _torch()
+    _need(X, "X", torch.bfloat16, 2)
+    M, K = X.shape
+    if (A is None) != (B is None):
+        raise ValueError("A and B go together")
+    r = 0
+    if A is not None:
+        _need(A, "A", torch.bfloat16, 2)
+        _need(B, "B", torch.bfloat16, 2)
+        r = A.shape[0]
+        if A.shape[1] != w.K or tuple(B.shape) != (w.N, r):
+            raise ValueError("A must be [r, K] and B [N, r]")
+    if K != w.K:
+        raise ValueError("X must be [M, K]")
+    if other is not None:
+        _need(other, other_name, torch.bfloat16, 2)
+        if tuple(other.shape) != (M, w.N):
+            raise ValueError(f"{other_name} must be [M, N]")
+    if H is not None:
+        if r == 0:
+            raise ValueError("H needs an adapter")
+        _need(H, "H", torch.float32, 2)
+        if tuple(H.shape) != (M, r):
+            raise ValueError("H must be [M, r]")
+    return int(M), int(K), int(r)
+
+
+def _need_ws(ws):
+    torch = _torch()
+    _need(ws, "ws", torch.uint8, 1)
+
+
+def _grads(out, want_dX, M, N, K, r, device):
+    """The gradients' tensors (dX, dA, dB), checked or allocated."""
+    torch = _torch()
+    shapes = ((M, K), (r, K), (N, r))
+    if out is None:
+        bf = dict(dtype=torch.bfloat16, device=device)
+        dX = torch.empty(shapes[0], **bf) if want_dX else None
+        return (dX,) + ((torch.empty(shapes[1], **bf), torch.empty(shapes[2], **bf)) if r else (None, None))
+    for t, name, shape in zip(out, ("dX", "dA", "dB"), shapes):
+        if t is None:
+            if name == "dX" or r == 0:
+                continue
+            raise ValueError(f"{name} is required")
+        _need(t, name, torch.bfloat16, 2)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+    return tuple(out)
+
+
+def qlora_linear_fwd_dropout(X, w: NF4Weight, A, B, alpha, drop: Dropout, want_H=False, use_double_quant=True, Y=None,
+                             ws=None, H=None):
+    """qlora_linear_fwd with dropout on the adapter's input: H = c (keep * X) A^T,
+    Y = X bf16(dequant(W))^T + (alpha/r) H B^T.  The workspace is
+    ``workspace(QN_OP_FWD_DROPOUT, ...)``."""
+    torch = _torch()
+    if A is None or B is None:
+        raise ValueError("A and B are required")
+    M, K, r = _linear_args(X, w, A, B, H, Y, "Y")
+    if Y is None:
+        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
+    want_H = want_H or H is not None
+    if want_H and H is None:
+        H = torch.empty((M, r), dtype=torch.float32, device=X.device)
+    if ws is None:
+        ws = workspace(QN_OP_FWD_DROPOUT, M, w.N, w.K, r, X.device)
+    _need_ws(ws)
+    st = w.struct(use_double_quant)
+    dev = _one_device(X, A, B, Y, H, ws, w.codes, w.absmax, w.absmax_q, w.scale2, _drop_dev(drop))
+    _launch(dev, "qlora_linear_fwd_dropout", _ptr(X), M, ctypes.byref(st), _ptr(A), _ptr(B), r, float(alpha),
+            _drop_ref(drop), _ptr(Y), _ptr(H), _ptr(ws), ws.numel())
+    return (Y, H) if want_H else Y
+
+
+def qlora_linear_bwd_dropout(dY, X, w: NF4Weight, A, B, alpha, drop: Dropout, want_dX=True, use_double_quant=True,
+                             out=None, ws=None, H=None):
+    """Backward of qlora_linear_fwd_dropout: (dX or None, dA, dB).  ``H`` is the
+    (dropped) one that forward returned, or None to form it again."""
+    if A is None or B is None:
+        raise ValueError("A and B are required")
+    M, K, r = _linear_args(X, w, A, B, H, dY, "dY")
+    dX, dA, dB = _grads(out, want_dX, M, w.N, K, r, X.device)
+    if ws is None:
+        ws = workspace(QN_OP_BWD, M, w.N, w.K, r, X.device)
+    _need_ws(ws)
+    st = w.struct(use_double_quant)
+    dev = _one_device(dY, X, A, B, H, ws, dX, dA, dB, w.codes, w.absmax, w.absmax_q, w.scale2, _drop_dev(drop))
+    _launch(dev, "qlora_linear_bwd_dropout", _ptr(dY), _ptr(X), _ptr(H), M, ctypes.byref(st), _ptr(A), _ptr(B), r,
+            float(alpha), _drop_ref(drop), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())
+    return dX, dA, dB
+
+
+def qlora_mx_linear_fwd(X, w: MXMatrix, A=None, B=None, alpha=0.0, drop: Optional[Dropout] = None, want_H=False,
+                        Y=None, ws=None, H=None):
+    """Y = mx(X) W^T + (alpha/r) H B^T over an MXFP4 base, H = c (keep * X) A^T;
+    returns Y (and H).  A = B = None: the base alone."""
+    torch = _torch()
+    M, K, r = _linear_args(X, w, A, B, H, Y, "Y")
+    if Y is None:
+        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
+    want_H = want_H or H is not None
+    if want_H and H is None:
+        if r == 0:
+            raise ValueError("H needs an adapter")
+        H = torch.empty((M, r), dtype=torch.float32, device=X.device)
+    if ws is None:
+        ws = mx_workspace(QN_OP_FWD, M, w.N, w.K, r, X.device)
+    _need_ws(ws)
+    st = w.struct()
+    dev = _one_device(X, A, B, Y, H, ws, w.codes, w.scales, _drop_dev(drop))
+    _launch(dev, "qlora_mx_linear_fwd", _ptr(X), M, ctypes.byref(st), _ptr(A), _ptr(B), r, float(alpha),
+            _drop_ref(drop), _ptr(Y), _ptr(H), _ptr(ws), ws.numel())
+    return (Y, H) if want_H else Y
+
+
+def qlora_mx_linear_bwd(dY, X, w: MXMatrix, A=None, B=None, alpha=0.0, drop: Optional[Dropout] = None, want_dX=True,
+                        out=None, ws=None, H=None):
+    """Backward of qlora_mx_linear_fwd: (dX or None, dA, dB); dA and dB are None
+    without an adapter."""
+    M, K, r = _linear_args(X, w, A, B, H, dY, "dY")
+    dX, dA, dB = _grads(out, want_dX, M, w.N, K, r, X.device)
+    if ws is None:
+        ws = mx_workspace(QN_OP_BWD, M, w.N, w.K, r, X.device)
+    _need_ws(ws)
+    st = w.struct()
+    dev = _one_device(dY, X, A, B, H, ws, dX, dA, dB, w.codes, w.scales, _drop_dev(drop))
+    _launch(dev, "qlora_mx_linear_bwd", _ptr(dY), _ptr(X), _ptr(H), M, ctypes.byref(st), _ptr(A), _ptr(B), r,
+            float(alpha), _drop_ref(drop), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())
+    return dX, dA, dB
+
+
 TRACE_KINDS = {1: "quantize", 2: "double_quant", 3: "dequant", 4: "gemv", 5: "gemm_fwd", 6: "gemm_dx",
-               7: "gemm_db", 8: "gemm_da", 9: "lowrank", 10: "merge", 11: "adamw8"}
+               7: "gemm_db", 8: "gemm_da", 9: "lowrank", 10: "merge", 11: "adamw8", 12: "dropout",
+               13: "mx_quantize", 14: "mx_dequant", 15: "mx_gemv", 16: "mx_gemm", 17: "mx_dx"}
 
 
 def set_gemm_variant(variant):

@@ -335,6 +335,128 @@ int qlora_linear_bwd(const void *dY, const void *X, const float *H, int64_t M,
                      int64_t r, float alpha, void *dX, void *dA, void *dB,
                      void *workspace, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------- dropout
+ * Counter-based dropout.  The adapter of a QLoRA linear is trained with
+ * dropout on its input ([QE] "Turn a LoRA script into a QLoRA script with one
+ * config object": the adapter's config); the mask is a pure function of
+ * (seed, offset, element index), so it is never stored: the backward forms it
+ * again.
+ * Element i of the tensor (row-major) is field i % 8 of generator call i / 8:
+ * Philox4x32 with 7 rounds, counter words (call lo, call hi, offset lo,
+ * offset hi), key words (seed lo, seed hi); its four output words hold eight
+ * 16-bit fields, word 0's low half first.  With thr = min(65535,
+ * round-half-up(65536 p)) the element is kept iff its field >= thr, and kept
+ * elements are scaled by c = fl32(1 / (1 - thr/65536)): p is taken to the
+ * nearest multiple of 2^-16 and the expectation is unbiased for that p.  An
+ * element that is not kept is +0 whatever it was (infinities and NaN
+ * included).  p = 0 keeps every element.
+ *   p           0 <= p < 1 (QN_ERR_VALUE otherwise).
+ *   offset      picks the mask within a seed: a step number, or a step number
+ *               and a layer number.
+ *   offset_dev  device uint64, 8-byte aligned, added to offset when the kernels
+ *               run, or NULL.  A captured graph replays the host values of its
+ *               capture; a counter here, advanced between replays, gives each
+ *               replay its own mask.  It must hold the same value in a step's
+ *               forward and backward. */
+typedef struct {
+  float p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t *offset_dev;
+} qn_dropout_config;
+
+/* y = dropout(x), element-wise; of a gradient, the same call is the backward.
+ * x, y  device, n elements of dtype (QN_F32 or QN_BF16), 16-byte aligned; y may
+ * be x (any other overlap is not allowed).  y[i] = c x[i] in fp32, rounded once
+ * to dtype. */
+int qn_dropout(const void *x, int dtype, int64_t n, const qn_dropout_config *drop, void *y, void *stream);
+
+/* qlora_linear_fwd and qlora_linear_bwd with dropout on the adapter's input:
+ *     H = c (keep * X) A^T,   Y = X * bf16(dequant(W))^T + (alpha/r) H B^T
+ *     dH = s G B,  dB = s G^T H,  dA = c dH^T (keep * X),
+ *     dX = G bf16(dequant(W)) + c keep * (dH A)
+ * keep over [M, K] (element m K + k).  Arguments and shape rules as there; drop
+ * is required (its p may be 0).  The forward's workspace is
+ * qlora_workspace_size(QN_OP_FWD_DROPOUT, ...) bytes (every M takes the MFMA
+ * path), the backward's that of QN_OP_BWD.  A given H is the dropped one, as
+ * this forward wrote it. */
+#define QN_OP_FWD_DROPOUT 2
+int qlora_linear_fwd_dropout(const void *X, int64_t M, const qn_nf4_weight *W, const void *A, const void *B,
+                             int64_t r, float alpha, const qn_dropout_config *drop, void *Y, float *H_out,
+                             void *workspace, size_t ws_bytes, void *stream);
+int qlora_linear_bwd_dropout(const void *dY, const void *X, const float *H, int64_t M, const qn_nf4_weight *W,
+                             const void *A, const void *B, int64_t r, float alpha,
+                             const qn_dropout_config *drop, void *dX, void *dA, void *dB, void *workspace,
+                             size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------ microscaled FP4
+ * MXFP4: 4-bit E2M1 elements (the QN_FP4 code order: sign bit 3, exponent bits
+ * 2..1, mantissa bit 0; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one 8-bit
+ * power of two per 32 consecutive elements of a row (E8M0: byte b stands for
+ * 2^(b - 127), byte 255 for NaN), the OCP microscaling format.  gfx950's matrix
+ * instructions multiply it as it is.
+ * A matrix [rows, cols], any sizes; its rows are padded with zero blocks to a
+ * multiple of 256 columns, C = ceil(cols / 256) chunks:
+ *   codes   uint8[rows][128 C]: element k of a row in byte k/2, low nibble for
+ *           even k.
+ *   scales  uint8[C][rows][8]: the eight block scales of chunk c of a row side
+ *           by side, all rows of a chunk together (a tile's scales are then one
+ *           contiguous read).
+ * Padding holds zero codes; its scale bytes are 0 and must not be 255.
+ * codes 16-byte aligned, scales 8-byte aligned.  rows * C < 2^31. */
+#define QN_MX_BLOCK 32
+#define QN_MX_CHUNK 256
+typedef struct {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  int64_t rows;
+  int64_t cols;
+} qn_mx_matrix;
+
+/* Quantisation of X[rows, cols] (device, QN_F32 or QN_BF16, 16-byte aligned) to
+ * MXFP4, padding included.  Per block: e = max(floor(log2 max|x|) - 2, -127),
+ * byte e + 127, code = x 2^-e to the nearest E2M1 value, ties to the even code,
+ * magnitudes above 6 to 6 (the OCP rule); signs are kept, that of zero too.  A
+ * block of zeros has byte 0; a block holding an infinity or a NaN has byte 255
+ * and zero codes. */
+int qn_mxfp4_quantize(const void *X, int x_dtype, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales,
+                      void *stream);
+
+/* out[rows, cols] (QN_F32 or QN_BF16, 16-byte aligned) = the values a matrix
+ * stands for: exact in fp32 and in bf16 for every scale byte up to 252 (the
+ * largest the quantiser writes); bytes 253 and 254 may overflow to infinity,
+ * byte 255 gives NaN. */
+int qn_mxfp4_dequant(const qn_mx_matrix *W, void *out, int out_dtype, void *stream);
+
+/* Workspace bytes of the MXFP4 linear for op = QN_OP_FWD (with or without
+ * dropout) or QN_OP_BWD; r = 0 is the linear without an adapter.  0 for an
+ * invalid op or shape. */
+size_t qlora_mx_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t r);
+
+/* QLoRA linear over an MXFP4 base W[N, K] (rows N, cols K):
+ *     Y = mx(X) W^T + (alpha/r) H B^T,   H = c (keep * X) A^T
+ * mx(X) is X quantised as by qn_mxfp4_quantize (within the call), the product
+ * exact up to fp32 accumulation; the adapter reads X itself.  drop NULL: no
+ * dropout (keep = 1, c = 1).  r = 0 with A, B and H_out NULL: the base alone
+ * (alpha and drop are not used).  Otherwise arguments as qlora_linear_fwd.
+ * Shape rules: M >= 1, N % 64 == 0, K % 64 == 0, N * 128 C <= INT32_MAX,
+ * N and K <= 2^22, M * C < 2^31, 0 <= r <= QN_MAX_RANK.  A non-finite block of X makes its row of Y
+ * NaN.  M <= 16 streams the weights once (both operands on the matrix cores),
+ * larger M runs tiles. */
+int qlora_mx_linear_fwd(const void *X, int64_t M, const qn_mx_matrix *W, const void *A, const void *B, int64_t r,
+                        float alpha, const qn_dropout_config *drop, void *Y, float *H_out, void *workspace,
+                        size_t ws_bytes, void *stream);
+
+/* Its backward: the rounding of X passes the gradient through unchanged, so
+ *     dX = G bf16(W) + c keep * (dH A),  dH = s G B,  dB = s G^T H,
+ *     dA = c dH^T (keep * X)
+ * with G = dY.  bf16(W) is exact (qn_mxfp4_dequant).  H as in qlora_linear_bwd
+ * (NULL recomputes it).  dX may be NULL to skip it; with r = 0, A, B, H, dA and
+ * dB are NULL and X may be. */
+int qlora_mx_linear_bwd(const void *dY, const void *X, const float *H, int64_t M, const qn_mx_matrix *W,
+                        const void *A, const void *B, int64_t r, float alpha, const qn_dropout_config *drop,
+                        void *dX, void *dA, void *dB, void *workspace, size_t ws_bytes, void *stream);
+
 /* Kernel-level timing log, for measurement (off by default; costs nothing when
  * off).  While enabled, each call brackets its dominant kernel with two HIP
  * events recorded on the call's own stream and logs them under one of the
@@ -355,6 +477,12 @@ int qlora_linear_bwd(const void *dY, const void *X, const float *H, int64_t M,
 #define QN_TRACE_LOWRANK 9       /* X A^T or dY B low-rank product               */
 #define QN_TRACE_MERGE 10        /* qlora_merge kernel                           */
 #define QN_TRACE_ADAMW8 11       /* qn_adamw8_step(_multi) kernel                */
+#define QN_TRACE_DROPOUT 12      /* qn_dropout kernel                            */
+#define QN_TRACE_MX_QUANTIZE 13  /* MXFP4 quantisation kernel                    */
+#define QN_TRACE_MX_DEQUANT 14   /* MXFP4 dequantisation kernel                  */
+#define QN_TRACE_MX_GEMV 15      /* MXFP4 linear, few rows: streaming kernel     */
+#define QN_TRACE_MX_GEMM 16      /* MXFP4 linear, forward tile kernel            */
+#define QN_TRACE_MX_DX 17        /* MXFP4 linear, dX tile kernel                 */
 int qn_trace_enable(int on);
 int qn_trace_read(int *kinds, float *ms, int cap);
 

@@ -42,6 +42,14 @@ Parity status per function:
   adamw8.adamw8_step        pinned (first step and trajectory against plain
                             fp64 AdamW, brute-force state rounding, pure weight
                             decay); AdamW itself is a reading (not on the pages).
+  dropout.keep              pinned (the generator against its authors' published
+                            test vectors at 7 rounds, kept share, element
+                            order); the choice of generator is a reading.
+  mxfp4.quantize / dequant  pinned (brute-force nearest value with ties, closed
+                            forms of the scale); the format is the OCP
+                            microscaling specification's, not on the pages.
+  mxfp4.linear_forward /    pinned (against linear.forward / backward without
+  linear_backward           dropout, finite differences with it).
   merge.merge               pinned (exact rational sum within its rounding
                             bound, zero adapter reads back the dequantised
                             weight, X W_m^T against the forward, re-quantising
@@ -55,6 +63,8 @@ from .dq import double_quant, dq_absmax
 from .linear import forward, backward, dequant_bf16_weight
 from .merge import merge, adapter_delta
 from . import adamw8
+from . import dropout
+from . import mxfp4
 from . import sizes
 
 __all__ = [
@@ -63,5 +73,5 @@ __all__ = [
     "quantize", "pack_codes", "unpack_codes", "dequant", "block_absmax",
     "double_quant", "dq_absmax",
     "forward", "backward", "dequant_bf16_weight", "merge", "adapter_delta",
-    "sizes", "adamw8",
+    "sizes", "adamw8", "dropout", "mxfp4",
 ]

@@ -1,0 +1,211 @@
+"""GPU dropout: the element-wise operator bit for bit, and the NF4 linear with
+dropout on the adapter's input against the fp64 oracle.
+
+Tolerances of the linear are sums of what the kernels round: a bf16 output is
+off by at most 2^-8 of its value (half a step is eps/2 = 2^-8 with a step of
+2^-7), a bf16 operand of a product by 2^-8 of each term, and an fp32 sum of n
+terms by n 2^-23 of the sum of its terms' magnitudes (each addition rounds
+once, 2^-24; the factor 2 covers the products' own grouping).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from bit_nf4_quantized_08_amd import lib, synth
+from oracle import dropout as D
+from oracle import mxfp4 as MX
+from tests.gpu_util import dev, guarded, guards_intact, host, say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+SEED, OFF = 0xFEDCBA9876543210, 0x0123456789ABCDEF
+HALF, EPS = 2.0 ** -8, 2.0 ** -23
+
+
+def _bits(t):
+    torch.cuda.synchronize()
+    return t.view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32).cpu()
+
+
+def _expect(x, p, seed=SEED, off=OFF):
+    """torch CPU result of the definition: fl32(x * c), then x's type; +0 where not kept."""
+    k = torch.from_numpy(D.keep(x.numel(), p, seed, off)).view(x.shape)
+    y = (x.float() * np.float32(D.scale(p))).to(x.dtype)
+    return torch.where(k, y, torch.zeros((), dtype=x.dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 4095, 4096, 4099, 1 << 17])
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.5, 0.99999])
+def test_elementwise_bit_for_bit(dtype, n, p):
+    say(f"dropout n={n} p={p} {dtype}")
+    x = torch.from_numpy(synth.gaussian((n,), 1.0, n)).to(dtype)
+    nbytes = n * x.element_size()
+    full, view = guarded(nbytes, dtype)
+    lib.dropout(x.to(dev()), lib.Dropout(p, SEED, OFF), out=view)
+    assert torch.equal(_bits(view), _bits(_expect(x, p)))
+    assert guards_intact(full, nbytes)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_in_place_special_values_and_backward(dtype):
+    """In place; infinities and NaN leave +0 where dropped; a gradient takes the same mask."""
+    say(f"dropout special values {dtype}")
+    x = torch.tensor([float("inf"), float("nan"), -float("inf"), -0.0, 1.0, -2.0, 3e38, 1e-40] * 33).to(dtype)
+    want = _expect(x, 0.5)
+    y = x.to(dev())
+    lib.dropout(y, lib.Dropout(0.5, SEED, OFF), out=y)
+    got = y.cpu()
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(_bits(got)[~nan], _bits(want)[~nan])
+    g = lib.dropout(torch.ones_like(y), lib.Dropout(0.5, SEED, OFF)).cpu()
+    assert torch.equal(g != 0, torch.from_numpy(D.keep(x.numel(), 0.5, SEED, OFF)))
+
+
+def test_offset_on_the_device_and_graph_replays():
+    """offset_dev is added when the kernel runs: replays of one capture give one
+    mask per value, with other work between them, equal to eager calls."""
+    say("dropout under capture with a device offset")
+    x = torch.randn(3000, device=dev()).to(torch.bfloat16)
+    step = torch.zeros(1, dtype=torch.int64, device=dev())
+    d = lib.Dropout(0.3, SEED, OFF, offset_dev=step)
+    y = torch.empty_like(x)
+    lib.dropout(x, d, out=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        lib.dropout(x, d, out=y)
+    seen = []
+    for rep in range(4):
+        step.fill_(rep)
+        g.replay()
+        other = lib.dropout(x, lib.Dropout(0.3, SEED, (OFF + rep) % (1 << 64)))
+        torch.cuda.synchronize()
+        assert torch.equal(_bits(y), _bits(other)), rep
+        seen.append(y.clone())
+    assert not torch.equal(seen[0], seen[1])
+
+
+def _inputs(M, N, K, r, seed):
+    W = synth.gaussian((N, K), 0.02, synth.SEED_W + seed)
+    X = synth.to_bf16(synth.gaussian((M, K), 1.0, synth.SEED_X + seed))
+    A = synth.to_bf16(synth.gaussian((r, K), 0.05, synth.SEED_A + seed))
+    B = synth.to_bf16(synth.gaussian((N, r), 0.05, synth.SEED_B + seed))
+    G = synth.to_bf16(synth.gaussian((M, N), 1.0, synth.SEED_DY + seed))
+    return W, X, A, B, G
+
+
+def check_step(Y, H, grads, G, X, base_in, What, A, B, alpha, keep, c, given_H):
+    """A forward's (Y, H) and a backward's (dX, dA, dB) within the rounding they do (see the top)."""
+    ref_Y, ref_H = MX.linear_forward(base_in, X, What, A, B, alpha, keep, c)
+    ab = np.abs
+    (M, K), N, r = X.shape, What.shape[0], A.shape[0]
+    s = alpha / r
+    kx = ab(X) if keep is None else np.where(keep, ab(X), 0.0) * c
+    km = np.ones_like(X) if keep is None else keep * c
+    H_err = K * EPS * (kx @ ab(A).T) + 2 * EPS * ab(ref_H)
+    if H is not None:
+        assert np.all(ab(host(H) - ref_H) <= H_err), "H"
+    tol = HALF * ab(ref_Y) + K * EPS * (ab(base_in) @ ab(What).T) \
+        + s * ((HALF * ab(ref_H) + H_err) @ ab(B).T) * (1 + r * EPS)
+    if Y is not None:
+        e = ab(host(Y).astype(np.float64) - ref_Y)
+        assert np.all(e <= tol), f"Y off by {(e / tol).max():.2f} of its tolerance"
+    if grads is None:
+        return
+    dX, dA, dB = grads
+    rX, rA, rB = MX.linear_backward(G, X, What, A, B, alpha, keep, c, H=given_H)
+    dH = s * (G @ B)
+    dH_err = HALF * ab(dH) + N * EPS * s * (ab(G) @ ab(B))
+    if dX is not None:
+        tol = HALF * ab(rX) + N * EPS * (ab(G) @ ab(What)) + km * (dH_err @ ab(A) + r * EPS * (ab(dH) @ ab(A)))
+        e = ab(host(dX).astype(np.float64) - rX)
+        assert np.all(e <= tol), f"dX off by {(e / tol).max():.2f} of its tolerance"
+    tol = HALF * ab(rA) + (dH_err.T @ kx) + M * EPS * (ab(dH).T @ kx)
+    e = ab(host(dA).astype(np.float64) - rA)
+    assert np.all(e <= tol), f"dA off by {(e / tol).max():.2f} of its tolerance"
+    Hb = ref_H if given_H is None else given_H
+    tol = HALF * ab(rB) + s * (ab(G).T @ (HALF * ab(Hb) + (H_err if given_H is None else 0.0))) \
+        + M * EPS * s * (ab(G).T @ ab(Hb))
+    e = ab(host(dB).astype(np.float64) - rB)
+    assert np.all(e <= tol), f"dB off by {(e / tol).max():.2f} of its tolerance"
+
+
+def run_nf4(M, N, K, r, p, variant=0, dq=True, give_H=True, want_dX=True, seed=0):
+    alpha = 2.0 * r
+    W, X, A, B, G = _inputs(M, N, K, r, seed)
+    w = lib.quantize_weight(to_dev(W))
+    d = lib.Dropout(p, SEED + seed, OFF)
+    Xd, Ad, Bd, Gd = (t.to(dev()) for t in (X, A, B, G))
+    nb = M * N * 2
+    full, view = guarded(nb, torch.bfloat16)
+    lib.set_gemm_variant(variant)
+    try:
+        Y, H = lib.qlora_linear_fwd_dropout(Xd, w, Ad, Bd, alpha, d, want_H=True, use_double_quant=dq,
+                                            Y=view.view(M, N))
+        grads = lib.qlora_linear_bwd_dropout(Gd, Xd, w, Ad, Bd, alpha, d, want_dX=want_dX, use_double_quant=dq,
+                                             H=H if give_H else None)
+        torch.cuda.synchronize()
+    finally:
+        lib.set_gemm_variant(0)
+    assert guards_intact(full, nb)
+    p_, a_, _ = oracle.quantize(W)
+    What = oracle.dequant_bf16_weight(p_, N, K, oracle.dq_absmax(*oracle.double_quant(a_)) if dq else a_)
+    keep = D.keep(M * K, p, SEED + seed, OFF).reshape(M, K)
+    Xv, Av, Bv, Gv = (synth.bf16_values(t).astype(np.float64) for t in (X, A, B, G))
+    check_step(Y, H, grads, Gv, Xv, Xv, What.astype(np.float64), Av, Bv, alpha, keep, D.scale(p),
+               host(H).astype(np.float64) if give_H else None)
+    return Y, H, grads
+
+
+@pytest.mark.parametrize("M, N, K, r, p", [
+    (1, 64, 64, 1, 0.5), (5, 128, 192, 8, 0.1), (8, 64, 256, 16, 0.25), (9, 192, 128, 13, 0.1), (77, 320, 512, 24, 0.5),
+    (130, 64, 1024, 33, 0.05), (300, 512, 320, 64, 0.9), (33, 128, 128, 16, 0.0),
+])
+def test_nf4_linear_with_dropout(M, N, K, r, p):
+    say(f"nf4 dropout step M={M} N={N} K={K} r={r} p={p}")
+    run_nf4(M, N, K, r, p, seed=M)
+
+
+@pytest.mark.parametrize("variant", [1, 2])
+@pytest.mark.parametrize("dq", [True, False])
+@pytest.mark.parametrize("give_H", [True, False])
+def test_nf4_dropout_on_both_dX_tilings(variant, dq, give_H):
+    say(f"nf4 dropout variant={variant} dq={dq} give_H={give_H}")
+    run_nf4(300, 384, 576, 20, 0.2, variant=variant, dq=dq, give_H=give_H, seed=variant)
+
+
+def test_nf4_dropout_without_dX_and_without_dropping():
+    """want_dX=False leaves dA and dB; p = 0 is the plain linear's arithmetic on the MFMA path."""
+    say("nf4 dropout, no dX; p = 0 against the plain entry points")
+    run_nf4(40, 128, 256, 8, 0.3, want_dX=False)
+    W, X, A, B, G = (t if isinstance(t, np.ndarray) else t.to(dev()) for t in _inputs(40, 128, 256, 8, 1))
+    w = lib.quantize_weight(to_dev(W))
+    d = lib.Dropout(0.0, SEED, OFF)
+    Y, H = lib.qlora_linear_fwd_dropout(X, w, A, B, 16.0, d, want_H=True)
+    Y0, H0 = lib.qlora_linear_fwd(X, w, A, B, 16.0, want_H=True)
+    assert torch.equal(Y, Y0) and torch.equal(H, H0)
+    for a, b in zip(lib.qlora_linear_bwd_dropout(G, X, w, A, B, 16.0, d, H=H),
+                    lib.qlora_linear_bwd(G, X, w, A, B, 16.0, H=H)):
+        assert torch.equal(a, b)
+
+
+def test_masked_infinities_reach_nothing():
+    """X infinite at dropped positions only: H, and with it dA and dB, stay finite and equal those of X = 0 there."""
+    say("nf4 dropout, infinities at dropped positions")
+    M, N, K, r, p = 20, 64, 128, 8, 0.4
+    W, X, A, B, G = _inputs(M, N, K, r, 3)
+    keep = torch.from_numpy(D.keep(M * K, p, SEED, OFF).reshape(M, K))
+    w = lib.quantize_weight(to_dev(W))
+    d = lib.Dropout(p, SEED, OFF)
+    A, B, G = A.to(dev()), B.to(dev()), G.to(dev())
+    res = []
+    for fill in (float("inf"), 0.0):
+        Xf = torch.where(keep, X, torch.full_like(X, fill)).to(dev())
+        _, H = lib.qlora_linear_fwd_dropout(Xf, w, A, B, 16.0, d, want_H=True)
+        _, dA, dB = lib.qlora_linear_bwd_dropout(G, Xf, w, A, B, 16.0, d, H=H)
+        res.append((H, dA, dB))
+    for a, b in zip(*res):
+        assert torch.isfinite(a).all() and torch.equal(a, b)

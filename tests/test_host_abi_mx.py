@@ -1,0 +1,133 @@
+"""CPU-only: argument checks of the dropout and MXFP4 entry points.  Every call
+here is refused on the host before a launch (the addresses are made up)."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+from bit_nf4_quantized_08_amd import lib
+
+pytestmark = pytest.mark.skipif(not os.path.exists(lib.LIB_PATH), reason="library not built")
+
+FAKE, BIG = 0x10000, 1 << 40
+vp = ctypes.c_void_p
+NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, VALUE = 1, 2, 3, 4, 5, 7
+
+
+def drop(p=0.1, dev=0):
+    return ctypes.byref(lib.DropoutStruct(p, 1, 2, dev))
+
+
+def mx(rows=64, cols=64, codes=FAKE, scales=FAKE):
+    return ctypes.byref(lib.MXMatrixStruct(codes, scales, rows, cols))
+
+
+def test_dropout_refusals():
+    f = lib.load().qn_dropout
+    assert f(vp(0), 0, 8, drop(), vp(FAKE), vp(0)) == NULL
+    assert f(vp(FAKE), 0, 8, None, vp(FAKE), vp(0)) == NULL
+    assert f(vp(FAKE), 0, 8, drop(), vp(0), vp(0)) == NULL
+    assert f(vp(FAKE), 2, 8, drop(), vp(FAKE), vp(0)) == DTYPE
+    assert f(vp(FAKE), 0, 0, drop(), vp(FAKE), vp(0)) == SHAPE
+    assert f(vp(FAKE), 0, BIG + 1, drop(), vp(FAKE), vp(0)) == SHAPE
+    assert f(vp(FAKE + 8), 0, 8, drop(), vp(FAKE), vp(0)) == ALIGN
+    assert f(vp(FAKE), 0, 8, drop(dev=FAKE + 4), vp(FAKE), vp(0)) == ALIGN
+    for p in (1.0, -0.1, 2.0, float("nan"), float("inf")):
+        assert f(vp(FAKE), 0, 8, drop(p), vp(FAKE), vp(0)) == VALUE
+
+
+def test_mx_codec_refusals():
+    L = lib.load()
+    q = lambda x=FAKE, dt=0, rows=4, cols=32, c=FAKE, s=FAKE: L.qn_mxfp4_quantize(vp(x), dt, rows, cols, vp(c), vp(s),
+                                                                                  vp(0))
+    assert q(x=0) == q(c=0) == q(s=0) == NULL
+    assert q(dt=2) == DTYPE
+    assert q(rows=0) == q(cols=0) == q(cols=-5) == SHAPE
+    assert q(rows=1 << 31, cols=1) == q(rows=1 << 20, cols=1 << 20) == SHAPE
+    assert q(x=FAKE + 2) == q(c=FAKE + 8) == q(s=FAKE + 4) == ALIGN
+    d = lambda w, out=FAKE, dt=0: L.qn_mxfp4_dequant(w, vp(out), dt, vp(0))
+    assert d(None) == d(mx(codes=0)) == d(mx(scales=0)) == d(mx(), out=0) == NULL
+    assert d(mx(rows=0)) == SHAPE
+    assert d(mx(), dt=9) == DTYPE
+    assert d(mx(), out=FAKE + 4) == d(mx(codes=FAKE + 4)) == d(mx(scales=FAKE + 4)) == ALIGN
+
+
+def test_mx_workspace_size_rules():
+    f = lib.mx_workspace_size
+    for op in (lib.QN_OP_FWD, lib.QN_OP_BWD):
+        assert f(op, 1, 64, 64, 0) > 0 and f(op, 4096, 8192, 8192, 64) > 0
+        assert f(op, 0, 64, 64, 8) == f(op, 8, 63, 64, 8) == f(op, 8, 64, 96, 8) == f(op, 8, 64, 64, 65) == 0
+        assert f(op, 8, 64, 64, -1) == f(op, 8, (1 << 22) + 64, 64, 8) == f(op, 8, 64, (1 << 22) + 64, 8) == 0
+        assert f(op, 8, 1 << 20, 1 << 20, 8) == 0 and f(op, 1 << 40, 64, 64, 8) == 0
+    assert f(2, 8, 64, 64, 8) == 0
+    assert lib.workspace_size(lib.QN_OP_FWD_DROPOUT, 1, 64, 64, 8) > 0
+    assert lib.workspace_size(lib.QN_OP_FWD_DROPOUT, 1, 64, 60, 8) == 0
+
+
+def _fwd(W=None, X=FAKE, A=FAKE, B=FAKE, r=8, alpha=16.0, d=None, Y=FAKE, H=0, ws=FAKE, n=BIG, M=4, wide=True):
+    return lib.load().qlora_mx_linear_fwd(vp(X), M, W if W is not None else mx(), vp(A), vp(B), r, alpha, d, vp(Y),
+                                          vp(H), vp(ws), n, vp(0))
+
+
+def test_mx_forward_refusals():
+    assert _fwd(X=0) == _fwd(Y=0) == _fwd(A=0) == _fwd(B=0) == _fwd(W=mx(codes=0)) == NULL
+    assert _fwd(M=0) == _fwd(r=65) == _fwd(r=-1) == _fwd(W=mx(rows=32)) == _fwd(W=mx(cols=32)) == SHAPE
+    assert _fwd(r=0) == _fwd(r=0, A=0) == _fwd(r=0, A=0, B=0, H=FAKE) == SHAPE   # operands of no adapter
+    assert _fwd(r=0, A=0, B=0, ws=0) == WORKSPACE
+    assert _fwd(alpha=float("inf")) == _fwd(d=drop(1.0)) == VALUE
+    assert _fwd(X=FAKE + 8) == _fwd(A=FAKE + 2) == _fwd(B=FAKE + 2) == _fwd(Y=FAKE + 2) == _fwd(H=FAKE + 2) == ALIGN
+    assert _fwd(d=drop(dev=FAKE + 1)) == ALIGN
+    assert _fwd(ws=0) == _fwd(n=16) == WORKSPACE
+    assert _fwd(ws=FAKE + 16) == ALIGN
+
+
+def _bwd(W=None, G=FAKE, X=FAKE, A=FAKE, B=FAKE, r=8, alpha=16.0, d=None, dX=FAKE, dA=FAKE, dB=FAKE, H=0, ws=FAKE,
+         n=BIG, M=4):
+    return lib.load().qlora_mx_linear_bwd(vp(G), vp(X), vp(H), M, W if W is not None else mx(), vp(A), vp(B), r, alpha,
+                                          d, vp(dX), vp(dA), vp(dB), vp(ws), n, vp(0))
+
+
+def test_mx_backward_refusals():
+    assert _bwd(G=0) == _bwd(X=0) == _bwd(A=0) == _bwd(B=0) == _bwd(dA=0) == _bwd(dB=0) == NULL
+    none = dict(r=0, A=0, B=0, dA=0, dB=0)
+    assert _bwd(**dict(none, dX=0)) == NULL
+    assert _bwd(**dict(none, dA=FAKE)) == _bwd(**dict(none, H=FAKE)) == _bwd(M=0) == _bwd(W=mx(rows=65)) == SHAPE
+    assert _bwd(alpha=float("nan")) == _bwd(d=drop(-1.0)) == VALUE
+    assert _bwd(G=FAKE + 2) == _bwd(dX=FAKE + 2) == _bwd(dA=FAKE + 2) == _bwd(H=FAKE + 2) == ALIGN
+    assert _bwd(ws=0) == _bwd(n=16) == _bwd(**dict(none, n=16)) == WORKSPACE
+
+
+def test_nf4_dropout_refusals():
+    L = lib.load()
+    w = lib.NF4WeightStruct(FAKE, FAKE, 0, 0, 64, 64, 0)
+    f = lambda d=drop(), M=4, r=8, n=BIG, X=FAKE, bw=ctypes.byref(w): L.qlora_linear_fwd_dropout(
+        vp(X), M, bw, vp(FAKE), vp(FAKE), r, 16.0, d, vp(FAKE), vp(0), vp(FAKE), n, vp(0))
+    assert f(d=None) == f(X=0) == f(bw=None) == NULL
+    assert f(M=0) == f(r=0) == SHAPE
+    assert f(d=drop(1.5)) == VALUE and f(d=drop(dev=FAKE + 2)) == ALIGN and f(n=16) == WORKSPACE
+    b = lambda d=drop(), M=4, n=BIG, dA=FAKE: L.qlora_linear_bwd_dropout(
+        vp(FAKE), vp(FAKE), vp(0), M, ctypes.byref(w), vp(FAKE), vp(FAKE), 8, 16.0, d, vp(FAKE), vp(dA), vp(FAKE),
+        vp(FAKE), n, vp(0))
+    assert b(d=None) == b(dA=0) == NULL
+    assert b(M=0) == SHAPE and b(d=drop(float("nan"))) == VALUE and b(n=16) == WORKSPACE
+
+
+def test_python_refusals():
+    """The binding refuses before it reaches the library."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        lib.mxfp4_quantize(x)
+    with pytest.raises(ValueError, match="GPU"):
+        lib.dropout(x, lib.Dropout(0.1, 1))
+    with pytest.raises(ValueError, match="seed"):
+        lib.Dropout(0.1, 1 << 64).struct()
+    with pytest.raises(ValueError, match="offset"):
+        lib.Dropout(0.1, 1, offset=-1).struct()
+    with pytest.raises(ValueError, match="GPU"):
+        lib.Dropout(0.1, 1, offset_dev=torch.zeros(1, dtype=torch.int64)).struct()
+    m = lib.MXMatrix.empty(3, 300, device="cpu")
+    assert tuple(m.codes.shape) == (3, 256) and tuple(m.scales.shape) == (2, 3, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        m.struct()
