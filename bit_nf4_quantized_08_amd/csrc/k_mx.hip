@@ -13,9 +13,9 @@
 //   mx_gemm_kernel       tiles of mx(X) W^T with the adapter term (bound by the
 //                        matrix cores and the clock they sustain), optionally
 //                        over a part of K with fp32 partial sums
-//   mx_decode_kernel     M <= 16: streams the weights (bound by memory); its
-//                        last workgroups form the adapter's H partials
-//   mx_finish_kernel     adds partial sums and the adapter term
+//   mx_prep_kernel       M <= 16: X^ and the adapter's H partials
+//   mx_decode_kernel     M <= 16: streams the weights (bound by memory)
+//   mx_finish_kernel     adds partial products and the adapter term
 
 #include <algorithm>
 
@@ -116,20 +116,20 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
 
-// VEC: cols is a multiple of 8, so that a unit is aligned and whole.
-template <bool BF16, bool VEC>
-__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint8_t *__restrict__ x, uint32_t rows,
-                                                               int64_t cols, FastDiv cd, uint32_t chunks,
-                                                               uint8_t *__restrict__ codes,
-                                                               uint8_t *__restrict__ scales) {
+// VEC: cols is a multiple of 8, so that a unit is aligned and whole.  T threads
+// take chunks `first` .. of the matrix, U units each.
+template <bool BF16, bool VEC, int T, int U>
+__device__ __forceinline__ void quantize_units(const uint8_t *__restrict__ x, uint32_t rows, int64_t cols, FastDiv cd,
+                                               uint32_t chunks, uint32_t first, uint8_t *__restrict__ codes,
+                                               uint8_t *__restrict__ scales) {
   constexpr int V = BF16 ? 1 : 2, ES = BF16 ? 2 : 4;
   const int tid = threadIdx.x;
-  u32x4 v[kUnits][V];
-  uint32_t ch[kUnits], row[kUnits];
-  const uint32_t c0 = blockIdx.x * (kThreads / 32 * kUnits) + (tid >> 5);
+  u32x4 v[U][V];
+  uint32_t ch[U], row[U];
+  const uint32_t c0 = first + (tid >> 5);
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const uint32_t c = c0 + i * (kThreads / 32);
+  for (int i = 0; i < U; ++i) {
+    const uint32_t c = c0 + i * (T / 32);
     row[i] = div_by(c, cd);
     ch[i] = c - row[i] * cd.d;
     const int64_t col = (int64_t)ch[i] * 256 + 8 * (tid & 31);
@@ -155,17 +155,26 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint8_t *__
     }
   }
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
+  for (int i = 0; i < U; ++i) {
     uint32_t m = unit_amax<BF16>(v[i]);
     m = max(m, dpp<0xB1>(m));
     m = max(m, dpp<0x4E>(m));
     const uint32_t b = scale_byte<BF16>(m);
-    const uint32_t c = c0 + i * (kThreads / 32);
+    const uint32_t c = c0 + i * (T / 32);
     if (c < chunks) {
       reinterpret_cast<uint32_t *>(codes)[(int64_t)c * 32 + (tid & 31)] = unit_codes<BF16>(v[i], b);
       if ((tid & 3) == 0) scales[((int64_t)ch[i] * rows + row[i]) * 8 + ((tid & 31) >> 2)] = (uint8_t)b;
     }
   }
+}
+
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint8_t *__restrict__ x, uint32_t rows,
+                                                               int64_t cols, FastDiv cd, uint32_t chunks,
+                                                               uint8_t *__restrict__ codes,
+                                                               uint8_t *__restrict__ scales) {
+  quantize_units<BF16, VEC, kThreads, kUnits>(x, rows, cols, cd, chunks, blockIdx.x * (kThreads / 32 * kUnits), codes,
+                                              scales);
 }
 
 template <bool BF16, bool VEC>
@@ -460,38 +469,45 @@ void mx_gemm_kernel(MxGemmArgs a) {
 }
 
 // ------------------------------------------------------------------ few rows
-// M <= 16.  A wave owns 16 weight rows x 1024 columns: eight sub-steps of
-// v_mfma_scale_f32_16x16x128 with the weights as the first operand (lane: row
-// lane % 16, block lane / 16 of the sub-step's four, 64 contiguous bytes of a
-// row per load) and the 16 rows of X^ as the second.  All eight loads of a
-// group of rows are in flight before the first is used, the next group's
-// before this group is multiplied.  X^ is quantised by the wave itself, in
-// LDS, block by block (a lane per block: the rows that exist, not sixteen),
-// while its first weight loads are on their way.
+// M <= 16, two launches.  The first quantises X and forms partial sums of H = X
+// A^T; the second streams the weights and, when a workgroup's waves cover all
+// of K (up to 8192 columns), finishes Y.
+//
+// Streaming: a wave owns 16 weight rows x 1024 columns at a time, eight
+// sub-steps of v_mfma_scale_f32_16x16x128 with the weights as the first operand
+// (lane: row lane % 16, block lane / 16 of the sub-step's four) and the 16 rows
+// of X^ as the second.  The codes come through LDS by direct loads of two rows x
+// 512 contiguous bytes each: read straight into the fragments they would come
+// as 64-byte pieces of 16 rows (8192 x 8192, M = 1: 10.4 against 12.1 us).  The
+// wave reads a group's eight fragments into registers and asks for the next
+// group before it multiplies, so its 8 KB of LDS are always on their way.  16-byte
+// piece p of row r sits at slot p ^ r, which spreads a fragment read's 16 rows
+// over the banks.
 // A workgroup's 8 waves cover nk (a power of two) column segments of 8 / nk
-// row groups; partial sums meet in LDS, so that K up to 8192 leaves one sum.
+// sets of row groups; partial sums meet in LDS.
 constexpr int DW = 8;                 // waves
 constexpr int DSEG = 1024;            // columns per wave
 constexpr int DSUB = DSEG / 128;      // sub-steps
 constexpr int HSEG = 256;             // columns per wave of the H partials
 
-struct MxDecodeArgs {
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+
+struct MxPrepArgs {
   const uint16_t *X;
-  int64_t M, N, K, C;
-  const uint8_t *wc, *ws;
+  int64_t M, K;
+  FastDiv cd;          // by the chunks of a row
+  uint32_t chunks;     // of X
+  uint8_t *xc, *xs;
+  int qblocks;         // workgroups that quantise; the rest form H partials
   const uint16_t *A;
   int64_t r;
   DropArgs drop;
-  float *y_part;       // [ksplits][M][N]
   float *h_part;       // [hsplits][M][64]
-  uint16_t *out;       // written instead of y_part when non-null (no adapter, one split)
-  int nk, ksplits, row_blocks, hsplits, groups;   // groups: 16-row groups per wave
+  int hsplits;
 };
 
-__device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
-
 // H partials: workgroup b of them takes 16 ranks of A and 8 x HSEG columns.
-__device__ void decode_h(const MxDecodeArgs &a, int b, float (*red)[256]) {
+__device__ void prep_h(const MxPrepArgs &a, int b, float (*red)[256]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, kb = lane >> 4;
   const int jt = b / a.hsplits, hs = b % a.hsplits, j = 16 * jt + l16;
   const int64_t k0 = (int64_t)hs * (DW * HSEG) + wave * HSEG + 8 * kb;
@@ -531,118 +547,197 @@ __device__ void decode_h(const MxDecodeArgs &a, int b, float (*red)[256]) {
   }
 }
 
+__global__ __launch_bounds__(64 * DW) void mx_prep_kernel(MxPrepArgs a) {
+  __shared__ float red[DW][256];
+  if ((int)blockIdx.x < a.qblocks)
+    quantize_units<true, true, 64 * DW, 1>(reinterpret_cast<const uint8_t *>(a.X), (uint32_t)a.M, a.K, a.cd, a.chunks,
+                                           blockIdx.x * (64 * DW / 32), a.xc, a.xs);
+  else
+    prep_h(a, (int)blockIdx.x - a.qblocks, red);
+}
+
+// Adapter operands of a 16 x 16 block of Y (v_mfma_f32_16x16x32_bf16, B's rows
+// first): H's row m from its partial sums, ranks 8 kb .. + 7 of group jg of 32,
+// scaled by c, then s H in two bf16 pieces (high and the rest, 2^-17 of it left
+// over, so H counts as in fp32).
+struct HPieces {
+  bf16x8 hi, lo;
+};
+struct AdapterArgs {
+  const float *hp;     // [hsplits][M][ldh] unscaled (ldh 32 or 64; columns at or beyond r undefined), or null
+  int hsplits, ldh;
+  const uint16_t *B;   // bf16 [N, r]
+  int64_t r;
+  float s, c;
+  float *H_out;        // or null
+};
+
+// `store`: this lane's ranks of row m go to H_out.
+__device__ __forceinline__ HPieces load_h(const AdapterArgs &a, int64_t M, int64_t m, int j0, bool store) {
+  float h[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) h[t] = 0.0f;
+  // Batches of four partial sums, loaded without a condition (past the last
+  // one it is read again and dropped), so that a batch waits once.
+  const int jc = j0 < a.ldh ? j0 : 0;
+  for (int q0 = 0; q0 < a.hsplits; q0 += 4) {
+    f32x4 v[4][2];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.hp + ((int64_t)min(q0 + q, a.hsplits - 1) * M + m) * a.ldh + jc);
+      v[q][0] = p[0];
+      v[q][1] = p[1];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q0 + q < a.hsplits)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) h[t] += v[q][t >> 2][t & 3];
+  }
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) h[t] = j0 + t < a.r ? h[t] * a.c : 0.0f;
+  if (store)
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (j0 + t < a.r) a.H_out[m * a.r + j0 + t] = h[t];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const float x = a.s * h[2 * t], y = a.s * h[2 * t + 1];
+    hi[t] = pack_bf16x2(x, y);
+    lo[t] = pack_bf16x2(x - bf16_lo(hi[t]), y - bf16_hi(hi[t]));
+  }
+  return HPieces{__builtin_bit_cast(bf16x8, (u32x4{hi[0], hi[1], hi[2], hi[3]})),
+                 __builtin_bit_cast(bf16x8, (u32x4{lo[0], lo[1], lo[2], lo[3]}))};
+}
+
+// B[n][j0 .. j0 + 7], zero beyond r.
+__device__ __forceinline__ bf16x8 load_b(const AdapterArgs &a, int64_t n, int j0) {
+  uint32_t w[4];
+  if ((a.r & 7) == 0) {
+    const u32x4 v = j0 < a.r ? *reinterpret_cast<const u32x4 *>(a.B + n * a.r + j0) : u32x4{0, 0, 0, 0};
+    return __builtin_bit_cast(bf16x8, v);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t x = j0 + 2 * t < a.r ? a.B[n * a.r + j0 + 2 * t] : 0u;
+    const uint32_t y = j0 + 2 * t + 1 < a.r ? a.B[n * a.r + j0 + 2 * t + 1] : 0u;
+    w[t] = x | y << 16;
+  }
+  return __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+}
+
+__device__ __forceinline__ f32x4 add_adapter(f32x4 acc, bf16x8 b, const HPieces &h) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, h.hi, acc, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, h.lo, acc, 0, 0, 0);
+}
+
+struct MxDecodeArgs {
+  const uint8_t *xc, *xs;   // X^: codes [M, 128 C], scales [C][M][8]
+  int64_t M, N, C;
+  const uint8_t *wc, *ws;
+  AdapterArgs ad;           // used when out is written
+  uint16_t *out;            // Y, when one workgroup covers K; else null and
+  float *y_part;            // [ksplits][M][N]
+  int nk, row_blocks;
+};
+
 template <int G>   // row groups per wave
 __global__ __launch_bounds__(64 * DW) void mx_decode_kernel(MxDecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t xq[DW][16 * DSEG / 2];   // a wave's X^: piece (m, block) of 16 bytes
-  __shared__ __attribute__((aligned(16))) uint8_t xe[DW][16 * 32];         // its scale bytes, [m][block % 4][block / 4]
-  // The partial sums [DW][G * 256] take the place of the wave's own X^, which
-  // is in registers by then.
-  static_assert(G * 1024 <= 16 * DSEG / 2, "partial sums fit");
-  auto red = [&](int w) { return reinterpret_cast<float *>(xq[w]); };
+  __shared__ __attribute__((aligned(16))) uint8_t stage[DW][16 * DSEG / 2];   // a wave's weights
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, kb = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int hb = (int)blockIdx.x - a.row_blocks * a.ksplits;
-  if (hb >= 0) {
-    decode_h(a, hb, reinterpret_cast<float (*)[256]>(&xq[0][0]));
-    return;
-  }
   const int rb = (int)blockIdx.x % a.row_blocks, ks = (int)blockIdx.x / a.row_blocks;
   const int seg = wave & (a.nk - 1), rg = wave / a.nk, ng = DW / a.nk;
   const int64_t k0 = ((int64_t)ks * a.nk + seg) * DSEG;
   const int64_t pitch = 128 * a.C;
   const int64_t n0 = ((int64_t)rb * ng + rg) * (16 * G);     // first row of the wave
-  const int subs = (int)min((int64_t)DSUB, max((int64_t)0, (256 * a.C - k0) / 128));   // sub-steps that exist (even)
+  const int bytes = (int)min((int64_t)DSEG / 2, max((int64_t)0, pitch - k0 / 2));   // of the segment that exist
 
-  // Weights: row n0 + 16 g + l16, piece 4 i + kb of the segment.
+  // X^: row l16, piece 4 i + kb of the segment; zero past the row or the rows.
+  const rsrc_t rx = make_rsrc_u(a.xc, a.M * pitch);
+  u32x4 xv[DSUB];
+  u32x2 xe[DSUB / 2];
+#pragma unroll
+  for (int i = 0; i < DSUB; ++i)
+    xv[i] = __builtin_amdgcn_raw_buffer_load_b128(
+        rx, l16 < a.M && 64 * i < bytes ? (uint32_t)(l16 * pitch + k0 / 2 + 64 * i + 16 * kb) : kOutOfRange, 0, 0);
+  const rsrc_t rxs = make_rsrc_u(a.xs, a.C * a.M * 8);
+#pragma unroll
+  for (int i = 0; i < DSUB / 2; ++i)
+    xe[i] = __builtin_amdgcn_raw_buffer_load_b64(
+        rxs, l16 < a.M && 128 * i < bytes ? (uint32_t)(((k0 / 256 + i) * a.M + l16) * 8) : kOutOfRange, 0, 0);
+
+  // Weights: direct load t of a group brings rows 2 t and 2 t + 1 (slot lane % 32
+  // of row 2 t + lane / 32: piece slot ^ row).  Out-of-range lanes bring zeros.
   const rsrc_t rw = make_rsrc_u(a.wc + n0 * pitch + k0 / 2, (a.N - n0) * pitch - k0 / 2);
-  uint32_t wv[2][DSUB][4];
-  u32x2 wsv[2][DSUB / 2];
-  auto load_w = [&](int buf, int g) {
-    const bool in = n0 + 16 * g + l16 < a.N;
+  const rsrc_t rs = make_rsrc_u(a.ws, a.C * a.N * 8);
+  const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(stage[wave]));
+  u32x2 we[DSUB / 2];
+  auto load_w = [&](int g) {
 #pragma unroll
-    for (int i = 0; i < DSUB; ++i) {
-      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
-          rw, in && i < subs ? (uint32_t)((16 * g + l16) * pitch + 64 * i + 16 * kb) : kOutOfRange, 0, 0);
-      wv[buf][i][0] = v.x; wv[buf][i][1] = v.y; wv[buf][i][2] = v.z; wv[buf][i][3] = v.w;
+    for (int t = 0; t < 8; ++t) {
+      const int row = 2 * t + (lane >> 5), piece = (lane & 31) ^ row;
+      const bool in = n0 + 16 * g + row < a.N && 16 * piece < bytes;
+      load_lds16(rw, lds + 1024 * t, in ? (uint32_t)((16 * g + row) * pitch + 16 * piece) : kOutOfRange, 0);
     }
 #pragma unroll
-    for (int i = 0; i < DSUB / 2; ++i) {
-      const int64_t c = k0 / 256 + i;
-      const rsrc_t rs = make_rsrc_u(a.ws + (c < a.C ? c * a.N * 8 : 0), c < a.C ? a.N * 8 : 0);
-      wsv[buf][i] = __builtin_amdgcn_raw_buffer_load_b64(rs, in ? (uint32_t)((n0 + 16 * g + l16) * 8) : kOutOfRange, 0, 0);
-    }
+    for (int i = 0; i < DSUB / 2; ++i)
+      we[i] = __builtin_amdgcn_raw_buffer_load_b64(
+          rs, n0 + 16 * g + l16 < a.N && 128 * i < bytes ? (uint32_t)(((k0 / 256 + i) * a.N + n0 + 16 * g + l16) * 8) : kOutOfRange,
+          0, 0);
   };
-  load_w(0, 0);
-
-  // X^ of the wave's segment: lane t takes block t & 31 of rows t >> 5, + 2, ...
-  {
-    const int b = lane & 31;
-    const int64_t k = k0 + 32 * b;
-    for (int m = lane >> 5; m < (int)a.M; m += 2) {
-      u32x4 v[4];
-      const rsrc_t rx = make_rsrc_u(a.X, a.M * a.K * 2);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        v[q] = __builtin_amdgcn_raw_buffer_load_b128(rx, k < a.K ? (uint32_t)((m * a.K + k + 8 * q) * 2) : kOutOfRange, 0, 0);
-      uint32_t am = 0;
-      uint32_t c[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const u32x4 u[1] = {v[q]};
-        am = max(am, unit_amax<true>(u));
-      }
-      const uint32_t byte = scale_byte<true>(am);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const u32x4 u[1] = {v[q]};
-        c[q] = unit_codes<true>(u, byte);
-      }
-      *reinterpret_cast<u32x4 *>(&xq[wave][(m * 32 + b) * 16]) = u32x4{c[0], c[1], c[2], c[3]};
-      xe[wave][m * 32 + (b & 3) * 8 + (b >> 2)] = (uint8_t)byte;
-    }
-  }
-  __builtin_amdgcn_wave_barrier();
-  // Fragments: row l16 (rows at or beyond M hold whatever LDS held: their
-  // products land in columns of the result that are never stored).
-  i32x8 xf[DSUB];
-#pragma unroll
-  for (int i = 0; i < DSUB; ++i) {
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(&xq[wave][(l16 * 32 + 4 * i + kb) * 16]);
-    xf[i] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-  }
-  const u32x2 xsc = *reinterpret_cast<const u32x2 *>(&xe[wave][l16 * 32 + kb * 8]);
+  load_w(0);
 
   f32x4 acc[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    if (g + 1 < G) load_w((g + 1) & 1, g + 1);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's direct loads have landed
+    asm volatile("" ::: "memory");
+    i32x8 wf[DSUB];
+#pragma unroll
+    for (int i = 0; i < DSUB; ++i) {
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(&stage[wave][l16 * 512 + 16 * ((4 * i + kb) ^ l16)]);
+      wf[i] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+    }
+    uint32_t sw[DSUB];
+#pragma unroll
+    for (int i = 0; i < DSUB; ++i) sw[i] = ((i & 1) ? we[i >> 1].y : we[i >> 1].x) >> (8 * kb);
+    if (g + 1 < G) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the fragments are read before LDS is refilled
+      load_w(g + 1);
+    }
     acc[g] = zero4();
-    auto sub = [&](auto I) {
-      constexpr int i = decltype(I)::value;
-      const uint32_t(&w)[4] = wv[g & 1][i];
-      const i32x8 wf = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-      const uint32_t sw = ((i & 1) ? wsv[g & 1][i >> 1].y : wsv[g & 1][i >> 1].x) >> (8 * kb);
-      const uint32_t sx = (i < 4) ? xsc.x : xsc.y;
-      // Sub-steps past the segment's end hold zero codes under scale byte 0,
-      // and X^ there was quantised from zeros.
-      acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[i], acc[g], 4, 4, 0, (int)sw, i & 3, (int)sx);
-    };
-    sub(std::integral_constant<int, 0>{}); sub(std::integral_constant<int, 1>{});
-    sub(std::integral_constant<int, 2>{}); sub(std::integral_constant<int, 3>{});
-    sub(std::integral_constant<int, 4>{}); sub(std::integral_constant<int, 5>{});
-    sub(std::integral_constant<int, 6>{}); sub(std::integral_constant<int, 7>{});
+#pragma unroll
+    for (int i = 0; i < DSUB; ++i) {
+      const i32x8 xf = {(int)xv[i].x, (int)xv[i].y, (int)xv[i].z, (int)xv[i].w, 0, 0, 0, 0};
+      const uint32_t sx = ((i & 1) ? xe[i >> 1].y : xe[i >> 1].x) >> (8 * kb);
+      acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf, acc[g], 4, 4, 0, (int)sw[i], 0, (int)sx);
+    }
   }
   // acc[g][e]: weight row 16 g + 4 kb + e, row l16 of X.
+  if (a.out && a.ad.hp && seg == 0) {
+    const int64_t mc = min((int64_t)l16, a.M - 1);
+#pragma unroll 1
+    for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32) {
+      const HPieces h = load_h(a.ad, a.M, mc, j0, a.ad.H_out && rb == 0 && rg == 0 && l16 < a.M);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        acc[g] = add_adapter(acc[g], load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0), h);
+    }
+  }
+  // Partial sums [G * 256] in place of the wave's own stage.
+  static_assert(G * 1024 <= 16 * DSEG / 2, "partial sums fit");
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) red(wave)[g * 256 + l16 * 16 + 4 * kb + e] = acc[g][e];
+    for (int e = 0; e < 4; ++e) reinterpret_cast<float *>(stage[wave])[g * 256 + l16 * 16 + 4 * kb + e] = acc[g][e];
   __syncthreads();
-  // Element idx of a row group set: (group set q, g, m, row in 16).
+  // Element idx of a row group set: (set q, group, row of X, row in 16).
   for (int idx = tid; idx < ng * G * 256; idx += 64 * DW) {
     const int q = idx / (G * 256), in = idx % (G * 256);
     float v = 0.0f;
-    for (int w = 0; w < a.nk; ++w) v += red(q * a.nk + w)[in];
+    for (int w = 0; w < a.nk; ++w) v += reinterpret_cast<const float *>(stage[q * a.nk + w])[in];
     const int64_t n = ((int64_t)rb * ng + q) * (16 * G) + 16 * (in >> 8) + (in & 15);
     const int m = (in >> 4) & 15;
     if (m < a.M && n < a.N) {
@@ -652,58 +747,42 @@ __global__ __launch_bounds__(64 * DW) void mx_decode_kernel(MxDecodeArgs a) {
   }
 }
 
-// Y = sum of the partial products + s H B^T, H = c * (sum of its partials);
-// also writes H.  A workgroup owns 64 columns and 16 rows; thread t column
-// t & 63, rows (t >> 6) + 4 i.  H stays in fp32.
+// Y = sum of the partial products + s H B^T; also writes H.  A wave owns 16
+// columns x 16 rows of Y and needs no LDS; a lane ends with four consecutive
+// columns of one row: 16-byte reads of the partial products, one 8-byte store.
 struct MxFinishArgs {
   const float *part;   // [splits][M][N]
   int splits;
-  const float *hp;     // [hsplits][M][ldh] unscaled, or null
-  int hsplits, ldh;
-  int64_t M, N, r;
-  const uint16_t *B;
-  float s, c;
+  AdapterArgs ad;
+  int64_t M, N;
   uint16_t *out;
-  float *H_out;
 };
 
 __global__ __launch_bounds__(256) void mx_finish_kernel(MxFinishArgs a) {
-  __shared__ float h[16][65];
-  __shared__ float bt[64][65];
-  const int tid = threadIdx.x;
-  const int64_t m0 = (int64_t)blockIdx.y * 16, n = (int64_t)blockIdx.x * 64 + (tid & 63);
-  float v[4];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, kb = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16, m = (int64_t)blockIdx.y * 16 + l16;
+  const bool in = m < a.M;
+  const int64_t mc = in ? m : a.M - 1;   // lanes past the rows read the last one
+  f32x4 acc = zero4();
+  for (int q0 = 0; q0 < a.splits; q0 += 4) {
+    f32x4 v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = 0.0f;
-  for (int s = 0; s < a.splits; ++s)
+    for (int q = 0; q < 4; ++q)
+      v[q] = *reinterpret_cast<const f32x4 *>(a.part + ((int64_t)min(q0 + q, a.splits - 1) * a.M + mc) * a.N + n0 + 4 * kb);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + (tid >> 6) + 4 * i;
-      if (m < a.M) v[i] += a.part[((int64_t)s * a.M + m) * a.N + n];
-    }
-  if (a.hp) {
-    for (int i = tid; i < 16 * 64; i += 256) {
-      const int64_t m = m0 + (i >> 6);
-      const int j = i & 63;
-      float x = 0.0f;
-      if (m < a.M && j < a.r)
-        for (int s = 0; s < a.hsplits; ++s) x += a.hp[((int64_t)s * a.M + m) * a.ldh + j];
-      x *= a.c;
-      h[i >> 6][j] = x;
-      if (a.H_out && blockIdx.x == 0 && m < a.M && j < a.r) a.H_out[m * a.r + j] = x;
-    }
-    const int r = (int)a.r;
-    for (int i = tid; i < 64 * r; i += 256) bt[i / r][i % r] = bf16_to_f32(a.B[(int64_t)blockIdx.x * 64 * r + i]);
-    __syncthreads();
-    for (int j = 0; j < r; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += (a.s * h[(tid >> 6) + 4 * i][j]) * bt[tid & 63][j];
+    for (int q = 0; q < 4; ++q)
+      if (q0 + q < a.splits) acc += v[q];
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + (tid >> 6) + 4 * i;
-    if (m < a.M) a.out[m * a.N + n] = f32_to_bf16(v[i]);
-  }
+  if (a.ad.hp)
+    for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32) {
+      const bf16x8 b = load_b(a.ad, n0 + l16, j0);
+      acc = add_adapter(acc, b, load_h(a.ad, a.M, mc, j0, a.ad.H_out && blockIdx.x == 0 && wave == 0 && in));
+    }
+  // acc[e]: column n0 + 4 kb + e, row m.
+  if (in)
+    *reinterpret_cast<u32x2 *>(a.out + m * a.N + n0 + 4 * kb) =
+        u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
 }
 
 // ------------------------------------------------------------------ plans
@@ -722,21 +801,21 @@ struct Carve {
 constexpr int64_t kDecodeRows = 16;
 
 struct DecodePlan {
-  int nk, ksplits, row_blocks, hsplits, hblocks, groups;
+  int nk, ksplits, row_blocks, hsplits, groups;
 };
-DecodePlan decode_plan(int64_t N, int64_t K, int64_t r) {
+DecodePlan decode_plan(int64_t N, int64_t K) {
   DecodePlan p;
   const int64_t segs = cdiv(K, DSEG);
   p.nk = 1;
   while (p.nk < DW && p.nk < segs) p.nk *= 2;
   p.ksplits = (int)cdiv(segs, p.nk);
-  // Row groups per wave: one while that leaves workgroups waiting for few
-  // rounds, then two or four (X^ is quantised once per wave, whatever it owns).
+  // Row groups per wave: one while the workgroups are resident at once (two to
+  // a CU), then two or four, which keeps them resident for longer weights and
+  // lets a wave ask for its next rows before it is done with these.
   const int64_t wgs = cdiv(N, 16 * (DW / p.nk)) * p.ksplits;
   p.groups = wgs <= 2 * device_cus() ? 1 : (wgs <= 4 * device_cus() ? 2 : 4);
   p.row_blocks = (int)cdiv(N, (int64_t)16 * p.groups * (DW / p.nk));
   p.hsplits = (int)cdiv(K, DW * HSEG);
-  p.hblocks = r ? (int)cdiv(r, 16) * p.hsplits : 0;
   return p;
 }
 
@@ -754,32 +833,29 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t C) {
 }
 
 struct FwdPieces {
-  float *y_part, *h_part;                // decode, or the split tiles
-  uint8_t *xc, *xs;                      // X^
-  uint16_t *sH;
-  float *hf, *lr_part;
+  uint8_t *xc, *xs;        // X^
+  float *y_part;           // partial products (decode beyond one workgroup's columns, split tiles)
+  float *h_part;           // partial sums of H (decode: [hsplits][M][64]; tiles: the low-rank kernel's)
+  uint16_t *sH;            // bf16 s H (tiles that finish Y themselves)
   size_t bytes;
 };
 FwdPieces fwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r) {
   FwdPieces p{};
   Carve c(ws);
+  const int64_t C = mx_chunks(K);
+  p.xc = c.take<uint8_t>(M * 128 * C);
+  p.xs = c.take<uint8_t>(M * 8 * C);
   if (M <= kDecodeRows) {
-    const DecodePlan d = decode_plan(N, K, r);
-    p.y_part = c.take<float>((int64_t)d.ksplits * M * N);
+    const DecodePlan d = decode_plan(N, K);
+    if (d.ksplits > 1) p.y_part = c.take<float>((int64_t)d.ksplits * M * N);
     if (r) p.h_part = c.take<float>((int64_t)d.hsplits * M * 64);
   } else {
-    const int64_t C = mx_chunks(K);
     const GemmPlan g = gemm_plan(M, N, C);
-    p.xc = c.take<uint8_t>(M * 128 * C);
-    p.xs = c.take<uint8_t>(M * 8 * C);
     if (g.splits > 1) p.y_part = c.take<float>((int64_t)g.splits * M * N);
-    if (r) {
-      if (g.splits > 1) p.hf = c.take<float>(M * r);
-      else p.sH = c.take<uint16_t>(M * 64);
-      p.lr_part = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
-    }
+    if (r) p.h_part = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
+    if (r && g.splits == 1) p.sH = c.take<uint16_t>(M * 64);
   }
-  p.bytes = std::max<size_t>(c.off, 256);
+  p.bytes = c.off;
   return p;
 }
 
@@ -800,17 +876,28 @@ hipError_t launch_tiles(MxGemmArgs g, hipStream_t st) {
 }
 
 hipError_t launch_finish(const MxFinishArgs &f, hipStream_t st) {
-  const dim3 grid((unsigned)(f.N / 64), (unsigned)cdiv(f.M, 16));
+  const dim3 grid((unsigned)(f.N / 64), (unsigned)cdiv(f.M, 16));   // N % 64 == 0
   hipLaunchKernelGGL(mx_finish_kernel, grid, dim3(256), 0, st, f);
   return hipGetLastError();
 }
 
 hipError_t run_decode(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
-  const DecodePlan p = decode_plan(a.N, a.K, a.r);
-  const bool direct = a.r == 0 && p.ksplits == 1;
-  MxDecodeArgs d{a.X, a.M, a.N, a.K, mx_chunks(a.K), a.codes, a.scales, a.A, a.r, a.drop, w.y_part, w.h_part,
-                 direct ? a.Y : nullptr, p.nk, p.ksplits, p.row_blocks, p.hsplits, p.groups};
-  const dim3 grid((unsigned)(p.row_blocks * p.ksplits + p.hblocks)), block(64 * DW);
+  const DecodePlan p = decode_plan(a.N, a.K);
+  const int64_t C = mx_chunks(a.K);
+  const dim3 block(64 * DW);
+  {
+    const uint32_t chunks = (uint32_t)(a.M * C);
+    const int qblocks = (int)cdiv(chunks, 64 * DW / 32);
+    const int hblocks = a.r ? (int)cdiv(a.r, 16) * p.hsplits : 0;
+    const MxPrepArgs q{a.X, a.M, a.K, fast_div((uint32_t)C), chunks, w.xc, w.xs, qblocks, a.A, a.r, a.drop,
+                       w.h_part, p.hsplits};
+    hipLaunchKernelGGL(mx_prep_kernel, dim3((unsigned)(qblocks + hblocks)), block, 0, st, q);
+    QN_TRY(hipGetLastError());
+  }
+  const AdapterArgs ad{a.r ? w.h_part : nullptr, p.hsplits, 64, a.B, a.r, a.s, a.drop.c, a.H_out};
+  const MxDecodeArgs d{w.xc, w.xs, a.M, a.N, C, a.codes, a.scales, ad, p.ksplits == 1 ? a.Y : nullptr, w.y_part,
+                       p.nk, p.row_blocks};
+  const dim3 grid((unsigned)(p.row_blocks * p.ksplits));
   {
     TraceScope tr(QN_TRACE_MX_GEMV, st);
     if (p.groups == 1) hipLaunchKernelGGL(mx_decode_kernel<1>, grid, block, 0, st, d);
@@ -818,9 +905,8 @@ hipError_t run_decode(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
     else hipLaunchKernelGGL(mx_decode_kernel<4>, grid, block, 0, st, d);
   }
   QN_TRY(hipGetLastError());
-  if (direct) return hipSuccess;
-  return launch_finish(MxFinishArgs{w.y_part, p.ksplits, a.r ? w.h_part : nullptr, p.hsplits, 64, a.M, a.N, a.r, a.B,
-                                    a.s, a.drop.c, a.Y, a.H_out}, st);
+  if (p.ksplits == 1) return hipSuccess;
+  return launch_finish(MxFinishArgs{w.y_part, p.ksplits, ad, a.M, a.N, a.Y}, st);
 }
 
 template <bool Q>
@@ -874,24 +960,21 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
     LowRankArgs l{};
     l.L = a.X; l.ldl = a.K; l.M = a.M; l.Kc = a.K;
     l.P = a.A; l.ldp = a.K; l.R = a.r; l.scale = a.s; l.drop = a.drop;
-    l.Mp = a.M; l.part = w.lr_part;
-    if (p.splits > 1) {
-      l.out_f32 = a.H_out ? a.H_out : w.hf;
-    } else {
-      l.out_f32 = a.H_out;
-      l.out_b = w.sH;
-      l.ldb = 64;
-    }
-    QN_TRY(launch_lowrank(l, st));
+    l.Mp = a.M; l.part = w.h_part;
+    l.out_f32 = a.H_out;
+    l.out_b = w.sH;
+    l.ldb = 64;
+    // Split tiles end in a finishing kernel, which adds H's partial sums itself.
+    QN_TRY(p.splits > 1 ? launch_lowrank_part(l, st) : launch_lowrank(l, st));
   }
   MxGemmArgs g{w.xc, w.xs, a.codes, a.scales, a.M, a.N, C, a.r ? w.sH : nullptr, a.B, a.r, a.Y, w.y_part,
                0, 0, 0, p.splits};
   if (p.bm == 256) return launch_tiles<2, 4, 4, 2, false>(g, st);
   if (p.splits == 1) return launch_tiles<2, 2, 2, 2, false>(g, st);
   QN_TRY((launch_tiles<2, 2, 2, 2, true>(g, st)));
-  // The low-rank product's H already carries the dropout's factor.
-  return launch_finish(MxFinishArgs{w.y_part, p.splits, a.r ? (a.H_out ? a.H_out : w.hf) : nullptr, 1, (int)a.r, a.M,
-                                    a.N, a.r, a.B, a.s, 1.0f, a.Y, nullptr}, st);
+  const AdapterArgs ad{a.r ? w.h_part : nullptr, lowrank_splits(a.M, a.K), (int)align_up(a.r, 32), a.B, a.r, a.s,
+                       a.drop.c, a.H_out};
+  return launch_finish(MxFinishArgs{w.y_part, p.splits, ad, a.M, a.N, a.Y}, st);
 }
 
 }  // namespace qn

@@ -547,19 +547,34 @@ def qlora_linear_bwd(dY, X, w: NF4Weight, A, B, alpha, want_dX=True, use_double_
 
 
 # ------------------------------------------------- dropout and the MXFP4 base
-def _one_device(*tensors):
-    """The one GPU all given tensors (None skipped) lie on."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop()
+def _operand(t, name, dtype, shape=None):
+    """Check a GPU operand (type, contiguity, shape); its address.  The quick test
+    comes first: these calls are short, and a full report is made only to raise."""
+    if not (getattr(t, "is_cuda", False) and t.dtype == dtype and t.is_contiguous()):
+        _need(t, name, dtype)
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
-def _launch(device, fn, *args):
-    """Call fn(*args, stream) with the tensors' device current, on its current stream."""
+def _launch(tensors, fn, *args):
+    """Call fn(*args, stream) on the current stream of the one GPU that all the
+    tensors (None skipped) lie on."""
     torch = _torch()
-    with torch.cuda.device(device):
-        _check(fn, getattr(load(), fn)(*args, _stream()))
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if dev is None:
+                dev = d
+            elif d != dev:
+                raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
+    call = getattr(_lib or load(), fn)
+    if dev == torch.cuda.current_device():
+        _check(fn, call(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, call(*args, torch.cuda.current_stream(dev).cuda_stream))
 
 
 @dataclass
@@ -574,24 +589,20 @@ class Dropout:
     offset_dev: Optional[object] = None
 
     def struct(self):
-        torch = _torch()
-        for name in ("seed", "offset"):
-            if not 0 <= int(getattr(self, name)) < 1 << 64:
-                raise ValueError(f"{name} must be in [0, 2^64)")
+        seed, offset, dev = int(self.seed), int(self.offset), 0
+        if not 0 <= seed < 1 << 64:
+            raise ValueError("seed must be in [0, 2^64)")
+        if not 0 <= offset < 1 << 64:
+            raise ValueError("offset must be in [0, 2^64)")
         if self.offset_dev is not None:
-            _need(self.offset_dev, "offset_dev", torch.int64)
+            dev = _operand(self.offset_dev, "offset_dev", _torch().int64)
             if self.offset_dev.numel() != 1:
                 raise ValueError("offset_dev must hold one element")
-        return DropoutStruct(float(self.p), int(self.seed), int(self.offset),
-                             self.offset_dev.data_ptr() if self.offset_dev is not None else 0)
+        return DropoutStruct(float(self.p), seed, offset, dev)
 
 
 def _drop_ref(drop):
     return ctypes.byref(drop.struct()) if drop is not None else None
-
-
-def _drop_dev(drop):
-    return drop.offset_dev if drop is not None else None
 
 
 def dropout(x, drop: Dropout, out=None):
@@ -599,17 +610,21 @@ def dropout(x, drop: Dropout, out=None):
     ``x``.  Applied to a gradient with the same ``drop`` it is the backward."""
     torch = _torch()
     _need(x, "x")
-    if x.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("x must be float32 or bfloat16")
+    dt = _codec_type(x, "x")
     if out is None:
         out = torch.empty_like(x)
-    _need(out, "out", x.dtype)
-    if out.shape != x.shape:
-        raise ValueError("out must have x's shape")
-    dev = _one_device(x, out, drop.offset_dev)
-    dt = QN_BF16 if x.dtype == torch.bfloat16 else QN_F32
-    _launch(dev, "qn_dropout", _ptr(x), dt, x.numel(), _drop_ref(drop), _ptr(out))
+    po = _operand(out, "out", x.dtype, tuple(x.shape))
+    _launch((x, out, drop.offset_dev), "qn_dropout", x.data_ptr(), dt, x.numel(), _drop_ref(drop), po)
     return out
+
+
+def _codec_type(t, name):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return QN_BF16
+    if t.dtype == torch.float32:
+        return QN_F32
+    raise ValueError(f"{name} must be float32 or bfloat16")
 
 
 @dataclass
@@ -637,30 +652,23 @@ class MXMatrix:
         return self.cols
 
     def struct(self):
-        torch = _torch()
-        _need(self.codes, "codes", torch.uint8)
-        _need(self.scales, "scales", torch.uint8)
+        u8 = _torch().uint8
         C = -(-self.cols // QN_MX_CHUNK)
-        if self.codes.numel() != self.rows * 128 * C or self.scales.numel() != self.rows * 8 * C:
-            raise ValueError("codes must be [rows, 128 C] and scales [C, rows, 8] with C = ceil(cols / 256)")
-        return MXMatrixStruct(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+        return MXMatrixStruct(_operand(self.codes, "codes", u8, (self.rows, 128 * C)),
+                              _operand(self.scales, "scales", u8, (C, self.rows, 8)), self.rows, self.cols)
 
 
 def mxfp4_quantize(X, out: Optional[MXMatrix] = None):
     """qn_mxfp4_quantize of a 2-D fp32 or bf16 device tensor -> MXMatrix."""
-    torch = _torch()
     _need(X, "X", ndim=2)
-    if X.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("X must be float32 or bfloat16")
+    dt = _codec_type(X, "X")
     rows, cols = X.shape
     if out is None:
         out = MXMatrix.empty(rows, cols, X.device)
     if (out.rows, out.cols) != (rows, cols):
         raise ValueError("out must have X's shape")
     st = out.struct()
-    dev = _one_device(X, out.codes, out.scales)
-    dt = QN_BF16 if X.dtype == torch.bfloat16 else QN_F32
-    _launch(dev, "qn_mxfp4_quantize", _ptr(X), dt, rows, cols, _ptr(out.codes), _ptr(out.scales))
+    _launch((X, out.codes, out.scales), "qn_mxfp4_quantize", X.data_ptr(), dt, rows, cols, st.codes, st.scales)
     return out
 
 
@@ -668,16 +676,13 @@ def mxfp4_dequant(w: MXMatrix, out_dtype="bf16", out=None):
     """The values an MXMatrix stands for, [rows, cols] bf16 (or fp32); a given
     ``out`` decides the type."""
     torch = _torch()
-    types = {"bf16": torch.bfloat16, "f32": torch.float32}
-    if out is None:
-        out = torch.empty((w.rows, w.cols), dtype=types[out_dtype], device=w.codes.device)
-    _need(out, "out", ndim=2)
-    if out.dtype not in types.values() or tuple(out.shape) != (w.rows, w.cols):
-        raise ValueError("out must be a float32 or bfloat16 [rows, cols] tensor")
     st = w.struct()
-    dev = _one_device(w.codes, w.scales, out)
-    dt = QN_BF16 if out.dtype == torch.bfloat16 else QN_F32
-    _launch(dev, "qn_mxfp4_dequant", ctypes.byref(st), _ptr(out), dt)
+    if out is None:
+        out = torch.empty((w.rows, w.cols), dtype={"bf16": torch.bfloat16, "f32": torch.float32}[out_dtype],
+                          device=w.codes.device)
+    dt = _codec_type(out, "out")
+    po = _operand(out, "out", out.dtype, (w.rows, w.cols))
+    _launch((w.codes, w.scales, out), "qn_mxfp4_dequant", ctypes.byref(st), po, dt)
     return out
 
 
@@ -694,56 +699,58 @@ def mx_workspace(op, M, N, K, r, device="cuda"):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _linear_args(X, w, A, B, H, other=None, other_name=None):
-    """Check a linear's operands; (M, K, r).  A and B are both None for r = 0."""
-    torch = _torch()
-    _need(X, "X", torch.bfloat16, 2)
+def _addr(t):
+    return t.data_ptr() if t is not None else 0
+
+
+def _linear_args(X, w, A, B, H, other, name):
+    """Check a linear's operands; (M, r).  A and B are both None for r = 0."""
+    bf = _torch().bfloat16
+    _need(X, "X", bf, 2)
     M, K = X.shape
+    if K != w.K:
+        raise ValueError("X must be [M, K]")
     if (A is None) != (B is None):
         raise ValueError("A and B go together")
     r = 0
     if A is not None:
-        _need(A, "A", torch.bfloat16, 2)
-        _need(B, "B", torch.bfloat16, 2)
         r = A.shape[0]
-        if A.shape[1] != w.K or tuple(B.shape) != (w.N, r):
-            raise ValueError("A must be [r, K] and B [N, r]")
-    if K != w.K:
-        raise ValueError("X must be [M, K]")
+        _operand(A, "A", bf, (r, K))
+        _operand(B, "B", bf, (w.N, r))
     if other is not None:
-        _need(other, other_name, torch.bfloat16, 2)
-        if tuple(other.shape) != (M, w.N):
-            raise ValueError(f"{other_name} must be [M, N]")
+        _operand(other, name, bf, (M, w.N))
     if H is not None:
         if r == 0:
             raise ValueError("H needs an adapter")
-        _need(H, "H", torch.float32, 2)
-        if tuple(H.shape) != (M, r):
-            raise ValueError("H must be [M, r]")
-    return int(M), int(K), int(r)
+        _operand(H, "H", _torch().float32, (M, r))
+    return int(M), int(r)
 
 
-def _need_ws(ws):
+def _outputs(X, w, M, r, Y, H, want_H):
+    """A forward's (Y, H), allocated where not given; H None unless wanted."""
     torch = _torch()
-    _need(ws, "ws", torch.uint8, 1)
+    if Y is None:
+        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
+    if want_H and H is None:
+        if r == 0:
+            raise ValueError("H needs an adapter")
+        H = torch.empty((M, r), dtype=torch.float32, device=X.device)
+    return Y, H
 
 
-def _grads(out, want_dX, M, N, K, r, device):
+def _grads(out, want_dX, X, w, M, r):
     """The gradients' tensors (dX, dA, dB), checked or allocated."""
     torch = _torch()
-    shapes = ((M, K), (r, K), (N, r))
+    bf = torch.bfloat16
+    shapes = ((M, w.K), (r, w.K), (w.N, r))
     if out is None:
-        bf = dict(dtype=torch.bfloat16, device=device)
-        dX = torch.empty(shapes[0], **bf) if want_dX else None
-        return (dX,) + ((torch.empty(shapes[1], **bf), torch.empty(shapes[2], **bf)) if r else (None, None))
+        new = [torch.empty(s, dtype=bf, device=X.device) for s in shapes[:3 if r else 1]]
+        return (new[0] if want_dX else None,) + (tuple(new[1:]) if r else (None, None))
     for t, name, shape in zip(out, ("dX", "dA", "dB"), shapes):
-        if t is None:
-            if name == "dX" or r == 0:
-                continue
+        if t is not None:
+            _operand(t, name, bf, shape)
+        elif name != "dX" and r:
             raise ValueError(f"{name} is required")
-        _need(t, name, torch.bfloat16, 2)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}")
     return tuple(out)
 
 
@@ -752,23 +759,18 @@ def qlora_linear_fwd_dropout(X, w: NF4Weight, A, B, alpha, drop: Dropout, want_H
     """qlora_linear_fwd with dropout on the adapter's input: H = c (keep * X) A^T,
     Y = X bf16(dequant(W))^T + (alpha/r) H B^T.  The workspace is
     ``workspace(QN_OP_FWD_DROPOUT, ...)``."""
-    torch = _torch()
     if A is None or B is None:
         raise ValueError("A and B are required")
-    M, K, r = _linear_args(X, w, A, B, H, Y, "Y")
-    if Y is None:
-        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
-    want_H = want_H or H is not None
-    if want_H and H is None:
-        H = torch.empty((M, r), dtype=torch.float32, device=X.device)
+    M, r = _linear_args(X, w, A, B, H, Y, "Y")
+    Y, H = _outputs(X, w, M, r, Y, H, want_H)
     if ws is None:
         ws = workspace(QN_OP_FWD_DROPOUT, M, w.N, w.K, r, X.device)
-    _need_ws(ws)
+    pw = _operand(ws, "ws", _torch().uint8)
     st = w.struct(use_double_quant)
-    dev = _one_device(X, A, B, Y, H, ws, w.codes, w.absmax, w.absmax_q, w.scale2, _drop_dev(drop))
-    _launch(dev, "qlora_linear_fwd_dropout", _ptr(X), M, ctypes.byref(st), _ptr(A), _ptr(B), r, float(alpha),
-            _drop_ref(drop), _ptr(Y), _ptr(H), _ptr(ws), ws.numel())
-    return (Y, H) if want_H else Y
+    _launch((X, A, B, Y, H, ws, w.codes, w.absmax, w.absmax_q, w.scale2, drop.offset_dev),
+            "qlora_linear_fwd_dropout", X.data_ptr(), M, ctypes.byref(st), A.data_ptr(), B.data_ptr(), r, float(alpha),
+            _drop_ref(drop), Y.data_ptr(), _addr(H), pw, ws.numel())
+    return Y if H is None else (Y, H)
 
 
 def qlora_linear_bwd_dropout(dY, X, w: NF4Weight, A, B, alpha, drop: Dropout, want_dX=True, use_double_quant=True,
@@ -777,15 +779,17 @@ def qlora_linear_bwd_dropout(dY, X, w: NF4Weight, A, B, alpha, drop: Dropout, wa
     (dropped) one that forward returned, or None to form it again."""
     if A is None or B is None:
         raise ValueError("A and B are required")
-    M, K, r = _linear_args(X, w, A, B, H, dY, "dY")
-    dX, dA, dB = _grads(out, want_dX, M, w.N, K, r, X.device)
+    if dY is None:
+        raise ValueError("dY is required")
+    M, r = _linear_args(X, w, A, B, H, dY, "dY")
+    dX, dA, dB = _grads(out, want_dX, X, w, M, r)
     if ws is None:
         ws = workspace(QN_OP_BWD, M, w.N, w.K, r, X.device)
-    _need_ws(ws)
+    pw = _operand(ws, "ws", _torch().uint8)
     st = w.struct(use_double_quant)
-    dev = _one_device(dY, X, A, B, H, ws, dX, dA, dB, w.codes, w.absmax, w.absmax_q, w.scale2, _drop_dev(drop))
-    _launch(dev, "qlora_linear_bwd_dropout", _ptr(dY), _ptr(X), _ptr(H), M, ctypes.byref(st), _ptr(A), _ptr(B), r,
-            float(alpha), _drop_ref(drop), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())
+    _launch((dY, X, A, B, H, ws, dX, dA, dB, w.codes, w.absmax, w.absmax_q, w.scale2, drop.offset_dev),
+            "qlora_linear_bwd_dropout", dY.data_ptr(), X.data_ptr(), _addr(H), M, ctypes.byref(st), A.data_ptr(),
+            B.data_ptr(), r, float(alpha), _drop_ref(drop), _addr(dX), dA.data_ptr(), dB.data_ptr(), pw, ws.numel())
     return dX, dA, dB
 
 
@@ -793,38 +797,33 @@ def qlora_mx_linear_fwd(X, w: MXMatrix, A=None, B=None, alpha=0.0, drop: Optiona
                         Y=None, ws=None, H=None):
     """Y = mx(X) W^T + (alpha/r) H B^T over an MXFP4 base, H = c (keep * X) A^T;
     returns Y (and H).  A = B = None: the base alone."""
-    torch = _torch()
-    M, K, r = _linear_args(X, w, A, B, H, Y, "Y")
-    if Y is None:
-        Y = torch.empty((M, w.N), dtype=torch.bfloat16, device=X.device)
-    want_H = want_H or H is not None
-    if want_H and H is None:
-        if r == 0:
-            raise ValueError("H needs an adapter")
-        H = torch.empty((M, r), dtype=torch.float32, device=X.device)
+    M, r = _linear_args(X, w, A, B, H, Y, "Y")
+    Y, H = _outputs(X, w, M, r, Y, H, want_H)
     if ws is None:
         ws = mx_workspace(QN_OP_FWD, M, w.N, w.K, r, X.device)
-    _need_ws(ws)
+    pw = _operand(ws, "ws", _torch().uint8)
     st = w.struct()
-    dev = _one_device(X, A, B, Y, H, ws, w.codes, w.scales, _drop_dev(drop))
-    _launch(dev, "qlora_mx_linear_fwd", _ptr(X), M, ctypes.byref(st), _ptr(A), _ptr(B), r, float(alpha),
-            _drop_ref(drop), _ptr(Y), _ptr(H), _ptr(ws), ws.numel())
-    return (Y, H) if want_H else Y
+    _launch((X, A, B, Y, H, ws, w.codes, w.scales, drop.offset_dev if drop is not None else None),
+            "qlora_mx_linear_fwd", X.data_ptr(), M, ctypes.byref(st), _addr(A), _addr(B), r, float(alpha),
+            _drop_ref(drop), Y.data_ptr(), _addr(H), pw, ws.numel())
+    return Y if H is None else (Y, H)
 
 
 def qlora_mx_linear_bwd(dY, X, w: MXMatrix, A=None, B=None, alpha=0.0, drop: Optional[Dropout] = None, want_dX=True,
                         out=None, ws=None, H=None):
     """Backward of qlora_mx_linear_fwd: (dX or None, dA, dB); dA and dB are None
     without an adapter."""
-    M, K, r = _linear_args(X, w, A, B, H, dY, "dY")
-    dX, dA, dB = _grads(out, want_dX, M, w.N, K, r, X.device)
+    if dY is None:
+        raise ValueError("dY is required")
+    M, r = _linear_args(X, w, A, B, H, dY, "dY")
+    dX, dA, dB = _grads(out, want_dX, X, w, M, r)
     if ws is None:
         ws = mx_workspace(QN_OP_BWD, M, w.N, w.K, r, X.device)
-    _need_ws(ws)
+    pw = _operand(ws, "ws", _torch().uint8)
     st = w.struct()
-    dev = _one_device(dY, X, A, B, H, ws, dX, dA, dB, w.codes, w.scales, _drop_dev(drop))
-    _launch(dev, "qlora_mx_linear_bwd", _ptr(dY), _ptr(X), _ptr(H), M, ctypes.byref(st), _ptr(A), _ptr(B), r,
-            float(alpha), _drop_ref(drop), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())
+    _launch((dY, X, A, B, H, ws, dX, dA, dB, w.codes, w.scales, drop.offset_dev if drop is not None else None),
+            "qlora_mx_linear_bwd", dY.data_ptr(), X.data_ptr(), _addr(H), M, ctypes.byref(st), _addr(A), _addr(B), r,
+            float(alpha), _drop_ref(drop), _addr(dX), _addr(dA), _addr(dB), pw, ws.numel())
     return dX, dA, dB
 
 
