@@ -1,0 +1,234 @@
+// Column sums over rows on the matrix cores (gfx950): out[j][c] = sum_m Lt[j][m] *
+// Q[m][c] for j < R <= 64, the contraction of dA = dH^T (keep * X) and dB^T = (s
+// H)^T dY, which runs down the rows of row-major activations.  Lt is [rows, Mp]
+// bf16, zero beyond R and M.
+//
+// Bound by reading Q once (4096 x 8192 bf16: 64 MiB); the products are 64 MACs
+// per element of Q, too many for vector dot products (the v_dot2 kernel of
+// k_lowrank.hip takes 150 us for the two sums at R = 64) and little for the
+// matrix cores.  The MFMA wants eight consecutive rows of one column, so a
+// 64-row x 256-column stage of Q goes through LDS as it lies and comes back by
+// the transposing read (ds_read_b64_tr_b16), as in k_mxdx.hip.  The stage is
+// filled through registers, not by direct loads: a 16-byte piece there is one
+// call of the dropout generator, so the mask is applied on the way.
+//
+// A workgroup (8 waves) owns 256 columns and a range of rows; wave w multiplies
+// columns 32 w .. + 31 with all ranks.  Stage of Q: row m (512 bytes), piece u of
+// 8 columns at slot u ^ 4 (m & 3), so that a transposing read's four rows fall
+// on different banks.  Stage of Lt: 64 ranks x 64 rows (128 bytes per rank),
+// direct loads, piece k of rank j at slot k ^ ((j >> 1) & 7).  Two stages each.
+// The partial sums of the row ranges go to `part` and are added in order by
+// the reduce kernel, so results depend on the shape alone.
+
+#include <algorithm>
+
+#include "qn_philox.h"
+#include "qn_tile.h"
+
+namespace qn {
+namespace {
+
+constexpr int CS_THREADS = 512;
+constexpr int CS_COLS = 256;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+template <int RT, bool DROP>   // 32-rank tiles
+__global__ __launch_bounds__(CS_THREADS) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
+  __shared__ __attribute__((aligned(16))) uint8_t qs0[64 * 512];
+  __shared__ __attribute__((aligned(16))) uint8_t qs1[64 * 512];
+  __shared__ __attribute__((aligned(16))) uint8_t ls0[32 * RT * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t ls1[32 * RT * 128];
+  const ColSumArgs a = blockIdx.z ? a1 : a0;
+  const int64_t c0 = (int64_t)blockIdx.x * CS_COLS;
+  if (c0 >= a.Ncols) return;   // the other sum is wider
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = (int)blockIdx.y;
+  const int steps = (int)((a.M + 63) / 64);
+  const int s0 = (int)((int64_t)steps * split / a.splits), s1 = (int)((int64_t)steps * (split + 1) / a.splits);
+
+  // Q: thread t loads pieces (t & 31) of rows t / 32 + 16 i of a stage, i < 4.
+  const int qu = tid & 31, qr = tid >> 5;
+  const uint32_t qo = c0 + 8 * qu < a.Ncols ? (uint32_t)((qr * a.Ncols + c0 + 8 * qu) * 2) : kOutOfRange;
+  const uint32_t qst = (uint32_t)(qr * 512 + 16 * (qu ^ (4 * (qr & 3))));   // row qr + 16 i: + 8192 i
+  u32x4 qv[4];
+  auto load_q = [&](int s) {
+    // The resource starts at the stage's first row: offsets within 64 rows.
+    const rsrc_t rq = make_rsrc_u(a.Q + (int64_t)s * 64 * a.Ncols, (a.M - (int64_t)s * 64) * a.Ncols * 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      qv[i] = __builtin_amdgcn_raw_buffer_load_b128(
+          rq, qo == kOutOfRange ? kOutOfRange : qo + (uint32_t)(i * 32 * a.Ncols), 0, 0);
+  };
+  DropKey dk{};
+  const bool dropping = DROP && a.drop.thr != 0;
+  if constexpr (DROP)
+    if (dropping) dk = drop_key(a.drop);
+  const uint64_t call0 = (uint64_t)qr * (uint64_t)(a.Ncols / 8) + (uint64_t)(c0 / 8 + qu);
+  auto store_q = [&](int s, uint8_t *dst) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DROP) {
+        if (dropping) {
+          uint32_t w[4];
+          philox7(call0 + (uint64_t)((int64_t)s * 64 + 16 * i) * (uint64_t)(a.Ncols / 8), dk, w);
+          qv[i] &= u32x4{keep_mask2(w[0], dk.thr2), keep_mask2(w[1], dk.thr2), keep_mask2(w[2], dk.thr2),
+                         keep_mask2(w[3], dk.thr2)};
+        }
+      }
+      *reinterpret_cast<u32x4 *>(dst + qst + 8192 * i) = qv[i];
+    }
+  };
+  // Lt: direct load g covers ranks 8 g .. + 7, 64 rows (128 bytes); RT * 4 loads.
+  const int lj = 8 * wave + (lane >> 3);
+  const uint32_t lo = lj < a.R ? (uint32_t)(lj * a.Mp * 2 + 16 * ((lane & 7) ^ ((lj >> 1) & 7))) : kOutOfRange;
+  auto issue_l = [&](uint8_t *dst, int s) {
+    const rsrc_t rl = make_rsrc_u(a.Lt + (int64_t)s * 64, (a.R * a.Mp - (int64_t)s * 64) * 2);
+    if (wave < 4 * RT)
+      load_lds16(rl, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(dst)) + wave * 1024, lo, 0);
+  };
+
+  f32x16 acc[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
+  // Fragments of sub-step c: lane half h takes rows 32 h + 8 c .. + 7.
+  // A lane of a transposing read points at row (lane % 16) / 4 of four, columns
+  // 4 (lane % 4) of its group's 16; rows 8 c + 4 p on add whole rows.
+  uint32_t fl[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) fl[c] = (uint32_t)(lr * 128 + 16 * ((4 * lh + c) ^ ((lr >> 1) & 7)));
+  const int tr = (lane & 15) >> 2, tc = 32 * wave + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const uint32_t fq = (uint32_t)((32 * lh + tr) * 512 + 16 * ((tc >> 3) ^ (4 * tr)) + 2 * (tc & 7));
+  auto multiply = [&](const uint8_t *q, const uint8_t *l) {
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+    const uint32_t qb = lds_offset(q);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)(qb + fq + c * 4096));
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)(qb + fq + c * 4096 + 2048));
+      const bf16x8 b = __builtin_bit_cast(bf16x8, (s16x8){x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w});
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8 *>(l + t * 32 * 128 + fl[c]), b,
+                                                         acc[t], 0, 0, 0);
+    }
+  };
+
+  // Step s reads stage (s - s0) & 1; the other (last read before the previous
+  // barrier) receives step s + 1, whose rows of Q are in registers, and step s + 2
+  // is requested.  Those four loads stay in flight across the barrier: it waits
+  // for the direct load of Lt, issued before them, and for LDS only.
+  const int last = s1 - 1;
+  auto barrier = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0074);   // vmcnt(4), lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+  };
+  auto step = [&](int s, const uint8_t *q, const uint8_t *l, uint8_t *qn, uint8_t *ln) {
+    store_q(min(s + 1, last), qn);
+    __builtin_amdgcn_sched_barrier(0);
+    issue_l(ln, min(s + 1, last));
+    __builtin_amdgcn_sched_barrier(0);
+    load_q(min(s + 2, last));
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(q, l);
+    barrier();
+  };
+  if (s0 < s1) {
+    load_q(s0);
+    issue_l(ls0, s0);
+    store_q(s0, qs0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_q(min(s0 + 1, last));
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    for (int s = s0; s < s1; s += 2) {
+      step(s, qs0, ls0, qs1, ls1);
+      if (s + 1 >= s1) break;
+      step(s + 1, qs1, ls1, qs0, ls0);
+    }
+  }
+  // The loads past the end land before the wave ends (they write only its own
+  // registers, and LDS that no one reads).
+  // acc[t][e]: rank 32 t + 8 (e / 4) + 4 lh + e % 4, column c0 + 32 wave + lr.
+  const int64_t col = c0 + 32 * wave + lr;
+  float *part = a.part + (int64_t)split * a.R * a.Ncols;
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int j = 32 * t + 8 * (e >> 2) + 4 * lh + (e & 3);
+      if (j < a.R && col < a.Ncols) part[(int64_t)j * a.Ncols + col] = acc[t][e];
+    }
+}
+
+// out = bf16(c * sum of the ranges), as [R][Ncols] or transposed [Ncols][R]: a
+// workgroup owns 64 columns and up to 64 ranks, loads them along the columns
+// and stores along whichever is contiguous, through LDS.
+__global__ __launch_bounds__(256) void colsum_reduce_kernel(ColSumArgs a0, ColSumArgs a1) {
+  __shared__ float tile[64][65];
+  const ColSumArgs &a = blockIdx.y ? a1 : a0;
+  const int64_t c0 = (int64_t)blockIdx.x * 64;
+  if (c0 >= a.Ncols) return;
+  const int tid = threadIdx.x, cl = tid & 63;
+  const int R = (int)a.R;
+  const int64_t stride = a.R * a.Ncols;
+  const int j0 = (int)blockIdx.z * 16, j1 = min(R, j0 + 16);   // ranks of this workgroup
+  if (j0 >= R) return;
+  for (int j = j0 + (tid >> 6); j < j1; j += 4) {
+    const float *p = a.part + (int64_t)j * a.Ncols + c0 + cl;   // Ncols % 64 == 0
+    float v = 0.0f;
+    for (int q0 = 0; q0 < a.splits; q0 += 8) {
+      float x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = p[(int64_t)min(q0 + q, a.splits - 1) * stride];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q0 + q < a.splits) v += x[q];
+    }
+    v *= a.drop.c;
+    if (a.transpose) tile[cl][j - j0] = v;
+    else a.out[(int64_t)j * a.Ncols + c0 + cl] = f32_to_bf16(v);
+  }
+  if (!a.transpose) return;
+  __syncthreads();
+  const int w = j1 - j0;
+  for (int i = tid; i < 64 * w; i += 256) a.out[(c0 + i / w) * a.R + j0 + i % w] = f32_to_bf16(tile[i / w][i % w]);
+}
+
+}  // namespace
+
+// Enough ranges for about two workgroups per CU over the call's two sums
+// (`cols` columns between them), at least 128 rows each and at most 16.
+int colsum_splits(int64_t M, int64_t cols) {
+  const int64_t tiles = (cols + CS_COLS - 1) / CS_COLS;
+  const int64_t want = (2 * device_cus() + tiles - 1) / tiles;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 16), (M + 127) / 128));
+}
+
+hipError_t launch_colsum2(const ColSumArgs &a, const ColSumArgs &b, hipStream_t st, int trace_kind) {
+  const int64_t ncols = std::max(a.Ncols, b.Ncols), R = std::max(a.R, b.R);
+  const dim3 grid((unsigned)((ncols + CS_COLS - 1) / CS_COLS), (unsigned)a.splits, 2u), block(CS_THREADS);
+  {
+    TraceScope tr(trace_kind, st);
+    const bool drop = a.drop.thr || b.drop.thr;
+    if (R <= 32) {
+      if (drop) hipLaunchKernelGGL((colsum_kernel<1, true>), grid, block, 0, st, a, b);
+      else hipLaunchKernelGGL((colsum_kernel<1, false>), grid, block, 0, st, a, b);
+    } else {
+      if (drop) hipLaunchKernelGGL((colsum_kernel<2, true>), grid, block, 0, st, a, b);
+      else hipLaunchKernelGGL((colsum_kernel<2, false>), grid, block, 0, st, a, b);
+    }
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(colsum_reduce_kernel, dim3((unsigned)(ncols / 64), 2u, (unsigned)((R + 15) / 16)), dim3(256), 0, st,
+                     a, b);
+  return hipGetLastError();
+}
+
+}  // namespace qn

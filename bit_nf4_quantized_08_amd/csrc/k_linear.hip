@@ -805,13 +805,20 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     QN_TRY(launch_lowrank2(ld, a.H ? nullptr : &lh, st));
   }
 
-  // One launch: dB [N, r] = ((sH)^T dY)^T and dA [r, K] = dH^T X, contractions over M.
-  {
+  // One launch: dB [N, r] = ((sH)^T dY)^T and dA [r, K] = dH^T X, contractions over
+  // M: on the matrix cores for the MXFP4 base and under dropout; without either
+  // the vector kernel, whose sums (and so whose results) those calls keep.
+  if (a.mx_scales || a.drop.thr) {
+    const int splits = colsum_splits(a.M, a.N + a.K);
+    const ColSumArgs cb{sHt, Mp, a.dY, a.M, a.N, a.r, bpart, splits, a.dB, true, kNoDrop};
+    const ColSumArgs ca{dHt, Mp, a.X, a.M, a.K, a.r, apart, splits, a.dA, false, a.drop};
+    QN_TRY(launch_colsum2(cb, ca, st, QN_TRACE_GEMM_DB));
+  } else {
     ColRedArgs cb{}, ca{};
     cb.Lt = sHt; cb.Mp = Mp; cb.Q = a.dY; cb.ldq = a.N; cb.M = a.M; cb.Ncols = a.N; cb.R = a.r;
     cb.part = bpart; cb.out = a.dB; cb.transpose = true;
     ca.Lt = dHt; ca.Mp = Mp; ca.Q = a.X; ca.ldq = a.K; ca.M = a.M; ca.Ncols = a.K; ca.R = a.r;
-    ca.part = apart; ca.out = a.dA; ca.transpose = false; ca.drop = a.drop;
+    ca.part = apart; ca.out = a.dA; ca.transpose = false;
     QN_TRY(launch_colred2(cb, &ca, st, QN_TRACE_GEMM_DB));
   }
   // dX [M, K] = dY [M, N] * W_hat [N, K] + dH [M, r] * A [r, K]

@@ -349,11 +349,6 @@ hipError_t launch_lowrank(const LowRankArgs &a, hipStream_t st) { return launch_
 // reads).  Per-split partial sums go to `part`; a second kernel adds the
 // splits in order and rounds to bf16.  Like the low-rank product, one launch
 // can carry two independent reductions over the same rows (blockIdx.z).
-//
-// Dropout of Q (dA's X): the four lanes of a quad hold the eight columns of one
-// generator call, two each.  Of four rows, lane j of the quad runs the call of
-// row j, and a 4 x 4 transpose within the quad (DPP) hands every lane its own
-// word of all four rows; the sum is scaled by 1/(1-p) when it is rounded.
 namespace qn {
 namespace {
 
@@ -362,22 +357,7 @@ constexpr int CR_COLS = 128;
 constexpr int CR_RB = 128;        // rows per split
 constexpr int CR_PAIRS = CR_RB / 2;
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t quad_perm(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
-}
-
-// w[i] of lane j of a quad <- w[j] of lane i.
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
-  const bool odd = lane & 1, hi = lane & 2;
-  uint32_t x = quad_perm<0xB1>(odd ? w[0] : w[1]), y = quad_perm<0xB1>(odd ? w[2] : w[3]);
-  if (odd) { w[0] = x; w[2] = y; } else { w[1] = x; w[3] = y; }
-  x = quad_perm<0x4E>(hi ? w[0] : w[2]);
-  y = quad_perm<0x4E>(hi ? w[1] : w[3]);
-  if (hi) { w[0] = x; w[1] = y; } else { w[2] = x; w[3] = y; }
-}
-
-template <int R, bool DROP>
+template <int R>
 __global__ __launch_bounds__(CR_THREADS) void colred_kernel(ColRedArgs a0, ColRedArgs a1) {
   constexpr int RJ = R < 16 ? R : 16;            // rows of the output reduced per pass
   __shared__ uint32_t lt[CR_PAIRS * R];          // (Lt[j][2p], Lt[j][2p+1]) at [p][j]
@@ -425,26 +405,6 @@ __global__ __launch_bounds__(CR_THREADS) void colred_kernel(ColRedArgs a0, ColRe
     lt[p * R + j] = (j < a.R && mb + 2 * p < a.Mp) ? ltv[i] : 0u;
   }
   __syncthreads();
-
-  if constexpr (DROP) {
-    if (a.drop.thr) {
-      const DropKey dk = drop_key(a.drop);
-      const uint64_t call0 = (uint64_t)(c >> 3), pitch = (uint64_t)(a.ldq / 8);
-#pragma unroll
-      for (int u = 0; u < U; u += 2) {
-        // Row j of the four: row j & 1 of pair wave + 4 (u + j / 2).
-        const int j = lane & 3;
-        const uint64_t row = (uint64_t)mb + (uint64_t)(2 * (wave + 4 * (u + (j >> 1))) + (j & 1));
-        uint32_t w[4];
-        philox7(row * pitch + call0, dk, w);
-        quad_transpose(w, lane);
-        q[u][0] &= keep_mask2(w[0], dk.thr2);
-        q[u][1] &= keep_mask2(w[1], dk.thr2);
-        q[u + 1][0] &= keep_mask2(w[2], dk.thr2);
-        q[u + 1][1] &= keep_mask2(w[3], dk.thr2);
-      }
-    }
-  }
 
   float acc0[R], acc1[R];
 #pragma unroll
@@ -516,15 +476,7 @@ __global__ __launch_bounds__(256) void colred_reduce_kernel(ColRedArgs a0, ColRe
     for (int q = 0; q < BATCH; ++q)
       if (s0 + q < splits) v += x[q];
   }
-  a.out[a.transpose ? col * a.R + j : idx] = f32_to_bf16(v * a.drop.c);   // c = 1 without dropout
-}
-
-template <bool DROP>
-void launch_colred_rank(const ColRedArgs &a, const ColRedArgs &a1, int64_t R, dim3 grid, hipStream_t st) {
-  if (R <= 8) hipLaunchKernelGGL((colred_kernel<8, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
-  else if (R <= 16) hipLaunchKernelGGL((colred_kernel<16, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
-  else if (R <= 32) hipLaunchKernelGGL((colred_kernel<32, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
-  else hipLaunchKernelGGL((colred_kernel<64, DROP>), grid, dim3(CR_THREADS), 0, st, a, a1);
+  a.out[a.transpose ? col * a.R + j : idx] = f32_to_bf16(v);
 }
 
 }  // namespace
@@ -539,8 +491,10 @@ hipError_t launch_colred2(const ColRedArgs &a, const ColRedArgs *b, hipStream_t 
   const dim3 grid((unsigned)((ncols + CR_COLS - 1) / CR_COLS), (unsigned)splits, b ? 2u : 1u);
   {
     TraceScope tr(trace_kind, st);
-    if (a.drop.thr || a1.drop.thr) launch_colred_rank<true>(a, a1, R, grid, st);
-    else launch_colred_rank<false>(a, a1, R, grid, st);
+    if (R <= 8) hipLaunchKernelGGL(colred_kernel<8>, grid, dim3(CR_THREADS), 0, st, a, a1);
+    else if (R <= 16) hipLaunchKernelGGL(colred_kernel<16>, grid, dim3(CR_THREADS), 0, st, a, a1);
+    else if (R <= 32) hipLaunchKernelGGL(colred_kernel<32>, grid, dim3(CR_THREADS), 0, st, a, a1);
+    else hipLaunchKernelGGL(colred_kernel<64>, grid, dim3(CR_THREADS), 0, st, a, a1);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -206,13 +206,28 @@ struct ColRedArgs {
   float *part;
   uint16_t *out;
   bool transpose;
-  DropArgs drop = kNoDrop;   // thr > 0: Q is read as keep * Q and the sum scaled by c
 };
 int colred_splits(int64_t M);
 hipError_t launch_colred(const ColRedArgs &a, hipStream_t s, int trace_kind);
 // Two independent reductions over the same M in one launch (b may be null);
 // each needs its own `part`.
 hipError_t launch_colred2(const ColRedArgs &a, const ColRedArgs *b, hipStream_t s, int trace_kind);
+
+// The same sums on the matrix cores (k_colsum.hip), for the MXFP4 linear and for
+// dropout: `part` holds splits * R * Ncols floats, Ncols % 64 == 0.
+struct ColSumArgs {
+  const uint16_t *Lt;
+  int64_t Mp;
+  const uint16_t *Q;   // [M, Ncols]
+  int64_t M, Ncols, R;
+  float *part;
+  int splits;
+  uint16_t *out;
+  bool transpose;
+  DropArgs drop;       // thr > 0: Q is read as keep * Q and the sum scaled by c; kNoDrop for none
+};
+int colsum_splits(int64_t M, int64_t cols);
+hipError_t launch_colsum2(const ColSumArgs &a, const ColSumArgs &b, hipStream_t s, int trace_kind);
 
 // Forward pieces.
 struct FwdArgs {
