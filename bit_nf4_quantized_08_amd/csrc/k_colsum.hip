@@ -30,8 +30,6 @@ namespace {
 
 constexpr int CS_THREADS = 512;
 constexpr int CS_COLS = 256;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 template <int RT, bool DROP>   // 32-rank tiles
 __global__ __launch_bounds__(CS_THREADS) __attribute__((amdgpu_waves_per_eu(4, 4)))
@@ -104,13 +102,9 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
   const int tr = (lane & 15) >> 2, tc = 32 * wave + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
   const uint32_t fq = (uint32_t)((32 * lh + tr) * 512 + 16 * ((tc >> 3) ^ (4 * tr)) + 2 * (tc & 7));
   auto multiply = [&](const uint8_t *q, const uint8_t *l) {
-    typedef __attribute__((address_space(3))) s16x4 *lds4;
-    const uint32_t qb = lds_offset(q);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)(qb + fq + c * 4096));
-      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)(qb + fq + c * 4096 + 2048));
-      const bf16x8 b = __builtin_bit_cast(bf16x8, (s16x8){x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w});
+      const bf16x8 b = read_transposed(q + fq + c * 4096, q + fq + c * 4096 + 2048);
 #pragma unroll
       for (int t = 0; t < RT; ++t)
         acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8 *>(l + t * 32 * 128 + fl[c]), b,
@@ -123,11 +117,6 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
   // is requested.  Those four loads stay in flight across the barrier: it waits
   // for the direct load of Lt, issued before them, and for LDS only.
   const int last = s1 - 1;
-  auto barrier = [&]() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0074);   // vmcnt(4), lgkmcnt(0)
-    asm volatile("s_barrier" ::: "memory");
-  };
   auto step = [&](int s, const uint8_t *q, const uint8_t *l, uint8_t *qn, uint8_t *ln) {
     store_q(min(s + 1, last), qn);
     __builtin_amdgcn_sched_barrier(0);
@@ -136,7 +125,7 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
     load_q(min(s + 2, last));
     __builtin_amdgcn_sched_barrier(0);
     multiply(q, l);
-    barrier();
+    stage_barrier<4>();
   };
   if (s0 < s1) {
     load_q(s0);
@@ -145,7 +134,7 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
     __builtin_amdgcn_sched_barrier(0);
     load_q(min(s0 + 1, last));
     __builtin_amdgcn_sched_barrier(0);
-    barrier();
+    stage_barrier<4>();
     for (int s = s0; s < s1; s += 2) {
       step(s, qs0, ls0, qs1, ls1);
       if (s + 1 >= s1) break;

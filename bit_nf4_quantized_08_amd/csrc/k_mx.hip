@@ -246,8 +246,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequant_kernel(const uint8_t *__r
 // 16-byte piece k of row r at slot k ^ ((r >> 1) & 7): a fragment read takes
 // one piece of 16 consecutive rows, which then fall on 16 distinct groups of
 // four banks (rows are 128 bytes apart, two rows to a turn of the 64 banks).
-// Scales go straight to registers, one step ahead: 32 rows of a chunk are 256
-// contiguous bytes.
+// The scale bytes come with them (8 BM and 8 BN contiguous bytes, 16 a lane).
 // The adapter term bf16(s H) B^T (r <= 64) follows as bf16 MFMAs into the same
 // accumulators, its fragments read from global memory (H is small, B is read
 // once per tile column).
@@ -269,11 +268,15 @@ void mx_gemm_kernel(MxGemmArgs a) {
   constexpr int NW = WR * WC, BM = 32 * TM * WR, BN = 32 * TN * WC;
   constexpr int XL = BM / 8 / NW, WL = BN / 8 / NW;   // direct loads (8 rows each) per wave and step
   static_assert(XL * 8 * NW == BM && WL * 8 * NW == BN, "stage loads");
+  constexpr int XE = BM / 128, WE = BN / 128;         // direct loads of scales (128 rows each), a wave each
+  static_assert(XE >= 1 && WE >= 1 && XE + WE <= NW, "scale loads");
   constexpr int kPitch = 32 * TN + 8;                 // bf16 per row of a store block
   __shared__ __attribute__((aligned(16))) uint8_t xs0[BM * 128];
   __shared__ __attribute__((aligned(16))) uint8_t xs1[BM * 128];
   __shared__ __attribute__((aligned(16))) uint8_t ws0[BN * 128];
   __shared__ __attribute__((aligned(16))) uint8_t ws1[BN * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t es0[(BM + BN) * 8];   // scales: X^'s rows, then W's
+  __shared__ __attribute__((aligned(16))) uint8_t es1[(BM + BN) * 8];
   static_assert(NW * 32 * kPitch * 2 <= 2 * BM * 128 + 2 * BN * 128, "store blocks fit the stages");
 
   int tm, tn;
@@ -299,26 +302,22 @@ void mx_gemm_kernel(MxGemmArgs a) {
   for (int i = 0; i < XL; ++i) xo[i] = load_off(wave * XL + i);
 #pragma unroll
   for (int i = 0; i < WL; ++i) wo[i] = load_off(wave * WL + i);
-  auto issue = [&](uint8_t *xd, uint8_t *wd, int s) {
+  const int64_t xrow = m0 + wr * 32 * TM, wrow = n0 + wc * 32 * TN;
+  auto issue = [&](uint8_t *xd, uint8_t *wd, uint8_t *ed, int s) {
     const uint32_t xb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(xd)) + wave * XL * 1024;
     const uint32_t wb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(wd)) + wave * WL * 1024;
+    const uint32_t eb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(ed)) + wave * 1024;
 #pragma unroll
     for (int i = 0; i < XL; ++i) load_lds16(rx, xb + i * 1024, xo[i], s * 128);
 #pragma unroll
     for (int i = 0; i < WL; ++i) load_lds16(rw, wb + i * 1024, wo[i], s * 128);
-  };
-  // Scale dwords of step s: rows lr of each 32-row tile, blocks 4 lh .. +3.
-  struct Scales {
-    uint32_t a[TM], b[TN];
-  };
-  const int64_t xrow = m0 + wr * 32 * TM, wrow = n0 + wc * 32 * TN;
-  auto load_scales = [&](Scales &t, int s) {
-    const rsrc_t ra = make_rsrc_u(a.xs + ((int64_t)s * a.M + xrow) * 8, (a.M - xrow) * 8);
-    const rsrc_t rb = make_rsrc_u(a.ws + ((int64_t)s * a.N + wrow) * 8, (a.N - wrow) * 8);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) t.a[i] = __builtin_amdgcn_raw_buffer_load_b32(ra, (uint32_t)((32 * i + lr) * 8 + 4 * lh), 0, 0);
-#pragma unroll
-    for (int i = 0; i < TN; ++i) t.b[i] = __builtin_amdgcn_raw_buffer_load_b32(rb, (uint32_t)((32 * i + lr) * 8 + 4 * lh), 0, 0);
+    // Rows past the matrix read zero (the next chunk's rows, or nothing, lie there).
+    if (wave < XE + WE) {
+      const bool of_x = wave < XE;
+      const int64_t first = of_x ? m0 : n0, rows = of_x ? a.M : a.N;
+      const rsrc_t re = make_rsrc_u((of_x ? a.xs : a.ws) + ((int64_t)s * rows + first) * 8, (rows - first) * 8);
+      load_lds16(re, eb, (uint32_t)((of_x ? wave : wave - XE) * 1024 + lane * 16), 0);
+    }
   };
 
   f32x16 acc[TM][TN];
@@ -336,44 +335,61 @@ void mx_gemm_kernel(MxGemmArgs a) {
     const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
     return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
   };
-  auto multiply = [&](const uint8_t *xc, const uint8_t *wc_, const Scales &t) {
+  // Sub-step j: blocks 4 lh + j; byte j of the rows' scale dwords.
+  struct Frag {
+    i32x8 a[TM], b[TN];
+  };
+  const int ex = (wr * 32 * TM + lr) * 8 + 4 * lh, ew = (BM + wc * 32 * TN + lr) * 8 + 4 * lh;
+  auto step = [&](int s, const uint8_t *xc, const uint8_t *wc_, const uint8_t *ec, uint8_t *xn, uint8_t *wn, uint8_t *en) {
     const uint8_t *xp = xc + wr * 32 * TM * 128, *wp = wc_ + wc * 32 * TN * 128;
-    auto sub = [&](auto J) {
+    uint32_t ta[TM], tb[TN];
+    auto read_f = [&](Frag &f, int j) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) f.a[i] = frag(xp + i * 32 * 128 + fo[j]);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) f.b[i] = frag(wp + i * 32 * 128 + fo[j]);
+    };
+    auto mma = [&](const Frag &f, auto J) {
       constexpr int j = decltype(J)::value;
-      i32x8 fa[TM], fb[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = frag(xp + i * 32 * 128 + fo[j]);
-#pragma unroll
-      for (int i = 0; i < TN; ++i) fb[i] = frag(wp + i * 32 * 128 + fo[j]);
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int k = 0; k < TN; ++k)
-          acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[k], acc[i][k], 4, 4, j, (int)t.a[i], j,
-                                                                      (int)t.b[k]);
+          acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[i], f.b[k], acc[i][k], 4, 4, j, (int)ta[i], j,
+                                                                      (int)tb[k]);
     };
-    sub(std::integral_constant<int, 0>{});
-    sub(std::integral_constant<int, 1>{});
-    sub(std::integral_constant<int, 2>{});
-    sub(std::integral_constant<int, 3>{});
+    Frag f0, f1;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ta[i] = *reinterpret_cast<const uint32_t *>(ec + ex + 32 * 8 * i);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) tb[i] = *reinterpret_cast<const uint32_t *>(ec + ew + 32 * 8 * i);
+    read_f(f0, 0);
+    issue(xn, wn, en, min(s + 1, s1 - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    read_f(f1, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f0, std::integral_constant<int, 0>{});
+    __builtin_amdgcn_sched_barrier(0);
+    read_f(f0, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f1, std::integral_constant<int, 1>{});
+    __builtin_amdgcn_sched_barrier(0);
+    read_f(f1, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f0, std::integral_constant<int, 2>{});
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f1, std::integral_constant<int, 3>{});
+    __builtin_amdgcn_sched_barrier(0);
+    stage_barrier();
   };
-
-  Scales t0, t1;
-  issue(xs0, ws0, s0);
-  load_scales(t0, s0);
+  issue(xs0, ws0, es0, s0);
   stage_barrier();
   // Stage (s - s0) & 1 holds step s; the other is filled meanwhile (it was last
   // read before the previous barrier).  Past the end the last step is reloaded.
   for (int s = s0; s < s1; s += 2) {
-    issue(xs1, ws1, min(s + 1, s1 - 1));
-    load_scales(t1, min(s + 1, s1 - 1));
-    multiply(xs0, ws0, t0);
-    stage_barrier();
+    step(s, xs0, ws0, es0, xs1, ws1, es1);
     if (s + 1 >= s1) break;
-    issue(xs0, ws0, min(s + 2, s1 - 1));
-    load_scales(t0, min(s + 2, s1 - 1));
-    multiply(xs1, ws1, t1);
-    stage_barrier();
+    step(s + 1, xs1, ws1, es1, xs0, ws0, es0);
   }
 
   if constexpr (PART) {

@@ -38,7 +38,6 @@ namespace {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kRowPitch = 576;           // bytes per expanded row
 constexpr int kWStage = 64 * kRowPitch;  // bytes per expanded stage
 
@@ -93,19 +92,16 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     t.sb = __builtin_amdgcn_raw_buffer_load_b8(rs, (uint32_t)tid, s * 512, 0);
   };
   uint32_t wst = (uint32_t)(wn * kRowPitch + 16 * ch);
-  auto expand = [&](const Set &t, uint8_t *dst) {
+  auto expand = [&](const Set &t, int q, uint8_t *dst) {
     const float sc = as_f32(t.sb << 23);
     const uint32_t cw[4] = {t.code.x, t.code.y, t.code.z, t.code.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      u32x4 o;
-      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 0));
-      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 1));
-      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 2));
-      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 3));
-      if (t.sb == 255u) o = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
-      *reinterpret_cast<u32x4 *>(dst + wst + 128 * q) = o;
-    }
+    u32x4 o;
+    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 0));
+    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 1));
+    o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 2));
+    o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(cw[q], sc, 3));
+    if (t.sb == 255u) o = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+    *reinterpret_cast<u32x4 *>(dst + wst + 128 * q) = o;
   };
 
   f32x16 acc[TM][TN];
@@ -132,48 +128,71 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     return *reinterpret_cast<const bf16x8 *>(gst + fg[c] + i * 32 * 128);
   };
   auto read_w = [&](const uint8_t *wst_, int j, int c) {
-    typedef __attribute__((address_space(3))) s16x4 *lds4;
-    const uint32_t b = lds_offset(wst_) + fw[j] + c * 8 * kRowPitch;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)b);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(size_t)(b + 4 * kRowPitch));
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
-    return __builtin_bit_cast(bf16x8, (s16x8){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+    const uint8_t *b = wst_ + fw[j] + c * 8 * kRowPitch;
+    return read_transposed(b, b + 4 * kRowPitch);
   };
-  auto multiply = [&](const uint8_t *gst, const uint8_t *wst_) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      bf16x8 fa[TM], fb[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = read_g(gst, i, c);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = read_w(wst_, j, c);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
-  };
-
+  // Step s: stage (s - s0) & 1; past the end the last step is loaded again.  The
+  // four sub-steps' fragments are read one ahead, and unit q of the next stage is
+  // expanded with sub-step q's MFMAs.  The two loads of W (of step s + 2) are the
+  // last issued and stay in flight across the barrier.
   const int last = s1 - 1;
+  struct Frag {
+    bf16x8 a[TM], b[TN];
+  };
+  auto read_f = [&](Frag &f, const uint8_t *gst, const uint8_t *wst_, int c) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) f.a[i] = read_g(gst, i, c);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) f.b[j] = read_w(wst_, j, c);
+  };
+  auto mma = [&](const Frag &f) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+  };
+  auto step = [&](int s, const uint8_t *gc, const uint8_t *wc_, uint8_t *gn, uint8_t *wn_, const Set &t, Set &t2) {
+    Frag f0, f1;
+    read_f(f0, gc, wc_, 0);
+    issue_g(gn, min(s + 1, last));
+    __builtin_amdgcn_sched_barrier(0);
+    Set nt;
+    load_w(nt, min(s + 2, last));
+    __builtin_amdgcn_sched_barrier(0);
+    read_f(f1, gc, wc_, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f0);
+    expand(t, 0, wn_);
+    __builtin_amdgcn_sched_barrier(0);
+    read_f(f0, gc, wc_, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f1);
+    expand(t, 1, wn_);
+    __builtin_amdgcn_sched_barrier(0);
+    read_f(f1, gc, wc_, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f0);
+    expand(t, 2, wn_);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f1);
+    expand(t, 3, wn_);
+    __builtin_amdgcn_sched_barrier(0);
+    t2 = nt;
+    stage_barrier<2>();
+  };
   Set t0, t1;
   load_w(t0, s0);
   issue_g(gs0, s0);
+  __builtin_amdgcn_sched_barrier(0);
   load_w(t1, min(s0 + 1, last));
-  expand(t0, ws0);
-  stage_barrier();
-  // Step s: stage (s - s0) & 1; past the end the last step is loaded again.
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) expand(t0, q, ws0);
+  stage_barrier<2>();
   for (int s = s0; s < s1; s += 2) {
-    issue_g(gs1, min(s + 1, last));
-    load_w(t0, min(s + 2, last));
-    expand(t1, ws1);
-    multiply(gs0, ws0);
-    stage_barrier();
+    step(s, gs0, ws0, gs1, ws1, t1, t0);
     if (s + 1 >= s1) break;
-    issue_g(gs0, min(s + 2, last));
-    load_w(t1, min(s + 3, last));
-    expand(t0, ws0);
-    multiply(gs1, ws1);
-    stage_barrier();
+    step(s + 1, gs1, ws1, gs0, ws0, t0, t1);
   }
 
   const int64_t row0 = m0 + wr * 32 * TM, colw = k0 + 32 * UW * wc;   // the wave's first row and column

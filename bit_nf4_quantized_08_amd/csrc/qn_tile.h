@@ -31,11 +31,30 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t lds, uint32_t voff
                                            0, 0);
 }
 
-// Barrier that publishes a stage: the wave's direct-to-LDS loads have landed and
-// its LDS accesses are done before it arrives.
+// Barrier that publishes a stage: before it arrives, the wave's LDS accesses are
+// done and all but the last IN_FLIGHT of its global loads (direct-to-LDS loads
+// among them) have landed.  The loads that may stay in flight must be the last
+// ones issued (fenced from the scheduler); asm, because a compiler's own
+// workgroup fence would wait for them too.
+template <int IN_FLIGHT = 0>
 __device__ __forceinline__ void stage_barrier() {
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
+  static_assert(IN_FLIGHT < 16, "low bits of vmcnt");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | IN_FLIGHT);   // vmcnt(IN_FLIGHT), lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// Transposing LDS read: 16 lanes point at 4 rows x 16 columns of 16-bit values (8
+// bytes each) and receive 16 columns x 4 rows.  The pointer keeps its array, so
+// that the compiler does not take the read for one of another stage's bytes
+// and wait for the loads on their way there.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bf16x8 read_transposed(const uint8_t *lo, const uint8_t *hi) {
+  typedef __attribute__((address_space(3))) s16x4 *lds4;
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(__attribute__((address_space(3))) uint8_t *)lo);
+  const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(__attribute__((address_space(3))) uint8_t *)hi);
+  return __builtin_bit_cast(bf16x8, (s16x8){x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w});
 }
 
 // Tile of workgroup h: workgroups are dealt round-robin to the 8 XCDs, so XCD x
