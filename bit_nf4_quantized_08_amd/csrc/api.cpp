@@ -129,7 +129,7 @@ bool mx_shapes_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
   // dX; all of W's codes).
   if (K > (int64_t)1 << 22 || N > (int64_t)1 << 22) return false;
   if (N * 128 * qn::mx_chunks(K) > (int64_t)INT32_MAX) return false;
-  return M <= INT32_MAX / 64 && M <= INT32_MAX / qn::mx_chunks(K);
+  return M <= INT32_MAX / 64 && M <= ((int64_t)1 << 28) / qn::mx_chunks(K);   // X's scale bytes too
 }
 
 }  // namespace

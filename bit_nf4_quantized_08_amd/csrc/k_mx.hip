@@ -268,8 +268,8 @@ void mx_gemm_kernel(MxGemmArgs a) {
   constexpr int NW = WR * WC, BM = 32 * TM * WR, BN = 32 * TN * WC;
   constexpr int XL = BM / 8 / NW, WL = BN / 8 / NW;   // direct loads (8 rows each) per wave and step
   static_assert(XL * 8 * NW == BM && WL * 8 * NW == BN, "stage loads");
-  constexpr int XE = BM / 128, WE = BN / 128;         // direct loads of scales (128 rows each), a wave each
-  static_assert(XE >= 1 && WE >= 1 && XE + WE <= NW, "scale loads");
+  constexpr int EP = (BM + BN) / 128;                 // direct loads of scales (128 rows each)
+  static_assert(NW % EP == 0 && BM % 128 == 0, "scale loads");
   constexpr int kPitch = 32 * TN + 8;                 // bf16 per row of a store block
   __shared__ __attribute__((aligned(16))) uint8_t xs0[BM * 128];
   __shared__ __attribute__((aligned(16))) uint8_t xs1[BM * 128];
@@ -303,23 +303,26 @@ void mx_gemm_kernel(MxGemmArgs a) {
 #pragma unroll
   for (int i = 0; i < WL; ++i) wo[i] = load_off(wave * WL + i);
   const int64_t xrow = m0 + wr * 32 * TM, wrow = n0 + wc * 32 * TN;
-  auto issue = [&](uint8_t *xd, uint8_t *wd, uint8_t *ed, int s) {
-    const uint32_t xb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(xd)) + wave * XL * 1024;
-    const uint32_t wb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(wd)) + wave * WL * 1024;
-    const uint32_t eb = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(ed)) + wave * 1024;
-#pragma unroll
-    for (int i = 0; i < XL; ++i) load_lds16(rx, xb + i * 1024, xo[i], s * 128);
-#pragma unroll
-    for (int i = 0; i < WL; ++i) load_lds16(rw, wb + i * 1024, wo[i], s * 128);
-    // Rows past the matrix read zero (the next chunk's rows, or nothing, lie there).
-    if (wave < XE + WE) {
-      const bool of_x = wave < XE;
-      const int64_t first = of_x ? m0 : n0, rows = of_x ? a.M : a.N;
-      const rsrc_t re = make_rsrc_u((of_x ? a.xs : a.ws) + ((int64_t)s * rows + first) * 8, (rows - first) * 8);
-      load_lds16(re, eb, (uint32_t)((of_x ? wave : wave - XE) * 1024 + lane * 16), 0);
-    }
+  // Scales: load p covers rows 128 p .. of X^'s BM rows and then W's.  Every wave
+  // makes one load, so some are made twice, with the same bytes to the same
+  // place: a branch here would split the step's block, and the compiler would
+  // move the MFMAs past it.  Rows past the matrix get other rows' scales (or
+  // zero): their products are not stored.
+  const int erow = 128 * (wave % EP);
+  const bool of_x = erow < BM;
+  const rsrc_t re = of_x ? make_rsrc_u(a.xs, a.C * a.M * 8) : make_rsrc_u(a.ws, a.C * a.N * 8);
+  const uint32_t eo = (uint32_t)((of_x ? m0 + erow : n0 + erow - BM) * 8 + lane * 16);
+  const int estep = (int)((of_x ? a.M : a.N) * 8);
+  // Load i of step s into a stage.
+  constexpr int LOADS = XL + WL + 1;
+  const uint32_t xl = (uint32_t)(wave * XL * 1024), wl = (uint32_t)(wave * WL * 1024);
+  auto issue = [&](uint8_t *xd, uint8_t *wd, uint8_t *ed, int s, int i) {
+    if (i < XL) load_lds16(rx, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(xd)) + xl + i * 1024, xo[i], s * 128);
+    else if (i < XL + WL)
+      load_lds16(rw, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(wd)) + wl + (i - XL) * 1024, wo[i - XL], s * 128);
+    else
+      load_lds16(re, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(ed)) + 8 * erow, eo, s * estep);
   };
-
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -331,66 +334,98 @@ void mx_gemm_kernel(MxGemmArgs a) {
   uint32_t fo[4];   // LDS offset of sub-step j's piece in row lr of a tile
 #pragma unroll
   for (int j = 0; j < 4; ++j) fo[j] = (uint32_t)(lr * 128 + 16 * ((4 * lh + j) ^ ((lr >> 1) & 7)));
-  auto frag = [&](const uint8_t *p) {
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
-    return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-  };
+  // A fragment is four registers; the instruction's eight-register operand type
+  // is formed at its use (carried over the loop, its unused half would be too).
+  auto frag = [&](const uint8_t *p) { return *reinterpret_cast<const u32x4 *>(p); };
+  auto wide = [&](u32x4 v) { return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0}; };
   // Sub-step j: blocks 4 lh + j; byte j of the rows' scale dwords.
   struct Frag {
-    i32x8 a[TM], b[TN];
+    u32x4 a[TM], b[TN];
   };
+  struct Scales {
+    uint32_t a[TM], b[TN];
+  };
+  const int xp = wr * 32 * TM * 128, wp = wc * 32 * TN * 128;
   const int ex = (wr * 32 * TM + lr) * 8 + 4 * lh, ew = (BM + wc * 32 * TN + lr) * 8 + 4 * lh;
-  auto step = [&](int s, const uint8_t *xc, const uint8_t *wc_, const uint8_t *ec, uint8_t *xn, uint8_t *wn, uint8_t *en) {
-    const uint8_t *xp = xc + wr * 32 * TM * 128, *wp = wc_ + wc * 32 * TN * 128;
-    uint32_t ta[TM], tb[TN];
-    auto read_f = [&](Frag &f, int j) {
+  auto read_f = [&](Frag &f, const uint8_t *xc, const uint8_t *wc_, int j) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) f.a[i] = frag(xp + i * 32 * 128 + fo[j]);
+    for (int i = 0; i < TM; ++i) f.a[i] = frag(xc + xp + i * 32 * 128 + fo[j]);
 #pragma unroll
-      for (int i = 0; i < TN; ++i) f.b[i] = frag(wp + i * 32 * 128 + fo[j]);
-    };
-    auto mma = [&](const Frag &f, auto J) {
-      constexpr int j = decltype(J)::value;
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int k = 0; k < TN; ++k)
-          acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[i], f.b[k], acc[i][k], 4, 4, j, (int)ta[i], j,
-                                                                      (int)tb[k]);
-    };
-    Frag f0, f1;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) ta[i] = *reinterpret_cast<const uint32_t *>(ec + ex + 32 * 8 * i);
-#pragma unroll
-    for (int i = 0; i < TN; ++i) tb[i] = *reinterpret_cast<const uint32_t *>(ec + ew + 32 * 8 * i);
-    read_f(f0, 0);
-    issue(xn, wn, en, min(s + 1, s1 - 1));
-    __builtin_amdgcn_sched_barrier(0);
-    read_f(f1, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    mma(f0, std::integral_constant<int, 0>{});
-    __builtin_amdgcn_sched_barrier(0);
-    read_f(f0, 2);
-    __builtin_amdgcn_sched_barrier(0);
-    mma(f1, std::integral_constant<int, 1>{});
-    __builtin_amdgcn_sched_barrier(0);
-    read_f(f1, 3);
-    __builtin_amdgcn_sched_barrier(0);
-    mma(f0, std::integral_constant<int, 2>{});
-    __builtin_amdgcn_sched_barrier(0);
-    mma(f1, std::integral_constant<int, 3>{});
-    __builtin_amdgcn_sched_barrier(0);
-    stage_barrier();
+    for (int i = 0; i < TN; ++i) f.b[i] = frag(wc_ + wp + i * 32 * 128 + fo[j]);
   };
-  issue(xs0, ws0, es0, s0);
+  auto read_e = [&](Scales &t, const uint8_t *ec) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) t.a[i] = *reinterpret_cast<const uint32_t *>(ec + ex + 32 * 8 * i);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) t.b[i] = *reinterpret_cast<const uint32_t *>(ec + ew + 32 * 8 * i);
+  };
+  // Sub-step J's MFMAs, with hook(0) .. hook(3) spread between them.
+  auto mma = [&](const Frag &f, const Scales &t, auto J, auto &&hook) {
+    constexpr int j = decltype(J)::value, per = TM * TN / 4;
+#pragma unroll
+    for (int m = 0; m < TM * TN; ++m) {
+      const int i = m / TN, k = m % TN;
+      acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(f.a[i]), wide(f.b[k]), acc[i][k], 4, 4, j,
+                                                                  (int)t.a[i], j, (int)t.b[k]);
+      if (m % per == per - 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        hook(m / per);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  // One step: stage `c` now, stage `n` next.  On entry f0 and tc hold sub-step 0's
+  // fragments and the scales, and the first four loads of step s + 1 are on
+  // their way.  Fragments are read a sub-step ahead; the barrier comes when the
+  // last of them are in registers, so that the next stage's first fragments are
+  // read under the last sub-step's MFMAs.  The direct loads are spread over the
+  // MFMAs, the other loads of step s + 1 over sub-steps 0 and 1, the first four
+  // of step s + 2 over sub-step 3: issued together they fill the CU's vector
+  // memory path, and each wave would stand at its next load with its MFMAs
+  // behind it.  (Touching the lines of later steps to bring them into L2 costs
+  // more of that path than it saves: 139 -> 152 us.)
+  const int last = s1 - 1;
+  auto none = [](int) {};
+  auto step = [&](int s, uint8_t *xc, uint8_t *wc_, uint8_t *ec, uint8_t *xn, uint8_t *wn, uint8_t *en, Frag &f0, Frag &f1,
+                  const Scales &tc, Scales &tn_) {
+    const int sn = min(s + 1, last), sm = min(s + 2, last);
+    read_f(f1, xc, wc_, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f0, tc, std::integral_constant<int, 0>{}, [&](int q) {
+      if (4 + q < LOADS) issue(xn, wn, en, sn, 4 + q);
+    });
+    read_f(f0, xc, wc_, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f1, tc, std::integral_constant<int, 1>{}, [&](int q) {
+      if (8 + q < LOADS) issue(xn, wn, en, sn, 8 + q);
+    });
+    read_f(f1, xc, wc_, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f0, tc, std::integral_constant<int, 2>{}, none);
+    stage_barrier();
+    read_e(tn_, en);
+    read_f(f0, xn, wn, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f1, tc, std::integral_constant<int, 3>{}, [&](int q) { issue(xc, wc_, ec, sm, q); });
+  };
+  // Stage (s - s0) & 1 holds step s; past the end the last step is loaded again.
+  static_assert(LOADS > 4 && LOADS <= 12, "load schedule");
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) issue(xs0, ws0, es0, s0, i);
   stage_barrier();
-  // Stage (s - s0) & 1 holds step s; the other is filled meanwhile (it was last
-  // read before the previous barrier).  Past the end the last step is reloaded.
+  Frag f0, f1;
+  Scales t0, t1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) issue(xs1, ws1, es1, min(s0 + 1, last), i);
+  read_e(t0, es0);
+  read_f(f0, xs0, ws0, 0);
   for (int s = s0; s < s1; s += 2) {
-    step(s, xs0, ws0, es0, xs1, ws1, es1);
+    step(s, xs0, ws0, es0, xs1, ws1, es1, f0, f1, t0, t1);
     if (s + 1 >= s1) break;
-    step(s + 1, xs1, ws1, es1, xs0, ws0, es0);
+    step(s + 1, xs1, ws1, es1, xs0, ws0, es0, f0, f1, t1, t0);
   }
+  // The loads past the end must land before the stages are written again.
+  stage_barrier();
 
   if constexpr (PART) {
     float *part = a.part + (int64_t)split * a.M * a.N;

@@ -131,10 +131,13 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     const uint8_t *b = wst_ + fw[j] + c * 8 * kRowPitch;
     return read_transposed(b, b + 4 * kRowPitch);
   };
-  // Step s: stage (s - s0) & 1; past the end the last step is loaded again.  The
-  // four sub-steps' fragments are read one ahead, and unit q of the next stage is
-  // expanded with sub-step q's MFMAs.  The two loads of W (of step s + 2) are the
-  // last issued and stay in flight across the barrier.
+  // Step s: stage (s - s0) & 1; past the end the last step is loaded again.  On
+  // entry f0 holds sub-step 0's fragments.  Fragments are read a sub-step ahead,
+  // the next stage's codes are expanded with the first three sub-steps' MFMAs,
+  // and the barrier comes when the last fragments are in registers: the next
+  // stage's first fragments are read, and G of the step after asked for, under
+  // the last sub-step's MFMAs.  The two loads of W are the last issued before
+  // the barrier and stay in flight across it.
   const int last = s1 - 1;
   struct Frag {
     bf16x8 a[TM], b[TN];
@@ -151,11 +154,8 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
   };
-  auto step = [&](int s, const uint8_t *gc, const uint8_t *wc_, uint8_t *gn, uint8_t *wn_, const Set &t, Set &t2) {
-    Frag f0, f1;
-    read_f(f0, gc, wc_, 0);
-    issue_g(gn, min(s + 1, last));
-    __builtin_amdgcn_sched_barrier(0);
+  auto step = [&](int s, uint8_t *gc, const uint8_t *wc_, const uint8_t *gn, uint8_t *wn_, Frag &f0, Frag &f1,
+                  const Set &t, Set &t2) {
     Set nt;
     load_w(nt, min(s + 2, last));
     __builtin_amdgcn_sched_barrier(0);
@@ -163,22 +163,25 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     __builtin_amdgcn_sched_barrier(0);
     mma(f0);
     expand(t, 0, wn_);
+    expand(t, 1, wn_);
     __builtin_amdgcn_sched_barrier(0);
     read_f(f0, gc, wc_, 2);
     __builtin_amdgcn_sched_barrier(0);
     mma(f1);
-    expand(t, 1, wn_);
+    expand(t, 2, wn_);
     __builtin_amdgcn_sched_barrier(0);
     read_f(f1, gc, wc_, 3);
     __builtin_amdgcn_sched_barrier(0);
     mma(f0);
-    expand(t, 2, wn_);
-    __builtin_amdgcn_sched_barrier(0);
-    mma(f1);
     expand(t, 3, wn_);
     __builtin_amdgcn_sched_barrier(0);
     t2 = nt;
     stage_barrier<2>();
+    read_f(f0, gn, wn_, 0);
+    issue_g(gc, min(s + 2, last));
+    __builtin_amdgcn_sched_barrier(0);
+    mma(f1);
+    __builtin_amdgcn_sched_barrier(0);
   };
   Set t0, t1;
   load_w(t0, s0);
@@ -189,11 +192,18 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) expand(t0, q, ws0);
   stage_barrier<2>();
+  Frag f0, f1;
+  issue_g(gs1, min(s0 + 1, last));
+  __builtin_amdgcn_sched_barrier(0);
+  read_f(f0, gs0, ws0, 0);
   for (int s = s0; s < s1; s += 2) {
-    step(s, gs0, ws0, gs1, ws1, t1, t0);
+    step(s, gs0, ws0, gs1, ws1, f0, f1, t1, t0);
     if (s + 1 >= s1) break;
-    step(s + 1, gs1, ws1, gs0, ws0, t0, t1);
+    step(s + 1, gs1, ws1, gs0, ws0, f0, f1, t0, t1);
   }
+  // The loads past the end must land, and the last reads past it end, before the
+  // stages are written again.
+  stage_barrier();
 
   const int64_t row0 = m0 + wr * 32 * TM, colw = k0 + 32 * UW * wc;   // the wave's first row and column
   // dX column (from k0) of the wave's tile column x.
