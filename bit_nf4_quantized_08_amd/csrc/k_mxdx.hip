@@ -47,7 +47,7 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
   static_assert(WR * WC == 8 && TN * WC == 8, "8 waves over 256 columns");
   constexpr int BM = 32 * TM * WR, UW = 8 / WC;
   constexpr int GL = BM / 64;   // direct loads (8 rows each) per wave and step
-  static_assert(GL >= 1, "stage loads");
+  static_assert(GL >= 1 && GL <= 4, "stage loads");
   constexpr int kPitch = 32 * TN + 8;   // bf16 per row of a store block
   __shared__ __attribute__((aligned(16))) uint8_t gs0[BM * 128];
   __shared__ __attribute__((aligned(16))) uint8_t gs1[BM * 128];
@@ -72,10 +72,8 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     const int row = 8 * (wave * GL + i) + (lane >> 3);
     go[i] = (uint32_t)(row * a.N * 2 + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
   }
-  auto issue_g = [&](uint8_t *dst, int s) {
-    const uint32_t b = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(dst)) + wave * GL * 1024;
-#pragma unroll
-    for (int i = 0; i < GL; ++i) load_lds16(rg, b + i * 1024, go[i], s * 128);
+  auto issue_g = [&](uint8_t *dst, int s, int i) {
+    load_lds16(rg, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(dst)) + wave * GL * 1024 + i * 1024, go[i], s * 128);
   };
   // W: thread (n, ch) of a step.
   const int64_t C = (a.K + 255) / 256, pitch = 128 * C;
@@ -148,44 +146,52 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) f.b[j] = read_w(wst_, j, c);
   };
-  auto mma = [&](const Frag &f) {
+  // A sub-step's MFMAs, with hook(0) .. hook(3) spread between them.
+  auto mma = [&](const Frag &f, auto &&hook) {
+    constexpr int n = TM * TN, per = n >= 4 ? n / 4 : 1;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+    for (int m = 0; m < n; ++m) {
+      const int i = m / TN, j = m % TN;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+      if (m % per == per - 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        hook(m / per);
+        if (n < 4) hook(m + n);   // two MFMAs: two hooks after each
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
   };
   auto step = [&](int s, uint8_t *gc, const uint8_t *wc_, const uint8_t *gn, uint8_t *wn_, Frag &f0, Frag &f1,
                   const Set &t, Set &t2) {
     Set nt;
-    load_w(nt, min(s + 2, last));
-    __builtin_amdgcn_sched_barrier(0);
     read_f(f1, gc, wc_, 1);
     __builtin_amdgcn_sched_barrier(0);
-    mma(f0);
-    expand(t, 0, wn_);
-    expand(t, 1, wn_);
-    __builtin_amdgcn_sched_barrier(0);
+    mma(f0, [&](int q) {
+      if (q == 0) load_w(nt, min(s + 2, last));
+      if (q == 1) expand(t, 0, wn_);
+      if (q == 3) expand(t, 1, wn_);
+    });
     read_f(f0, gc, wc_, 2);
     __builtin_amdgcn_sched_barrier(0);
-    mma(f1);
-    expand(t, 2, wn_);
-    __builtin_amdgcn_sched_barrier(0);
+    mma(f1, [&](int q) {
+      if (q == 1) expand(t, 2, wn_);
+      if (q == 3) expand(t, 3, wn_);
+    });
     read_f(f1, gc, wc_, 3);
     __builtin_amdgcn_sched_barrier(0);
-    mma(f0);
-    expand(t, 3, wn_);
-    __builtin_amdgcn_sched_barrier(0);
+    mma(f0, [](int) {});
     t2 = nt;
     stage_barrier<2>();
     read_f(f0, gn, wn_, 0);
-    issue_g(gc, min(s + 2, last));
     __builtin_amdgcn_sched_barrier(0);
-    mma(f1);
-    __builtin_amdgcn_sched_barrier(0);
+    mma(f1, [&](int q) {
+      if (q < GL) issue_g(gc, min(s + 2, last), q);
+    });
   };
   Set t0, t1;
   load_w(t0, s0);
-  issue_g(gs0, s0);
+#pragma unroll
+  for (int i = 0; i < GL; ++i) issue_g(gs0, s0, i);
   __builtin_amdgcn_sched_barrier(0);
   load_w(t1, min(s0 + 1, last));
   __builtin_amdgcn_sched_barrier(0);
@@ -193,7 +199,8 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
   for (int q = 0; q < 4; ++q) expand(t0, q, ws0);
   stage_barrier<2>();
   Frag f0, f1;
-  issue_g(gs1, min(s0 + 1, last));
+#pragma unroll
+  for (int i = 0; i < GL; ++i) issue_g(gs1, min(s0 + 1, last), i);
   __builtin_amdgcn_sched_barrier(0);
   read_f(f0, gs0, ws0, 0);
   for (int s = s0; s < s1; s += 2) {
@@ -397,7 +404,7 @@ hipError_t launch_mx_dx(const MxDxArgs &in, hipStream_t st) {
   MxDxArgs a = in;
   const DxPlan p = dx_plan(a.M, a.N, a.K);
   a.splits = p.splits;
-  if (p.big) return launch_tiles<2, 4, 4, 2>(a, st);
+  if (p.big) return launch_tiles<4, 2, 2, 4>(a, st);
   const hipError_t e = launch_tiles<1, 2, 2, 4>(a, st);
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL(mx_dx_finish_kernel, dim3((unsigned)cdiv(a.M * (a.K / 8), 256)), dim3(256), 0, st, a);
