@@ -29,11 +29,18 @@
 // generator of qn_philox.h, so each lane masks the pieces it loaded, in
 // registers, before they go to LDS; the kept values stay unscaled bf16 and the
 // factor 1/(1-p) is applied to the fp32 sums, so dropout adds no rounding.
+//
+// Quantisation of L to MXFP4 in the same pass (the MXFP4 linear's activations):
+// the piece is also a quarter of a 32-element block, its quad holds the block, and the
+// LR_DEPTH steps of a loop turn are one 256-column chunk, whose eight scale
+// bytes of a row are collected and stored together.  The ranges then start at
+// whole chunks.  Against a quantisation pass of its own, X is read once.
 
 #include <algorithm>
 
 #include "qn_device.h"
 #include "qn_internal.h"
+#include "qn_mx.h"
 #include "qn_philox.h"
 
 namespace qn {
@@ -68,8 +75,8 @@ struct LowRankGroup {
 };
 
 // RT: 32-column tiles of the factor, R <= 32 * RT.  DROP: some product of the
-// launch drops elements of its L.
-template <int RT, bool DROP>
+// launch drops elements of its L.  QUANT: L is quantised too (one product).
+template <int RT, bool DROP, bool QUANT>
 __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup grp) {
   __shared__ __attribute__((aligned(16))) uint8_t ps[2][32 * RT * LR_PITCH];
   __shared__ __attribute__((aligned(16))) uint8_t xs[LR_THREADS / 64][32 * 128];   // each wave's L slab
@@ -83,7 +90,8 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
   const int lr = lane & 31, lh = lane >> 5;
 
   const int64_t steps = a.Kc / LR_CK;
-  const int64_t per = (steps + S - 1) / S;
+  static_assert(LR_DEPTH * LR_CK == QN_MX_CHUNK, "a loop turn is a chunk");
+  const int64_t per = QUANT ? ((steps + LR_DEPTH - 1) / LR_DEPTH + S - 1) / S * LR_DEPTH : (steps + S - 1) / S;
   const int64_t c0 = std::min<int64_t>(steps, (int64_t)s * per), c1 = std::min<int64_t>(steps, c0 + per);
 
   // L: load i of a step brings rows 8i .. 8i + 7 of the wave's 32, eight lanes
@@ -155,6 +163,10 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
   // Step cb + d reads register slot d and LDS buffer d & 1 (LR_DEPTH is even).
   static_assert(LR_DEPTH % 2 == 0, "LDS buffer parity follows the slot");
   const int64_t n = c1 - c0;
+  uint32_t qb[4] = {};
+  const int64_t qpitch = (a.Kc + QN_MX_CHUNK - 1) / QN_MX_CHUNK * (QN_MX_CHUNK / 8);   // dwords per row of codes
+  (void)qb;
+  (void)qpitch;
   if (n > 0) {
     const int64_t np = (n + LR_DEPTH - 1) / LR_DEPTH * LR_DEPTH;
 #pragma unroll
@@ -165,6 +177,17 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
 #pragma unroll
       for (int d = 0; d < LR_DEPTH; ++d) {
         const uint8_t *pb = ps[d & 1];
+        if constexpr (QUANT) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const u32x4 u[1] = {xr[d][i]};
+            const uint32_t b = scale_byte<true>(quad_max(unit_amax<true>(u)));
+            qb[i] = d == 0 ? b : qb[i] | b << (8 * d);
+            const int64_t m = m0 + 32 * wave + 8 * i + (lane >> 3);
+            if (m < a.M)
+              reinterpret_cast<uint32_t *>(a.qc)[m * qpitch + (c0 + cb + d) * (LR_CK / 8) + (lane & 7)] = unit_codes<true>(u, b);
+          }
+        }
         if constexpr (DROP) {
           if (dropping) {
 #pragma unroll
@@ -193,6 +216,18 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
         load_step(d, c0 + cb + d + LR_DEPTH);
         stage((d + 1) % LR_DEPTH, (d + 1) & 1);
         __syncthreads();
+      }
+      if constexpr (QUANT) {
+        // qb: the first quad of a row's eight lanes holds the even blocks' bytes
+        // of the chunk, the second the odd ones'.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t odd = (uint32_t)__builtin_amdgcn_ds_bpermute((lane | 4) * 4, (int)qb[i]);
+          const int64_t m = m0 + 32 * wave + 8 * i + (lane >> 3);
+          if ((lane & 7) == 0 && m < a.M)
+            *reinterpret_cast<u32x2 *>(a.qs + (((c0 + cb) / LR_DEPTH) * a.M + m) * 8) =
+                u32x2{__builtin_amdgcn_perm(odd, qb[i], 0x05010400u), __builtin_amdgcn_perm(odd, qb[i], 0x07030602u)};
+        }
       }
     }
   }
@@ -303,12 +338,15 @@ hipError_t launch_lowrank_group(const LowRankArgs *a, int n, bool finish, hipStr
   {
     TraceScope tr(QN_TRACE_LOWRANK, st);
     const dim3 grid((unsigned)wgs, (unsigned)n);
-    if (drop) {
-      if (R <= 32) hipLaunchKernelGGL((lowrank_part_kernel<1, true>), grid, dim3(LR_THREADS), 0, st, grp);
-      else hipLaunchKernelGGL((lowrank_part_kernel<2, true>), grid, dim3(LR_THREADS), 0, st, grp);
+    const bool quant = a[0].qc != nullptr;
+    if (quant && n != 1) return hipErrorInvalidValue;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(LR_THREADS), 0, st, grp); };
+    if (R <= 32) {
+      if (quant) drop ? go(lowrank_part_kernel<1, true, true>) : go(lowrank_part_kernel<1, false, true>);
+      else drop ? go(lowrank_part_kernel<1, true, false>) : go(lowrank_part_kernel<1, false, false>);
     } else {
-      if (R <= 32) hipLaunchKernelGGL((lowrank_part_kernel<1, false>), grid, dim3(LR_THREADS), 0, st, grp);
-      else hipLaunchKernelGGL((lowrank_part_kernel<2, false>), grid, dim3(LR_THREADS), 0, st, grp);
+      if (quant) drop ? go(lowrank_part_kernel<2, true, true>) : go(lowrank_part_kernel<2, false, true>);
+      else drop ? go(lowrank_part_kernel<2, true, false>) : go(lowrank_part_kernel<2, false, false>);
     }
   }
   hipError_t e = hipGetLastError();

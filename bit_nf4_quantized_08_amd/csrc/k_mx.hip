@@ -19,13 +19,13 @@
 
 #include <algorithm>
 
+#include "qn_mx.h"
 #include "qn_philox.h"
 #include "qn_tile.h"
 
 namespace qn {
 namespace {
 
-typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -51,70 +51,10 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, FastDiv f) { return (__um
 // ------------------------------------------------------------------ codec
 // Unit u of a matrix: 8 consecutive columns of one row, 32 units per 256-column
 // chunk, chunks of a row together.  A lane owns one unit, a quad of lanes one
-// block: the block's largest magnitude is an integer maximum of the absolute
-// bit patterns (two DPP steps), whose exponent field gives the scale byte
-// directly; the hardware conversion rounds x 2^-e to E2M1 (nearest even,
-// saturating), the same rule bit for bit, subnormal inputs included.  Each
-// thread takes kUnits units a workgroup apart, loads first.
+// block (qn_mx.h).  Each thread takes kUnits units a workgroup apart, loads
+// first.
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;
-
-// dword t of v (a vector of four dwords per register quad).
-template <int N>
-__device__ __forceinline__ uint32_t dw(const u32x4 (&v)[N], int t) {
-  const uint32_t w[4] = {v[t >> 2].x, v[t >> 2].y, v[t >> 2].z, v[t >> 2].w};
-  return w[t & 3];
-}
-
-// Largest absolute bit pattern of a unit: bf16 pairs packed (result in 16 bits)
-// or fp32.
-template <bool BF16>
-__device__ __forceinline__ uint32_t unit_amax(const u32x4 (&x)[BF16 ? 1 : 2]) {
-  if constexpr (BF16) {
-    u16x2 m = {0, 0};
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, dw(x, t) & 0x7FFF7FFFu));
-    return m.x > m.y ? m.x : m.y;
-  } else {
-    uint32_t m = 0;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) m = max(m, dw(x, t) & 0x7FFFFFFFu);
-    return m;
-  }
-}
-
-// Scale byte of a block from its largest absolute bit pattern: the exponent
-// field less 2, at least 0; 255 for a block that is not finite.
-template <bool BF16>
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
-  const uint32_t e = amax >> (BF16 ? 7 : 23);
-  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
-}
-
-// The unit's eight codes (one dword) under a scale byte.
-template <bool BF16>
-__device__ __forceinline__ uint32_t unit_codes(const u32x4 (&x)[BF16 ? 1 : 2], uint32_t byte) {
-  const float sc = as_f32(byte << 23);   // the conversion reads the exponent field; 0 stands for 2^-127
-  uint32_t c = 0;
-  if constexpr (BF16) {
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 0)), sc, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 1)), sc, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 2)), sc, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2v, dw(x, 3)), sc, 3);
-  } else {
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 0)), as_f32(dw(x, 1)), sc, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 2)), as_f32(dw(x, 3)), sc, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 4)), as_f32(dw(x, 5)), sc, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_f32(dw(x, 6)), as_f32(dw(x, 7)), sc, 3);
-  }
-  return byte == 255u ? 0u : c;
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
-}
 
 // VEC: cols is a multiple of 8, so that a unit is aligned and whole.  T threads
 // take chunks `first` .. of the matrix, U units each.
@@ -156,10 +96,7 @@ __device__ __forceinline__ void quantize_units(const uint8_t *__restrict__ x, ui
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    uint32_t m = unit_amax<BF16>(v[i]);
-    m = max(m, dpp<0xB1>(m));
-    m = max(m, dpp<0x4E>(m));
-    const uint32_t b = scale_byte<BF16>(m);
+    const uint32_t b = scale_byte<BF16>(quad_max(unit_amax<BF16>(v[i])));
     const uint32_t c = c0 + i * (T / 32);
     if (c < chunks) {
       reinterpret_cast<uint32_t *>(codes)[(int64_t)c * 32 + (tid & 31)] = unit_codes<BF16>(v[i], b);
@@ -1006,12 +943,15 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
   if (a.M <= kDecodeRows) return run_decode(a, w, st);
   const int64_t C = mx_chunks(a.K);
   const GemmPlan p = gemm_plan(a.M, a.N, C);
-  QN_TRY(launch_mx_quantize(a.X, 1, a.M, a.K, w.xc, w.xs, st));
-  if (a.r) {
+  if (a.r == 0) {
+    QN_TRY(launch_mx_quantize(a.X, 1, a.M, a.K, w.xc, w.xs, st));
+  } else {   // one pass over X: its low-rank product and its quantisation
+
     LowRankArgs l{};
     l.L = a.X; l.ldl = a.K; l.M = a.M; l.Kc = a.K;
     l.P = a.A; l.ldp = a.K; l.R = a.r; l.scale = a.s; l.drop = a.drop;
     l.Mp = a.M; l.part = w.h_part;
+    l.qc = w.xc; l.qs = w.xs;
     l.out_f32 = a.H_out;
     l.out_b = w.sH;
     l.ldb = 64;

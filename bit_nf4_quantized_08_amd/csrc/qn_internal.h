@@ -182,6 +182,8 @@ struct LowRankArgs {
   float *part;
   int splits;   // set by the launcher
   DropArgs drop = kNoDrop;   // thr > 0: L is read as keep * L and C scaled by c
+  uint8_t *qc = nullptr;     // non-null (a launch of one product): MXFP4 of L (before dropout) is written
+  uint8_t *qs = nullptr;     // too, codes [M, 128 C] and scales [C][M][8]
 };
 int lowrank_splits(int64_t M, int64_t Kc);
 size_t lowrank_part_bytes(int64_t M, int64_t Kc, int64_t R);
