@@ -22,6 +22,7 @@
 
 #include <algorithm>
 
+#include "qn_colsum.h"
 #include "qn_philox.h"
 #include "qn_tile.h"
 
@@ -155,38 +156,9 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
     }
 }
 
-// out = bf16(c * sum of the ranges), as [R][Ncols] or transposed [Ncols][R]: a
-// workgroup owns 64 columns and up to 64 ranks, loads them along the columns
-// and stores along whichever is contiguous, through LDS.
 __global__ __launch_bounds__(256) void colsum_reduce_kernel(ColSumArgs a0, ColSumArgs a1) {
-  __shared__ float tile[64][65];
-  const ColSumArgs &a = blockIdx.y ? a1 : a0;
-  const int64_t c0 = (int64_t)blockIdx.x * 64;
-  if (c0 >= a.Ncols) return;
-  const int tid = threadIdx.x, cl = tid & 63;
-  const int R = (int)a.R;
-  const int64_t stride = a.R * a.Ncols;
-  const int j0 = (int)blockIdx.z * 16, j1 = min(R, j0 + 16);   // ranks of this workgroup
-  if (j0 >= R) return;
-  for (int j = j0 + (tid >> 6); j < j1; j += 4) {
-    const float *p = a.part + (int64_t)j * a.Ncols + c0 + cl;   // Ncols % 64 == 0
-    float v = 0.0f;
-    for (int q0 = 0; q0 < a.splits; q0 += 8) {
-      float x[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = p[(int64_t)min(q0 + q, a.splits - 1) * stride];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q0 + q < a.splits) v += x[q];
-    }
-    v *= a.drop.c;
-    if (a.transpose) tile[cl][j - j0] = v;
-    else a.out[(int64_t)j * a.Ncols + c0 + cl] = f32_to_bf16(v);
-  }
-  if (!a.transpose) return;
-  __syncthreads();
-  const int w = j1 - j0;
-  for (int i = tid; i < 64 * w; i += 256) a.out[(c0 + i / w) * a.R + j0 + i % w] = f32_to_bf16(tile[i / w][i % w]);
+  __shared__ float tile[64 * 17];
+  colsum_reduce(blockIdx.y ? a1 : a0, (int)blockIdx.x, tile);
 }
 
 }  // namespace
@@ -213,10 +185,12 @@ hipError_t launch_colsum2(const ColSumArgs &a, const ColSumArgs &b, hipStream_t 
       else hipLaunchKernelGGL((colsum_kernel<2, false>), grid, block, 0, st, a, b);
     }
   }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(colsum_reduce_kernel, dim3((unsigned)(ncols / 64), 2u, (unsigned)((R + 15) / 16)), dim3(256), 0, st,
-                     a, b);
+  return hipGetLastError();
+}
+
+hipError_t launch_colsum_reduce(const ColSumArgs &a, const ColSumArgs &b, hipStream_t st) {
+  const dim3 grid((unsigned)std::max(colsum_reduce_blocks(a), colsum_reduce_blocks(b)), 2u);
+  hipLaunchKernelGGL(colsum_reduce_kernel, grid, dim3(256), 0, st, a, b);
   return hipGetLastError();
 }
 

@@ -770,7 +770,7 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   if (a.r == 0) {
     MxDxArgs x{a.dY, a.M, a.N, a.K, a.codes, a.mx_scales, nullptr, 0, nullptr, 0, kNoDrop, a.dX,
                static_cast<float *>(a.ws), 0};
-    return a.dX ? launch_mx_dx(x, st) : hipSuccess;
+    return a.dX ? launch_mx_dx(x, nullptr, st) : hipSuccess;
   }
   Carve c(a.ws);
   const int64_t rp = align_up(a.r, 32);
@@ -784,9 +784,10 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   float *dhpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(a.M, a.N, a.r)));
   float *hpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(a.M, a.K, a.r)));
 
+  const bool fused = a.mx_scales || a.drop.thr;   // the newer paths: B read as it is, sums on the matrix cores
   // B^T [rp, N] (rows >= r zero) so that dH = dY (B^T)^T runs on the low-rank
   // kernel; with the forward's H given, (sH)^T from it in the same launch.
-  {
+  if (!fused) {
     const int64_t elems = rp * a.N + (a.H ? rp * Mp : 0);
     hipLaunchKernelGGL(bwd_prep_kernel, dim3((unsigned)cdiv(elems, kThreads)), dim3(kThreads), 0, st, a.B, a.N,
                        a.r, rp, Bt, a.H, a.M, Mp, a.s, sHt);
@@ -802,17 +803,26 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     lh.L = a.X; lh.ldl = a.K; lh.M = a.M; lh.Kc = a.K;
     lh.P = a.A; lh.ldp = a.K; lh.R = a.r; lh.scale = a.s; lh.drop = a.drop;
     lh.out_t = sHt; lh.ldt_rows = rp; lh.Mp = Mp; lh.part = hpart;
-    QN_TRY(launch_lowrank2(ld, a.H ? nullptr : &lh, st));
+    if (fused) {
+      ld.P = a.B;
+      ld.p_transposed = true;
+      lh.given = a.H;   // (sH)^T from it, or H formed here
+      QN_TRY(launch_lowrank2(ld, &lh, st));
+    } else {
+      QN_TRY(launch_lowrank2(ld, a.H ? nullptr : &lh, st));
+    }
   }
 
   // One launch: dB [N, r] = ((sH)^T dY)^T and dA [r, K] = dH^T X, contractions over
   // M: on the matrix cores for the MXFP4 base and under dropout; without either
   // the vector kernel, whose sums (and so whose results) those calls keep.
-  if (a.mx_scales || a.drop.thr) {
+  ColSumArgs sums[2];
+  if (fused) {
     const int splits = colsum_splits(a.M, a.N + a.K);
-    const ColSumArgs cb{sHt, Mp, a.dY, a.M, a.N, a.r, bpart, splits, a.dB, true, kNoDrop};
-    const ColSumArgs ca{dHt, Mp, a.X, a.M, a.K, a.r, apart, splits, a.dA, false, a.drop};
-    QN_TRY(launch_colsum2(cb, ca, st, QN_TRACE_GEMM_DB));
+    sums[0] = ColSumArgs{sHt, Mp, a.dY, a.M, a.N, a.r, bpart, splits, a.dB, true, kNoDrop};
+    sums[1] = ColSumArgs{dHt, Mp, a.X, a.M, a.K, a.r, apart, splits, a.dA, false, a.drop};
+    QN_TRY(launch_colsum2(sums[0], sums[1], st, QN_TRACE_GEMM_DB));
+    if (!a.dX || !a.mx_scales) QN_TRY(launch_colsum_reduce(sums[0], sums[1], st));
   } else {
     ColRedArgs cb{}, ca{};
     cb.Lt = sHt; cb.Mp = Mp; cb.Q = a.dY; cb.ldq = a.N; cb.M = a.M; cb.Ncols = a.N; cb.R = a.r;
@@ -825,7 +835,7 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   if (a.dX && a.mx_scales) {
     MxDxArgs x{a.dY, a.M, a.N, a.K, a.codes, a.mx_scales, dHb, rp, a.A, a.r, a.drop, a.dX,
                reinterpret_cast<float *>(c.take<char>((int64_t)mx_dx_part_bytes(a.M, a.N, a.K))), 0};
-    return launch_mx_dx(x, st);
+    return launch_mx_dx(x, sums, st);
   }
   if (a.dX) {
     QGemmArgs g{};

@@ -76,7 +76,10 @@ struct LowRankGroup {
 
 // RT: 32-column tiles of the factor, R <= 32 * RT.  DROP: some product of the
 // launch drops elements of its L.  QUANT: L is quantised too (one product).
-template <int RT, bool DROP, bool QUANT>
+// PT: some product's factor is given transposed (P is [Kc, R], as B is for dH =
+// dY B): its 64 x R slab is loaded along its rows and written to the staged
+// layout two bytes at a time, which saves a launch that would transpose it.
+template <int RT, bool DROP, bool QUANT, bool PT>
 __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup grp) {
   __shared__ __attribute__((aligned(16))) uint8_t ps[2][32 * RT * LR_PITCH];
   __shared__ __attribute__((aligned(16))) uint8_t xs[LR_THREADS / 64][32 * 128];   // each wave's L slab
@@ -124,14 +127,24 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
   }
   // P: thread t moves 16-byte unit (t & 7) of rows t / 8 + 32 i, i < RT (rows
   // past R read zeros).
-  const rsrc_t rp = make_rsrc(a.P, a.R * a.ldp * 2);
+  // PT: thread t moves ranks 8 (u / 64) .. + 7 of row u % 64, u = t + 256 i, of the
+  // step's 64: a wave's lanes take one rank of 64 consecutive rows, side by side
+  // in LDS (a rank count that is not a multiple of 8 is loaded by elements).
+  const bool pt = PT && a.p_transposed, ptv = (a.R & 7) == 0;
+  const rsrc_t rp = make_rsrc(a.P, pt ? a.Kc * a.R * 2 : a.R * a.ldp * 2);
   uint32_t pvoff[RT], pls[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int j = tid / 8 + 32 * i, u = tid & 7;
     pvoff[i] = j < a.R ? (uint32_t)(j * a.ldp * 2 + 16 * u) : kOutOfRange;
     pls[i] = (uint32_t)(j * LR_PITCH + 16 * u);
+    if (pt) {
+      const int v = tid + 256 * i, row = v & 63, j0 = 8 * (v >> 6);
+      pvoff[i] = j0 < a.R ? (uint32_t)((row * a.R + j0) * 2) : kOutOfRange;
+      pls[i] = (uint32_t)(j0 * LR_PITCH + 2 * row);
+    }
   }
+  const int pstep = (int)(pt ? LR_CK * a.R * 2 : LR_CK * 2);   // bytes per step
 
   u32x4 xr[LR_DEPTH][4];
   u32x4 pr[LR_DEPTH][RT];
@@ -143,12 +156,38 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
     for (int i = 0; i < 4; ++i)
       xr[slot][i] = __builtin_amdgcn_raw_buffer_load_b128(rl, in ? lvo[i] : kOutOfRange, soff, 0);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-      pr[slot][i] = __builtin_amdgcn_raw_buffer_load_b128(rp, in ? pvoff[i] : kOutOfRange, soff, 0);
+    for (int i = 0; i < RT; ++i) {
+      if (PT && pt && !ptv) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t h[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool ok = in && pvoff[i] != kOutOfRange && (int)(pls[i] / LR_PITCH) + 2 * q + e < a.R;
+            h[e] = __builtin_amdgcn_raw_buffer_load_b16(rp, ok ? pvoff[i] + 4 * q + 2 * e : kOutOfRange, in ? (int)(c * pstep) : 0, 0);
+          }
+          w[q] = (h[0] & 0xFFFFu) | h[1] << 16;
+        }
+        pr[slot][i] = u32x4{w[0], w[1], w[2], w[3]};
+      } else {
+        pr[slot][i] = __builtin_amdgcn_raw_buffer_load_b128(rp, in ? pvoff[i] : kOutOfRange,
+                                                            PT ? (in ? (int)(c * pstep) : 0) : soff, 0);
+      }
+    }
   };
   auto stage = [&](int slot, int buf) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) *reinterpret_cast<u32x4 *>(&ps[buf][pls[i]]) = pr[slot][i];
+    for (int i = 0; i < RT; ++i) {
+      if (PT && pt) {
+        const uint32_t w[4] = {pr[slot][i].x, pr[slot][i].y, pr[slot][i].z, pr[slot][i].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint16_t *>(&ps[buf][pls[i] + e * LR_PITCH]) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      } else {
+        *reinterpret_cast<u32x4 *>(&ps[buf][pls[i]]) = pr[slot][i];
+      }
+    }
   };
 
   f32x16 acc[RT];
@@ -263,8 +302,10 @@ __global__ __launch_bounds__(256) void lowrank_finish_kernel(LowRankGroup grp) {
   const int64_t m0 = (int64_t)blockIdx.x * FIN_ROWS;
   if (m0 >= lowrank_rows(a)) return;
   const int tid = threadIdx.x;
-  const int64_t Rp = align32(a.R), plane = a.M * Rp;
-  const int S = a.splits;
+  // A given product is its own, dense, only partial sum.
+  const int64_t Rp = a.given ? a.R : align32(a.R), plane = a.M * Rp;
+  const int S = a.given ? 1 : a.splits;
+  const float *part = a.given ? a.given : a.part;
   // The loads carry no condition, so that they all issue before the first
   // wait: lanes outside the problem read the first element of each range, and
   // slots past the last range re-read the last one; both are discarded.
@@ -275,7 +316,7 @@ __global__ __launch_bounds__(256) void lowrank_finish_kernel(LowRankGroup grp) {
     const int e = tid + 256 * i, r = e / RW, j = e % RW;
     const int64_t m = m0 + r;
     in[i] = m < a.M && j < a.R;
-    const float *p = a.part + (in[i] ? m * Rp + j : 0);
+    const float *p = part + (in[i] ? m * Rp + j : 0);
 #pragma unroll
     for (int s = 0; s < LR_MAX_SPLITS; ++s) pv[i][s] = p[(int64_t)min(s, S - 1) * plane];
   }
@@ -286,7 +327,7 @@ __global__ __launch_bounds__(256) void lowrank_finish_kernel(LowRankGroup grp) {
 #pragma unroll
     for (int s = 0; s < LR_MAX_SPLITS; ++s)
       if (s < S) v += pv[i][s];
-    tile[r][j] = in[i] ? v * a.drop.c : 0.0f;   // c = 1 without dropout
+    tile[r][j] = in[i] ? v * (a.given ? 1.0f : a.drop.c) : 0.0f;   // c = 1 without dropout
   }
   __syncthreads();
   for (int idx = tid; idx < FIN_ROWS * 64; idx += 256) {
@@ -326,27 +367,37 @@ hipError_t launch_lowrank_group(const LowRankArgs *a, int n, bool finish, hipStr
   if (n < 1 || n > QN_MAX_GROUP) return hipErrorInvalidValue;
   LowRankGroup grp{};
   int64_t wgs = 0, fin = 0, R = 0;
-  bool drop = false;
+  bool drop = false, pt = false;
+  int np = 0;   // products to form; given ones (finished only) come last
   for (int i = 0; i < n; ++i) {
     grp.p[i] = a[i];
     grp.p[i].splits = lowrank_splits(a[i].M, a[i].Kc);
-    wgs = std::max<int64_t>(wgs, (a[i].M + LR_BM - 1) / LR_BM * grp.p[i].splits);
+    if (!a[i].given) {
+      if (np != i) return hipErrorInvalidValue;
+      ++np;
+      wgs = std::max<int64_t>(wgs, (a[i].M + LR_BM - 1) / LR_BM * grp.p[i].splits);
+    }
     fin = std::max<int64_t>(fin, (lowrank_rows(a[i]) + FIN_ROWS - 1) / FIN_ROWS);
     R = std::max(R, a[i].R);
-    drop = drop || a[i].drop.thr != 0;
+    drop = drop || (!a[i].given && a[i].drop.thr != 0);
+    pt = pt || a[i].p_transposed;
   }
+  if (np < 1) return hipErrorInvalidValue;
   {
     TraceScope tr(QN_TRACE_LOWRANK, st);
-    const dim3 grid((unsigned)wgs, (unsigned)n);
+    const dim3 grid((unsigned)wgs, (unsigned)np);
     const bool quant = a[0].qc != nullptr;
     if (quant && n != 1) return hipErrorInvalidValue;
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(LR_THREADS), 0, st, grp); };
+    if (quant && pt) return hipErrorInvalidValue;
     if (R <= 32) {
-      if (quant) drop ? go(lowrank_part_kernel<1, true, true>) : go(lowrank_part_kernel<1, false, true>);
-      else drop ? go(lowrank_part_kernel<1, true, false>) : go(lowrank_part_kernel<1, false, false>);
+      if (quant) drop ? go(lowrank_part_kernel<1, true, true, false>) : go(lowrank_part_kernel<1, false, true, false>);
+      else if (pt) drop ? go(lowrank_part_kernel<1, true, false, true>) : go(lowrank_part_kernel<1, false, false, true>);
+      else drop ? go(lowrank_part_kernel<1, true, false, false>) : go(lowrank_part_kernel<1, false, false, false>);
     } else {
-      if (quant) drop ? go(lowrank_part_kernel<2, true, true>) : go(lowrank_part_kernel<2, false, true>);
-      else drop ? go(lowrank_part_kernel<2, true, false>) : go(lowrank_part_kernel<2, false, false>);
+      if (quant) drop ? go(lowrank_part_kernel<2, true, true, false>) : go(lowrank_part_kernel<2, false, true, false>);
+      else if (pt) drop ? go(lowrank_part_kernel<2, true, false, true>) : go(lowrank_part_kernel<2, false, false, true>);
+      else drop ? go(lowrank_part_kernel<2, true, false, false>) : go(lowrank_part_kernel<2, false, false, false>);
     }
   }
   hipError_t e = hipGetLastError();

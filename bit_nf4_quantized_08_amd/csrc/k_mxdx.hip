@@ -30,6 +30,7 @@
 
 #include <algorithm>
 
+#include "qn_colsum.h"
 #include "qn_philox.h"
 #include "qn_tile.h"
 
@@ -315,8 +316,15 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
 }
 
 // dX = bf16(sum of the splits' partial products + the adapter term), one thread
-// per 8 columns (one generator call).
-__global__ __launch_bounds__(256) void mx_dx_finish_kernel(MxDxArgs a) {
+// per 8 columns (one generator call).  The workgroups past dX's (`blocks`) reduce
+// the call's two column sums: launches are what a small call costs.
+__global__ __launch_bounds__(256) void mx_dx_finish_kernel(MxDxArgs a, ColSumArgs c0, ColSumArgs c1, int blocks) {
+  __shared__ float tile[64 * 17];
+  if ((int)blockIdx.x >= blocks) {
+    const int b = (int)blockIdx.x - blocks, n0 = (int)colsum_reduce_blocks(c0);
+    colsum_reduce(b < n0 ? c0 : c1, b < n0 ? b : b - n0, tile);
+    return;
+  }
   const int64_t per = a.K / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= a.M * per) return;
   const int64_t m = i / per, k = 8 * (i % per);
@@ -400,14 +408,18 @@ size_t mx_dx_part_bytes(int64_t M, int64_t N, int64_t K) {
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)K * sizeof(float) : 0;
 }
 
-hipError_t launch_mx_dx(const MxDxArgs &in, hipStream_t st) {
+hipError_t launch_mx_dx(const MxDxArgs &in, const ColSumArgs *sums, hipStream_t st) {
   MxDxArgs a = in;
   const DxPlan p = dx_plan(a.M, a.N, a.K);
   a.splits = p.splits;
-  if (p.big) return launch_tiles<4, 2, 2, 4>(a, st);
-  const hipError_t e = launch_tiles<1, 2, 2, 4>(a, st);
-  if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(mx_dx_finish_kernel, dim3((unsigned)cdiv(a.M * (a.K / 8), 256)), dim3(256), 0, st, a);
+  const hipError_t e = p.big ? launch_tiles<4, 2, 2, 4>(a, st) : launch_tiles<1, 2, 2, 4>(a, st);
+  if (e != hipSuccess) return e;
+  if (p.splits == 1) return sums ? launch_colsum_reduce(sums[0], sums[1], st) : hipSuccess;
+  const int blocks = (int)cdiv(a.M * (a.K / 8), 256);
+  const ColSumArgs none{};
+  const int64_t more = sums ? colsum_reduce_blocks(sums[0]) + colsum_reduce_blocks(sums[1]) : 0;
+  hipLaunchKernelGGL(mx_dx_finish_kernel, dim3((unsigned)(blocks + more)), dim3(256), 0, st, a, sums ? sums[0] : none,
+                     sums ? sums[1] : none, blocks);
   return hipGetLastError();
 }
 

@@ -184,6 +184,8 @@ struct LowRankArgs {
   DropArgs drop = kNoDrop;   // thr > 0: L is read as keep * L and C scaled by c
   uint8_t *qc = nullptr;     // non-null (a launch of one product): MXFP4 of L (before dropout) is written
   uint8_t *qs = nullptr;     // too, codes [M, 128 C] and scales [C][M][8]
+  bool p_transposed = false; // P is [Kc, R] (ldp not used)
+  const float *given = nullptr;   // C itself, fp32 [M, R], scaled by drop.c already: the outputs only
 };
 int lowrank_splits(int64_t M, int64_t Kc);
 size_t lowrank_part_bytes(int64_t M, int64_t Kc, int64_t R);
@@ -230,6 +232,9 @@ struct ColSumArgs {
 };
 int colsum_splits(int64_t M, int64_t cols);
 hipError_t launch_colsum2(const ColSumArgs &a, const ColSumArgs &b, hipStream_t s, int trace_kind);
+// Their reduction over the splits, a launch of its own (the MXFP4 dX's finishing
+// pass, when there is one, takes it along: launch_mx_dx).
+hipError_t launch_colsum_reduce(const ColSumArgs &a, const ColSumArgs &b, hipStream_t s);
 
 // Forward pieces.
 struct FwdArgs {
@@ -313,6 +318,7 @@ struct MxDxArgs {
   int splits;              // set by the launcher
 };
 size_t mx_dx_part_bytes(int64_t M, int64_t N, int64_t K);
-hipError_t launch_mx_dx(const MxDxArgs &a, hipStream_t s);
+// With sums non-null (two ColSumArgs, already launched), also their reduction.
+hipError_t launch_mx_dx(const MxDxArgs &a, const ColSumArgs *sums, hipStream_t s);
 
 }  // namespace qn

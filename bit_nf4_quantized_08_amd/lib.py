@@ -571,10 +571,18 @@ def _launch(tensors, fn, *args):
                 raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
     call = getattr(_lib or load(), fn)
     if dev == torch.cuda.current_device():
-        _check(fn, call(*args, torch.cuda.current_stream(dev).cuda_stream))
+        _check(fn, call(*args, _raw_stream(dev)))
     else:
         with torch.cuda.device(dev):
-            _check(fn, call(*args, torch.cuda.current_stream(dev).cuda_stream))
+            _check(fn, call(*args, _raw_stream(dev)))
+
+
+def _raw_stream(dev):
+    """hipStream_t of the device's current stream (torch's own lookup, without
+    the Stream object that torch.cuda.current_stream builds around it)."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 @dataclass
