@@ -190,7 +190,8 @@ __global__ __launch_bounds__(kThreads) void mx_dequant_kernel(const uint8_t *__r
 struct MxGemmArgs {
   const uint8_t *xc, *xs;    // X^: codes [M, 128 C], scales [C][M][8]
   const uint8_t *wc, *ws;    // W: [N, 128 C], [C][N][8]
-  int64_t M, N, C;
+  int64_t M, N, C;           // N: columns of this launch
+  int64_t ldn;               // columns of Y and rows of the scale array
   const uint16_t *sH;        // bf16 [M, 64], zero beyond r, or null
   const uint16_t *B;         // bf16 [N, r]
   int64_t r;
@@ -247,9 +248,9 @@ void mx_gemm_kernel(MxGemmArgs a) {
   // zero): their products are not stored.
   const int erow = 128 * (wave % EP);
   const bool of_x = erow < BM;
-  const rsrc_t re = of_x ? make_rsrc_u(a.xs, a.C * a.M * 8) : make_rsrc_u(a.ws, a.C * a.N * 8);
+  const rsrc_t re = of_x ? make_rsrc_u(a.xs, a.C * a.M * 8) : make_rsrc_u(a.ws, (a.C - 1) * a.ldn * 8 + a.N * 8);
   const uint32_t eo = (uint32_t)((of_x ? m0 + erow : n0 + erow - BM) * 8 + lane * 16);
-  const int estep = (int)((of_x ? a.M : a.N) * 8);
+  const int estep = (int)((of_x ? a.M : a.ldn) * 8);
   // Load i of step s into a stage.
   constexpr int LOADS = XL + WL + 1;
   const uint32_t xl = (uint32_t)(wave * XL * 1024), wl = (uint32_t)(wave * WL * 1024);
@@ -437,7 +438,7 @@ void mx_gemm_kernel(MxGemmArgs a) {
     static_assert(2 * kPerStage + 2 * wper >= NW, "store blocks");
     blk = reinterpret_cast<uint16_t *>(p);
   }
-  const rsrc_t rout = make_rsrc_u(a.out + m0 * a.N, (a.M - m0) * a.N * 2);
+  const rsrc_t rout = make_rsrc_u(a.out + m0 * a.ldn, (a.M - m0) * a.ldn * 2);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -451,7 +452,7 @@ void mx_gemm_kernel(MxGemmArgs a) {
       const int row = kRows * q + lane / kPieces, c8 = 8 * (lane % kPieces);
       const u32x4 v = *reinterpret_cast<const u32x4 *>(&blk[row * kPitch + c8]);
       const int64_t lrow = wr * 32 * TM + 32 * i + row, n = wrow + c8;
-      __builtin_amdgcn_raw_buffer_store_b128(v, rout, n < a.N ? (uint32_t)((lrow * a.N + n) * 2) : kOutOfRange, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(v, rout, n < a.N ? (uint32_t)((lrow * a.ldn + n) * 2) : kOutOfRange, 0, 0);
     }
   }
 }
@@ -552,6 +553,7 @@ struct HPieces {
   bf16x8 hi, lo;
 };
 struct AdapterArgs {
+  const uint16_t *sH;  // bf16 s H [M, 64], zero beyond r: used as it is when non-null, else
   const float *hp;     // [hsplits][M][ldh] unscaled (ldh 32 or 64; columns at or beyond r undefined), or null
   int hsplits, ldh;
   const uint16_t *B;   // bf16 [N, r]
@@ -613,6 +615,11 @@ __device__ __forceinline__ bf16x8 load_b(const AdapterArgs &a, int64_t n, int j0
     w[t] = x | y << 16;
   }
   return __builtin_bit_cast(bf16x8, (u32x4{w[0], w[1], w[2], w[3]}));
+}
+
+// The same from bf16 s H.
+__device__ __forceinline__ bf16x8 load_sh(const AdapterArgs &a, int64_t m, int j0) {
+  return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(a.sH + m * 64 + j0));
 }
 
 __device__ __forceinline__ f32x4 add_adapter(f32x4 acc, bf16x8 b, const HPieces &h) {
@@ -762,11 +769,15 @@ __global__ __launch_bounds__(256) void mx_finish_kernel(MxFinishArgs a) {
     for (int q = 0; q < 4; ++q)
       if (q0 + q < a.splits) acc += v[q];
   }
-  if (a.ad.hp)
+  if (a.ad.sH) {
+    for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(load_b(a.ad, n0 + l16, j0), load_sh(a.ad, mc, j0), acc, 0, 0, 0);
+  } else if (a.ad.hp) {
     for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32) {
       const bf16x8 b = load_b(a.ad, n0 + l16, j0);
       acc = add_adapter(acc, b, load_h(a.ad, a.M, mc, j0, a.ad.H_out && blockIdx.x == 0 && wave == 0 && in));
     }
+  }
   // acc[e]: column n0 + 4 kb + e, row m.
   if (in)
     *reinterpret_cast<u32x2 *>(a.out + m * a.N + n0 + 4 * kb) =
@@ -807,18 +818,36 @@ DecodePlan decode_plan(int64_t N, int64_t K) {
   return p;
 }
 
+// Tiles of a forward.  256 x 256 ones (a workgroup fills a CU) move half the
+// bytes per product of 128 x 128 ones (two fit a CU), so they are taken when they
+// fill at least half the CUs.  A round of them costs about 2.0 us per chunk of K,
+// a round of 128 x 128 tiles 1.3 us with two on a CU, 0.8 us with one (8192 x
+// 8192 weights); a last round that is mostly empty is cut off as whole columns of
+// tiles and given to 128 x 128 tiles in a second launch (about 3 us) where that
+// is cheaper.  Fewer tiles than CUs are cut over K, each cut keeping two chunks.
 struct GemmPlan {
-  int bm, bn, splits;
+  int64_t wide;   // columns on 256 x 256 tiles
+  int splits;     // of the others, over K
 };
 GemmPlan gemm_plan(int64_t M, int64_t N, int64_t C) {
-  const int64_t cus = device_cus();
-  const int64_t big = cdiv(M, 256) * cdiv(N, 256);
-  if (big * 2 > cus) return GemmPlan{256, 256, 1};
+  const int64_t cus = device_cus(), tm = cdiv(M, 256), T = tm * cdiv(N, 256);
+  if (2 * T > cus) {
+    const int64_t rounds = T / cus, full = rounds * cus / tm * 256;   // columns of whole rounds
+    if (rounds == 0 || T % cus == 0 || full >= N) return GemmPlan{N, 1};
+    const int64_t rest = cdiv(M, 128) * cdiv(N - full, 128);
+    const double narrow = rest <= cus ? 0.8 : 1.3 * (double)cdiv(rest, 2 * cus);
+    return GemmPlan{narrow * (double)C + 3.0 < 2.0 * (double)C ? full : N, 1};
+  }
   const int64_t mid = cdiv(M, 128) * cdiv(N, 128);
   int splits = 1;
-  while (splits < 8 && mid * splits * 2 <= 2 * cus && C / (splits * 2) >= 2) splits *= 2;
-  return GemmPlan{128, 128, splits};
+  while (splits < 8 && mid * splits * 2 <= cus && C / (splits * 2) >= 2) splits *= 2;
+  return GemmPlan{0, splits};
 }
+
+// Rows up to which the finishing kernel of split tiles adds H's partial sums
+// itself (each of its waves reads them for its rows); beyond, the low-rank
+// product is finished once by a launch of its own.
+constexpr int64_t kFinishRows = 64;
 
 struct FwdPieces {
   uint8_t *xc, *xs;        // X^
@@ -841,7 +870,7 @@ FwdPieces fwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r) {
     const GemmPlan g = gemm_plan(M, N, C);
     if (g.splits > 1) p.y_part = c.take<float>((int64_t)g.splits * M * N);
     if (r) p.h_part = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
-    if (r && g.splits == 1) p.sH = c.take<uint16_t>(M * 64);
+    if (r && (g.splits == 1 || M > kFinishRows)) p.sH = c.take<uint16_t>(M * 64);
   }
   p.bytes = c.off;
   return p;
@@ -882,7 +911,7 @@ hipError_t run_decode(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
     hipLaunchKernelGGL(mx_prep_kernel, dim3((unsigned)(qblocks + hblocks)), block, 0, st, q);
     QN_TRY(hipGetLastError());
   }
-  const AdapterArgs ad{a.r ? w.h_part : nullptr, p.hsplits, 64, a.B, a.r, a.s, a.drop.c, a.H_out};
+  const AdapterArgs ad{nullptr, a.r ? w.h_part : nullptr, p.hsplits, 64, a.B, a.r, a.s, a.drop.c, a.H_out};
   const MxDecodeArgs d{w.xc, w.xs, a.M, a.N, C, a.codes, a.scales, ad, p.ksplits == 1 ? a.Y : nullptr, w.y_part,
                        p.nk, p.row_blocks};
   const dim3 grid((unsigned)(p.row_blocks * p.ksplits));
@@ -955,16 +984,24 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
     l.out_f32 = a.H_out;
     l.out_b = w.sH;
     l.ldb = 64;
-    // Split tiles end in a finishing kernel, which adds H's partial sums itself.
-    QN_TRY(p.splits > 1 ? launch_lowrank_part(l, st) : launch_lowrank(l, st));
+    QN_TRY(w.sH ? launch_lowrank(l, st) : launch_lowrank_part(l, st));
   }
-  MxGemmArgs g{w.xc, w.xs, a.codes, a.scales, a.M, a.N, C, a.r ? w.sH : nullptr, a.B, a.r, a.Y, w.y_part,
+  MxGemmArgs g{w.xc, w.xs, a.codes, a.scales, a.M, a.N, C, a.N, a.r ? w.sH : nullptr, a.B, a.r, a.Y, w.y_part,
                0, 0, 0, p.splits};
-  if (p.bm == 256) return launch_tiles<2, 4, 4, 2, false>(g, st);
+  if (p.wide) {
+    g.N = p.wide;
+    QN_TRY((launch_tiles<2, 4, 4, 2, false>(g, st)));
+    if (p.wide == a.N) return hipSuccess;
+    g.wc += p.wide * 128 * C;
+    g.ws += p.wide * 8;
+    if (g.sH) g.B += p.wide * a.r;
+    g.out += p.wide;
+    g.N = a.N - p.wide;
+  }
   if (p.splits == 1) return launch_tiles<2, 2, 2, 2, false>(g, st);
   QN_TRY((launch_tiles<2, 2, 2, 2, true>(g, st)));
-  const AdapterArgs ad{a.r ? w.h_part : nullptr, lowrank_splits(a.M, a.K), (int)align_up(a.r, 32), a.B, a.r, a.s,
-                       a.drop.c, a.H_out};
+  const AdapterArgs ad{a.r ? w.sH : nullptr, a.r ? w.h_part : nullptr, lowrank_splits(a.M, a.K), (int)align_up(a.r, 32),
+                       a.B, a.r, a.s, a.drop.c, a.H_out};
   return launch_finish(MxFinishArgs{w.y_part, p.splits, ad, a.M, a.N, a.Y}, st);
 }
 
