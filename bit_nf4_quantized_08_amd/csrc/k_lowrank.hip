@@ -361,9 +361,7 @@ size_t lowrank_part_bytes(int64_t M, int64_t Kc, int64_t R) {
   return (size_t)lowrank_splits(M, Kc) * (size_t)M * (size_t)align32(R) * sizeof(float);
 }
 
-namespace {
-
-hipError_t launch_lowrank_group(const LowRankArgs *a, int n, bool finish, hipStream_t st) {
+hipError_t launch_lowrank_n(const LowRankArgs *a, int n, hipStream_t st) {
   if (n < 1 || n > QN_MAX_GROUP) return hipErrorInvalidValue;
   LowRankGroup grp{};
   int64_t wgs = 0, fin = 0, R = 0;
@@ -401,19 +399,13 @@ hipError_t launch_lowrank_group(const LowRankArgs *a, int n, bool finish, hipStr
     }
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !finish) return e;
+  if (e != hipSuccess) return e;
   const dim3 fgrid((unsigned)fin, (unsigned)n);
   if (R <= 16) hipLaunchKernelGGL(lowrank_finish_kernel<16>, fgrid, dim3(256), 0, st, grp);
   else if (R <= 32) hipLaunchKernelGGL(lowrank_finish_kernel<32>, fgrid, dim3(256), 0, st, grp);
   else hipLaunchKernelGGL(lowrank_finish_kernel<64>, fgrid, dim3(256), 0, st, grp);
   return hipGetLastError();
 }
-
-}  // namespace
-
-hipError_t launch_lowrank_n(const LowRankArgs *a, int n, hipStream_t st) { return launch_lowrank_group(a, n, true, st); }
-
-hipError_t launch_lowrank_part(const LowRankArgs &a, hipStream_t st) { return launch_lowrank_group(&a, 1, false, st); }
 
 hipError_t launch_lowrank2(const LowRankArgs &a, const LowRankArgs *b, hipStream_t st) {
   const LowRankArgs two[2] = {a, b ? *b : a};

@@ -13,8 +13,8 @@
 //   mx_gemm_kernel       tiles of mx(X) W^T with the adapter term (bound by the
 //                        matrix cores and the clock they sustain), optionally
 //                        over a part of K with fp32 partial sums
-//   mx_prep_kernel       M <= 16: X^ and the adapter's H partials
-//   mx_decode_kernel     M <= 16: streams the weights (bound by memory)
+//   mx_prep_kernel       M <= 32: X^ and the adapter's H partials
+//   mx_decode_kernel     M <= 32: streams the weights (bound by memory)
 //   mx_finish_kernel     adds partial products and the adapter term
 
 #include <algorithm>
@@ -458,14 +458,14 @@ void mx_gemm_kernel(MxGemmArgs a) {
 }
 
 // ------------------------------------------------------------------ few rows
-// M <= 16, two launches.  The first quantises X and forms partial sums of H = X
+// M <= 32, two launches.  The first quantises X and forms partial sums of H = X
 // A^T; the second streams the weights and, when a workgroup's waves cover all
 // of K (up to 8192 columns), finishes Y.
 //
 // Streaming: a wave owns 16 weight rows x 1024 columns at a time, eight
 // sub-steps of v_mfma_scale_f32_16x16x128 with the weights as the first operand
-// (lane: row lane % 16, block lane / 16 of the sub-step's four) and the 16 rows
-// of X^ as the second.  The codes come through LDS by direct loads of two rows x
+// (lane: row lane % 16, block lane / 16 of the sub-step's four) and X^ in groups
+// of 16 rows, held in registers, as the second.  The codes come through LDS by direct loads of two rows x
 // 512 contiguous bytes each: read straight into the fragments they would come
 // as 64-byte pieces of 16 rows (8192 x 8192, M = 1: 10.4 against 12.1 us).  The
 // wave reads a group's eight fragments into registers and asks for the next
@@ -492,13 +492,15 @@ struct MxPrepArgs {
   int64_t r;
   DropArgs drop;
   float *h_part;       // [hsplits][M][64]
-  int hsplits;
+  int hsplits, mgroups;   // mgroups: 16-row groups of X
 };
 
-// H partials: workgroup b of them takes 16 ranks of A and 8 x HSEG columns.
+// H partials: workgroup b of them takes 16 rows of X, 16 ranks of A and 8 x HSEG
+// columns.
 __device__ void prep_h(const MxPrepArgs &a, int b, float (*red)[256]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, kb = lane >> 4;
-  const int jt = b / a.hsplits, hs = b % a.hsplits, j = 16 * jt + l16;
+  const int mg = b % a.mgroups, jt = b / a.mgroups / a.hsplits, hs = b / a.mgroups % a.hsplits, j = 16 * jt + l16;
+  const int64_t m = 16 * mg + l16;
   const int64_t k0 = (int64_t)hs * (DW * HSEG) + wave * HSEG + 8 * kb;
   const rsrc_t ra = make_rsrc_u(a.A, a.r * a.K * 2), rx = make_rsrc_u(a.X, a.M * a.K * 2);
   u32x4 av[HSEG / 32], xv[HSEG / 32];
@@ -506,14 +508,14 @@ __device__ void prep_h(const MxPrepArgs &a, int b, float (*red)[256]) {
   for (int i = 0; i < HSEG / 32; ++i) {
     const int64_t k = k0 + 32 * i;
     av[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, j < a.r && k < a.K ? (uint32_t)((j * a.K + k) * 2) : kOutOfRange, 0, 0);
-    xv[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, l16 < a.M && k < a.K ? (uint32_t)((l16 * a.K + k) * 2) : kOutOfRange, 0, 0);
+    xv[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, m < a.M && k < a.K ? (uint32_t)((m * a.K + k) * 2) : kOutOfRange, 0, 0);
   }
   if (a.drop.thr) {
     const DropKey dk = drop_key(a.drop);
 #pragma unroll
     for (int i = 0; i < HSEG / 32; ++i) {
       uint32_t w[4];
-      philox7((uint64_t)l16 * (uint64_t)(a.K / 8) + (uint64_t)((k0 + 32 * i) >> 3), dk, w);
+      philox7((uint64_t)m * (uint64_t)(a.K / 8) + (uint64_t)((k0 + 32 * i) >> 3), dk, w);
       xv[i] &= u32x4{keep_mask2(w[0], dk.thr2), keep_mask2(w[1], dk.thr2), keep_mask2(w[2], dk.thr2),
                      keep_mask2(w[3], dk.thr2)};
     }
@@ -528,11 +530,11 @@ __device__ void prep_h(const MxPrepArgs &a, int b, float (*red)[256]) {
   for (int e = 0; e < 4; ++e) red[wave][l16 * 16 + 4 * kb + e] = acc[e];
   __syncthreads();
   if (tid < 256) {
-    const int m = tid >> 4, jj = tid & 15;
+    const int mo = 16 * mg + (tid >> 4), jj = tid & 15;
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < DW; ++w) v += red[w][tid];
-    if (m < a.M) a.h_part[((int64_t)hs * a.M + m) * 64 + 16 * jt + jj] = v;
+    if (mo < a.M) a.h_part[((int64_t)hs * a.M + mo) * 64 + 16 * jt + jj] = v;
   }
 }
 
@@ -637,8 +639,10 @@ struct MxDecodeArgs {
   int nk, row_blocks;
 };
 
-template <int G>   // row groups per wave
-__global__ __launch_bounds__(64 * DW) void mx_decode_kernel(MxDecodeArgs a) {
+// G, MB: 16-row groups of W per wave and of X.  At most 128 registers: two
+// workgroups to a CU.
+template <int G, int MB>
+__global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4))) void mx_decode_kernel(MxDecodeArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t stage[DW][16 * DSEG / 2];   // a wave's weights
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, kb = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -649,19 +653,35 @@ __global__ __launch_bounds__(64 * DW) void mx_decode_kernel(MxDecodeArgs a) {
   const int64_t n0 = ((int64_t)rb * ng + rg) * (16 * G);     // first row of the wave
   const int bytes = (int)min((int64_t)DSEG / 2, max((int64_t)0, pitch - k0 / 2));   // of the segment that exist
 
-  // X^: row l16, piece 4 i + kb of the segment; zero past the row or the rows.
+  // Scale bytes of a lane's block in the eight sub-steps (byte kb of the sub-step's
+  // dword), four to a register: the instruction's byte select takes them there.
+  const uint32_t pick = 0x0C0C0000u | (uint32_t)(kb + 4) << 8 | (uint32_t)kb;
+  auto pack_scales = [&](const u32x2 (&e)[DSUB / 2], uint32_t (&out)[DSUB / 4]) {
+#pragma unroll
+    for (int h = 0; h < DSUB / 4; ++h)
+      out[h] = __builtin_amdgcn_perm(e[2 * h].y, e[2 * h].x, pick) |
+               __builtin_amdgcn_perm(e[2 * h + 1].y, e[2 * h + 1].x, pick) << 16;
+  };
+  // X^: rows 16 b + l16, piece 4 i + kb of the segment; zero past the row or the
+  // rows.
   const rsrc_t rx = make_rsrc_u(a.xc, a.M * pitch);
-  u32x4 xv[DSUB];
-  u32x2 xe[DSUB / 2];
-#pragma unroll
-  for (int i = 0; i < DSUB; ++i)
-    xv[i] = __builtin_amdgcn_raw_buffer_load_b128(
-        rx, l16 < a.M && 64 * i < bytes ? (uint32_t)(l16 * pitch + k0 / 2 + 64 * i + 16 * kb) : kOutOfRange, 0, 0);
   const rsrc_t rxs = make_rsrc_u(a.xs, a.C * a.M * 8);
+  u32x4 xv[MB][DSUB];
+  uint32_t xe[MB][DSUB / 4];
 #pragma unroll
-  for (int i = 0; i < DSUB / 2; ++i)
-    xe[i] = __builtin_amdgcn_raw_buffer_load_b64(
-        rxs, l16 < a.M && 128 * i < bytes ? (uint32_t)(((k0 / 256 + i) * a.M + l16) * 8) : kOutOfRange, 0, 0);
+  for (int b = 0; b < MB; ++b) {
+    const int m = 16 * b + l16;
+    u32x2 e[DSUB / 2];
+#pragma unroll
+    for (int i = 0; i < DSUB; ++i)
+      xv[b][i] = __builtin_amdgcn_raw_buffer_load_b128(
+          rx, m < a.M && 64 * i < bytes ? (uint32_t)(m * pitch + k0 / 2 + 64 * i + 16 * kb) : kOutOfRange, 0, 0);
+#pragma unroll
+    for (int i = 0; i < DSUB / 2; ++i)
+      e[i] = __builtin_amdgcn_raw_buffer_load_b64(
+          rxs, m < a.M && 128 * i < bytes ? (uint32_t)(((k0 / 256 + i) * a.M + m) * 8) : kOutOfRange, 0, 0);
+    pack_scales(e, xe[b]);
+  }
 
   // Weights: direct load t of a group brings rows 2 t and 2 t + 1 (slot lane % 32
   // of row 2 t + lane / 32: piece slot ^ row).  Out-of-range lanes bring zeros.
@@ -684,7 +704,7 @@ __global__ __launch_bounds__(64 * DW) void mx_decode_kernel(MxDecodeArgs a) {
   };
   load_w(0);
 
-  f32x4 acc[G];
+  f32x4 acc[G][MB];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's direct loads have landed
@@ -695,46 +715,59 @@ __global__ __launch_bounds__(64 * DW) void mx_decode_kernel(MxDecodeArgs a) {
       const u32x4 v = *reinterpret_cast<const u32x4 *>(&stage[wave][l16 * 512 + 16 * ((4 * i + kb) ^ l16)]);
       wf[i] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
     }
-    uint32_t sw[DSUB];
-#pragma unroll
-    for (int i = 0; i < DSUB; ++i) sw[i] = ((i & 1) ? we[i >> 1].y : we[i >> 1].x) >> (8 * kb);
+    uint32_t sw[DSUB / 4];
+    pack_scales(we, sw);
     if (g + 1 < G) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the fragments are read before LDS is refilled
       load_w(g + 1);
     }
-    acc[g] = zero4();
 #pragma unroll
-    for (int i = 0; i < DSUB; ++i) {
-      const i32x8 xf = {(int)xv[i].x, (int)xv[i].y, (int)xv[i].z, (int)xv[i].w, 0, 0, 0, 0};
-      const uint32_t sx = ((i & 1) ? xe[i >> 1].y : xe[i >> 1].x) >> (8 * kb);
-      acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf, acc[g], 4, 4, 0, (int)sw[i], 0, (int)sx);
+    for (int b = 0; b < MB; ++b) {
+      acc[g][b] = zero4();
+      auto sub = [&](auto I) {
+        constexpr int i = decltype(I)::value;
+        const i32x8 xf = {(int)xv[b][i].x, (int)xv[b][i].y, (int)xv[b][i].z, (int)xv[b][i].w, 0, 0, 0, 0};
+        acc[g][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf, acc[g][b], 4, 4, i & 3, (int)sw[i >> 2],
+                                                                     i & 3, (int)xe[b][i >> 2]);
+      };
+      sub(std::integral_constant<int, 0>{}); sub(std::integral_constant<int, 1>{});
+      sub(std::integral_constant<int, 2>{}); sub(std::integral_constant<int, 3>{});
+      sub(std::integral_constant<int, 4>{}); sub(std::integral_constant<int, 5>{});
+      sub(std::integral_constant<int, 6>{}); sub(std::integral_constant<int, 7>{});
     }
   }
-  // acc[g][e]: weight row 16 g + 4 kb + e, row l16 of X.
+  // acc[g][b][e]: weight row 16 g + 4 kb + e, row 16 b + l16 of X.
   if (a.out && a.ad.hp && seg == 0) {
-    const int64_t mc = min((int64_t)l16, a.M - 1);
-#pragma unroll 1
-    for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32) {
-      const HPieces h = load_h(a.ad, a.M, mc, j0, a.ad.H_out && rb == 0 && rg == 0 && l16 < a.M);
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-        acc[g] = add_adapter(acc[g], load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0), h);
+    for (int b = 0; b < MB; ++b) {
+      const int64_t m = 16 * b + l16, mc = min(m, a.M - 1);
+#pragma unroll 1
+      for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32) {
+        const HPieces h = load_h(a.ad, a.M, mc, j0, a.ad.H_out && rb == 0 && rg == 0 && m < a.M);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          acc[g][b] = add_adapter(acc[g][b], load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0), h);
+      }
     }
   }
-  // Partial sums [G * 256] in place of the wave's own stage.
-  static_assert(G * 1024 <= 16 * DSEG / 2, "partial sums fit");
+  // Partial sums [G * MB * 256] in place of the wave's own stage.
+  static_assert(G * MB * 1024 <= 16 * DSEG / 2, "partial sums fit");
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) reinterpret_cast<float *>(stage[wave])[g * 256 + l16 * 16 + 4 * kb + e] = acc[g][e];
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        reinterpret_cast<float *>(stage[wave])[(g * MB + b) * 256 + l16 * 16 + 4 * kb + e] = acc[g][b][e];
   __syncthreads();
-  // Element idx of a row group set: (set q, group, row of X, row in 16).
-  for (int idx = tid; idx < ng * G * 256; idx += 64 * DW) {
-    const int q = idx / (G * 256), in = idx % (G * 256);
+  // Element idx of a row group set: (set q, group g, group b, row of X in 16, row in 16).
+  constexpr int per = G * MB * 256;
+  for (int idx = tid; idx < ng * per; idx += 64 * DW) {
+    const int q = idx / per, in = idx % per, g = in / (MB * 256), b = in / 256 % MB;
     float v = 0.0f;
     for (int w = 0; w < a.nk; ++w) v += reinterpret_cast<const float *>(stage[q * a.nk + w])[in];
-    const int64_t n = ((int64_t)rb * ng + q) * (16 * G) + 16 * (in >> 8) + (in & 15);
-    const int m = (in >> 4) & 15;
+    const int64_t n = ((int64_t)rb * ng + q) * (16 * G) + 16 * g + (in & 15);
+    const int m = 16 * b + ((in >> 4) & 15);
     if (m < a.M && n < a.N) {
       if (a.out) a.out[m * a.N + n] = f32_to_bf16(v);
       else a.y_part[((int64_t)ks * a.M + m) * a.N + n] = v;
@@ -797,12 +830,12 @@ struct Carve {
   }
 };
 
-constexpr int64_t kDecodeRows = 16;
+constexpr int64_t kDecodeRows = 32;
 
 struct DecodePlan {
-  int nk, ksplits, row_blocks, hsplits, groups;
+  int nk, ksplits, row_blocks, groups;
 };
-DecodePlan decode_plan(int64_t N, int64_t K) {
+DecodePlan decode_plan(int64_t M, int64_t N, int64_t K) {
   DecodePlan p;
   const int64_t segs = cdiv(K, DSEG);
   p.nk = 1;
@@ -810,11 +843,11 @@ DecodePlan decode_plan(int64_t N, int64_t K) {
   p.ksplits = (int)cdiv(segs, p.nk);
   // Row groups per wave: one while the workgroups are resident at once (two to
   // a CU), then two or four, which keeps them resident for longer weights and
-  // lets a wave ask for its next rows before it is done with these.
+  // lets a wave ask for its next rows before it is done with these (four with 32
+  // rows of X would spill).
   const int64_t wgs = cdiv(N, 16 * (DW / p.nk)) * p.ksplits;
-  p.groups = wgs <= 2 * device_cus() ? 1 : (wgs <= 4 * device_cus() ? 2 : 4);
+  p.groups = wgs <= 2 * device_cus() ? 1 : (wgs <= 4 * device_cus() || M > 16 ? 2 : 4);
   p.row_blocks = (int)cdiv(N, (int64_t)16 * p.groups * (DW / p.nk));
-  p.hsplits = (int)cdiv(K, DW * HSEG);
   return p;
 }
 
@@ -824,7 +857,8 @@ DecodePlan decode_plan(int64_t N, int64_t K) {
 // a round of 128 x 128 tiles 1.3 us with two on a CU, 0.8 us with one (8192 x
 // 8192 weights); a last round that is mostly empty is cut off as whole columns of
 // tiles and given to 128 x 128 tiles in a second launch (about 3 us) where that
-// is cheaper.  Fewer tiles than CUs are cut over K, each cut keeping two chunks.
+// is cheaper.  128 x 128 tiles may be cut over K, for which the partial sums are
+// written and read once more.
 struct GemmPlan {
   int64_t wide;   // columns on 256 x 256 tiles
   int splits;     // of the others, over K
@@ -840,14 +874,15 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t C) {
   }
   const int64_t mid = cdiv(M, 128) * cdiv(N, 128);
   int splits = 1;
-  while (splits < 8 && mid * splits * 2 <= cus && C / (splits * 2) >= 2) splits *= 2;
+  double best = 1e300;
+  for (int k = 1; k <= 8 && (k == 1 || C / k >= 2); k *= 2) {
+    const double rounds = mid * k <= cus ? 0.8 : 1.3 * (double)cdiv(mid * k, 2 * cus);
+    const double sums = k == 1 ? 0.0 : 3.0 + (double)(k * M * N) * 8.0 / 4.5e6;   // written and read at 4.5 TB/s
+    const double us = rounds * (double)cdiv(C, k) + sums;
+    if (us < best) { best = us; splits = k; }
+  }
   return GemmPlan{0, splits};
 }
-
-// Rows up to which the finishing kernel of split tiles adds H's partial sums
-// itself (each of its waves reads them for its rows); beyond, the low-rank
-// product is finished once by a launch of its own.
-constexpr int64_t kFinishRows = 64;
 
 struct FwdPieces {
   uint8_t *xc, *xs;        // X^
@@ -856,21 +891,26 @@ struct FwdPieces {
   uint16_t *sH;            // bf16 s H (tiles that finish Y themselves)
   size_t bytes;
 };
+int prep_hsplits(int64_t K);
+// Rows up to which split tiles take X^ and H from the few-row path's first launch
+// and leave H's partial sums to their finishing kernel (each of its waves reads
+// them for its rows): the low-rank kernel has one workgroup per 128 rows and
+// range, too few for so little.
+constexpr int64_t kPrepRows = 128;
+
 FwdPieces fwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r) {
   FwdPieces p{};
   Carve c(ws);
   const int64_t C = mx_chunks(K);
   p.xc = c.take<uint8_t>(M * 128 * C);
   p.xs = c.take<uint8_t>(M * 8 * C);
-  if (M <= kDecodeRows) {
-    const DecodePlan d = decode_plan(N, K);
-    if (d.ksplits > 1) p.y_part = c.take<float>((int64_t)d.ksplits * M * N);
-    if (r) p.h_part = c.take<float>((int64_t)d.hsplits * M * 64);
-  } else {
-    const GemmPlan g = gemm_plan(M, N, C);
-    if (g.splits > 1) p.y_part = c.take<float>((int64_t)g.splits * M * N);
-    if (r) p.h_part = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
-    if (r && (g.splits == 1 || M > kFinishRows)) p.sH = c.take<uint16_t>(M * 64);
+  const int splits = M <= kDecodeRows ? decode_plan(M, N, K).ksplits : gemm_plan(M, N, C).splits;
+  if (splits > 1) p.y_part = c.take<float>((int64_t)splits * M * N);
+  if (r && (M <= kDecodeRows || (M <= kPrepRows && splits > 1))) {
+    p.h_part = c.take<float>((int64_t)prep_hsplits(K) * M * 64);
+  } else if (r) {
+    p.h_part = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
+    p.sH = c.take<uint16_t>(M * 64);
   }
   p.bytes = c.off;
   return p;
@@ -898,28 +938,33 @@ hipError_t launch_finish(const MxFinishArgs &f, hipStream_t st) {
   return hipGetLastError();
 }
 
+// X^ and H's partial sums (h_part [prep_hsplits][M][64]).
+int prep_hsplits(int64_t K) { return (int)cdiv(K, DW * HSEG); }
+hipError_t launch_prep(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
+  const int64_t C = mx_chunks(a.K);
+  const uint32_t chunks = (uint32_t)(a.M * C);
+  const int qblocks = (int)cdiv(chunks, 64 * DW / 32), mgroups = (int)cdiv(a.M, 16), hsplits = prep_hsplits(a.K);
+  const int hblocks = a.r ? (int)cdiv(a.r, 16) * hsplits * mgroups : 0;
+  const MxPrepArgs q{a.X, a.M, a.K, fast_div((uint32_t)C), chunks, w.xc, w.xs, qblocks, a.A, a.r, a.drop,
+                     w.h_part, hsplits, mgroups};
+  hipLaunchKernelGGL(mx_prep_kernel, dim3((unsigned)(qblocks + hblocks)), dim3(64 * DW), 0, st, q);
+  return hipGetLastError();
+}
+
 hipError_t run_decode(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
-  const DecodePlan p = decode_plan(a.N, a.K);
+  const DecodePlan p = decode_plan(a.M, a.N, a.K);
   const int64_t C = mx_chunks(a.K);
   const dim3 block(64 * DW);
-  {
-    const uint32_t chunks = (uint32_t)(a.M * C);
-    const int qblocks = (int)cdiv(chunks, 64 * DW / 32);
-    const int hblocks = a.r ? (int)cdiv(a.r, 16) * p.hsplits : 0;
-    const MxPrepArgs q{a.X, a.M, a.K, fast_div((uint32_t)C), chunks, w.xc, w.xs, qblocks, a.A, a.r, a.drop,
-                       w.h_part, p.hsplits};
-    hipLaunchKernelGGL(mx_prep_kernel, dim3((unsigned)(qblocks + hblocks)), block, 0, st, q);
-    QN_TRY(hipGetLastError());
-  }
-  const AdapterArgs ad{nullptr, a.r ? w.h_part : nullptr, p.hsplits, 64, a.B, a.r, a.s, a.drop.c, a.H_out};
+  QN_TRY(launch_prep(a, w, st));
+  const AdapterArgs ad{nullptr, a.r ? w.h_part : nullptr, prep_hsplits(a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
   const MxDecodeArgs d{w.xc, w.xs, a.M, a.N, C, a.codes, a.scales, ad, p.ksplits == 1 ? a.Y : nullptr, w.y_part,
                        p.nk, p.row_blocks};
   const dim3 grid((unsigned)(p.row_blocks * p.ksplits));
   {
     TraceScope tr(QN_TRACE_MX_GEMV, st);
-    if (p.groups == 1) hipLaunchKernelGGL(mx_decode_kernel<1>, grid, block, 0, st, d);
-    else if (p.groups == 2) hipLaunchKernelGGL(mx_decode_kernel<2>, grid, block, 0, st, d);
-    else hipLaunchKernelGGL(mx_decode_kernel<4>, grid, block, 0, st, d);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, d); };
+    if (a.M <= 16) p.groups == 1 ? go(mx_decode_kernel<1, 1>) : p.groups == 2 ? go(mx_decode_kernel<2, 1>) : go(mx_decode_kernel<4, 1>);
+    else p.groups == 1 ? go(mx_decode_kernel<1, 2>) : go(mx_decode_kernel<2, 2>);
   }
   QN_TRY(hipGetLastError());
   if (p.ksplits == 1) return hipSuccess;
@@ -974,6 +1019,8 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
   const GemmPlan p = gemm_plan(a.M, a.N, C);
   if (a.r == 0) {
     QN_TRY(launch_mx_quantize(a.X, 1, a.M, a.K, w.xc, w.xs, st));
+  } else if (!w.sH) {
+    QN_TRY(launch_prep(a, w, st));
   } else {   // one pass over X: its low-rank product and its quantisation
 
     LowRankArgs l{};
@@ -984,7 +1031,7 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
     l.out_f32 = a.H_out;
     l.out_b = w.sH;
     l.ldb = 64;
-    QN_TRY(w.sH ? launch_lowrank(l, st) : launch_lowrank_part(l, st));
+    QN_TRY(launch_lowrank(l, st));
   }
   MxGemmArgs g{w.xc, w.xs, a.codes, a.scales, a.M, a.N, C, a.N, a.r ? w.sH : nullptr, a.B, a.r, a.Y, w.y_part,
                0, 0, 0, p.splits};
@@ -1000,8 +1047,7 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
   }
   if (p.splits == 1) return launch_tiles<2, 2, 2, 2, false>(g, st);
   QN_TRY((launch_tiles<2, 2, 2, 2, true>(g, st)));
-  const AdapterArgs ad{a.r ? w.sH : nullptr, a.r ? w.h_part : nullptr, lowrank_splits(a.M, a.K), (int)align_up(a.r, 32),
-                       a.B, a.r, a.s, a.drop.c, a.H_out};
+  const AdapterArgs ad{w.sH, a.r ? w.h_part : nullptr, prep_hsplits(a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
   return launch_finish(MxFinishArgs{w.y_part, p.splits, ad, a.M, a.N, a.Y}, st);
 }
 

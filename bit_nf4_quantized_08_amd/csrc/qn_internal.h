@@ -190,9 +190,6 @@ struct LowRankArgs {
 int lowrank_splits(int64_t M, int64_t Kc);
 size_t lowrank_part_bytes(int64_t M, int64_t Kc, int64_t R);
 hipError_t launch_lowrank(const LowRankArgs &a, hipStream_t s);
-// The ranges' partial products only: a.part [lowrank_splits][M][R rounded up to
-// 32], not scaled by drop.c, columns at or beyond R zero.
-hipError_t launch_lowrank_part(const LowRankArgs &a, hipStream_t s);
 // Two independent products with the same rank bucket in one launch (b may be null).
 hipError_t launch_lowrank2(const LowRankArgs &a, const LowRankArgs *b, hipStream_t s);
 // Up to QN_MAX_GROUP independent products in one launch (blockIdx.y picks one).

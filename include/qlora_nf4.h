@@ -441,7 +441,7 @@ size_t qlora_mx_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t 
  * (alpha and drop are not used).  Otherwise arguments as qlora_linear_fwd.
  * Shape rules: M >= 1, N % 64 == 0, K % 64 == 0, N * 128 C <= INT32_MAX,
  * N and K <= 2^22, M * C <= 2^28, 0 <= r <= QN_MAX_RANK.  A non-finite block of X makes its row of Y
- * NaN.  M <= 16 streams the weights once (both operands on the matrix cores),
+ * NaN.  M <= 32 streams the weights once (both operands on the matrix cores),
  * larger M runs tiles. */
 int qlora_mx_linear_fwd(const void *X, int64_t M, const qn_mx_matrix *W, const void *A, const void *B, int64_t r,
                         float alpha, const qn_dropout_config *drop, void *Y, float *H_out, void *workspace,

@@ -148,7 +148,7 @@ def run_mx(M, N, K, r, p, give_H=True, backward=True, seed=0):
     return out
 
 
-@pytest.mark.parametrize("M", [1, 2, 3, 8, 15, 16])
+@pytest.mark.parametrize("M", [1, 2, 3, 8, 15, 16, 17, 31, 32])
 @pytest.mark.parametrize("N, K, r, p", [(64, 64, 8, None), (192, 320, 13, 0.25), (128, 1088, 64, None), (64, 2112, 0, None),
                                         (320, 4160, 16, 0.1)])
 def test_few_rows(M, N, K, r, p):
@@ -157,14 +157,16 @@ def test_few_rows(M, N, K, r, p):
 
 
 @pytest.mark.parametrize("M, N, K, r, p", [(1, 128, 8256, 8, None), (7, 64, 16448, 0, None), (16, 8192, 1024, 16, None),
-                                           (2, 16384, 256, 0, None), (5, 12352, 192, 24, 0.5)])
+                                           (2, 16384, 256, 0, None), (5, 12352, 192, 24, 0.5),
+                                           (20, 128, 8256, 13, 0.25), (32, 16384, 256, 64, None),
+                                           (25, 33024, 64, 8, 0.1)])
 def test_few_rows_long_rows_and_many_rows_of_weight(M, N, K, r, p):
     """Split columns (K beyond 8192) and two and four row groups per wave."""
     say(f"mx linear M={M} N={N} K={K} r={r} p={p}")
     run_mx(M, N, K, r, p, backward=False, seed=M)
 
 
-@pytest.mark.parametrize("M", [17, 64, 127, 128, 129, 300])
+@pytest.mark.parametrize("M", [33, 64, 127, 128, 129, 300])
 @pytest.mark.parametrize("N, K, r, p, give_H", [(64, 64, 8, None, True), (192, 320, 13, 0.25, False),
                                                 (448, 1088, 64, 0.5, True), (128, 704, 0, None, True),
                                                 (64, 192, 33, None, False)])
@@ -173,7 +175,9 @@ def test_tiles(M, N, K, r, p, give_H):
     run_mx(M, N, K, r, p, give_H=give_H, seed=M)
 
 
-@pytest.mark.parametrize("M, N, K, r, p", [(17, 64, 4096, 16, 0.1), (40, 4096, 64, 20, None), (200, 256, 2304, 0, None)])
+@pytest.mark.parametrize("M, N, K, r, p", [(17, 64, 4096, 16, 0.1), (40, 4096, 64, 20, None), (200, 256, 2304, 0, None),
+                                           (33, 64, 4096, 16, 0.1), (100, 192, 2304, 13, 0.25), (128, 64, 1600, 64, None),
+                                           (200, 64, 4096, 24, 0.1), (1000, 128, 2112, 5, 0.5)])
 def test_split_contractions(M, N, K, r, p):
     """Long contractions of small outputs, forward (over K) and dX (over N)."""
     say(f"mx linear split M={M} N={N} K={K} r={r} p={p}")
@@ -186,6 +190,13 @@ def test_large_tiles(r, p):
     say(f"mx linear large tiles r={r} p={p}")
     run_mx(2200, 4160, 320, r, p, seed=r)
     run_mx(2100, 320, 4160, r, p, seed=r + 1)
+
+
+@pytest.mark.parametrize("r, p", [(16, 0.2), (0, None)])
+def test_large_and_small_tiles_in_one_call(r, p):
+    """A last round that is mostly empty: whole columns of it go to the small tiles, a second launch at column offsets."""
+    say(f"mx linear mixed tiles r={r} p={p}")
+    run_mx(2200, 8448, 704, r, p, backward=False, seed=r)
 
 
 @pytest.mark.parametrize("M", [4, 40, 300])
