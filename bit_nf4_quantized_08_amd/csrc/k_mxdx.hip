@@ -219,26 +219,10 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     const int un = x >> 3, q = un / UW, u = un % UW;
     return 32 * (UW * wc + u) + 8 * q + (x & 7);
   };
-  if constexpr (PART) {
-    float *part = a.part + (int64_t)split * a.M * a.K;
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int64_t k = k0 + col_of(32 * j + lr);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int64_t m = row0 + 32 * i + 8 * (e >> 2) + 4 * lh + (e & 3);
-          if (m < a.M && k < a.K) part[m * a.K + k] = acc[i][j][e];
-        }
-      }
-    return;
-  }
-
   // Adapter term: A as an expanded stage (rows j < r, zero beyond), dH's
   // fragments from global memory.  Every wave has passed the last barrier, so
   // ws0 is free.
-  if (a.r) {
+  if (a.r && (!PART || split == 0)) {   // of split products, the first carries it
     {
       const rsrc_t ra = make_rsrc_u(a.A, a.r * a.K * 2);
       const int64_t col = k0 + 32 * ch;
@@ -287,6 +271,22 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     }
   }
 
+  if constexpr (PART) {
+    float *part = a.part + (int64_t)split * a.M * a.K;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int64_t k = k0 + col_of(32 * j + lr);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t m = row0 + 32 * i + 8 * (e >> 2) + 4 * lh + (e & 3);
+          if (m < a.M && k < a.K) part[m * a.K + k] = acc[i][j][e];
+        }
+      }
+    return;
+  }
+
   // Store through LDS: each wave turns its 32-row blocks into whole 16-byte
   // pieces of dX's rows.  ws1 (the stages of G too) is no longer read; ws0 may
   // still be (adapter), so the blocks lie in ws1, gs0 and gs1.
@@ -315,9 +315,9 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
   }
 }
 
-// dX = bf16(sum of the splits' partial products + the adapter term), one thread
-// per 8 columns (one generator call).  The workgroups past dX's (`blocks`) reduce
-// the call's two column sums: launches are what a small call costs.
+// dX = bf16(sum of the splits' partial products), one thread per 8 columns.  The
+// workgroups past dX's (`blocks`) reduce the call's two column sums: launches are
+// what a small call costs.
 __global__ __launch_bounds__(256) void mx_dx_finish_kernel(MxDxArgs a, ColSumArgs c0, ColSumArgs c1, int blocks) {
   __shared__ float tile[64 * 17];
   if ((int)blockIdx.x >= blocks) {
@@ -325,59 +325,48 @@ __global__ __launch_bounds__(256) void mx_dx_finish_kernel(MxDxArgs a, ColSumArg
     colsum_reduce(b < n0 ? c0 : c1, b < n0 ? b : b - n0, tile);
     return;
   }
-  const int64_t per = a.K / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.M * per) return;
-  const int64_t m = i / per, k = 8 * (i % per);
-  float v[8], t[8];
+  const int64_t n = a.M * a.K, i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (i >= n) return;
+  f32x4 v0 = {0.0f, 0.0f, 0.0f, 0.0f}, v1 = v0;
+  for (int q0 = 0; q0 < a.splits; q0 += 4) {   // four loads at a time, past the last one again
+    f32x4 x[4][2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = t[e] = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part + ((int64_t)s * a.M + m) * a.K + k);
-    const f32x4 x = p[0], y = p[1];
-    const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += z[e];
-  }
-  for (int64_t j = 0; j < a.r; ++j) {
-    const float h = bf16_to_f32(a.dHb[m * a.ldh + j]);
-    const u32x4 x = *reinterpret_cast<const u32x4 *>(a.A + j * a.K + k);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      t[2 * e] += h * bf16_lo(w[e]);
-      t[2 * e + 1] += h * bf16_hi(w[e]);
+    for (int q = 0; q < 4; ++q) {
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part + (int64_t)min(q0 + q, a.splits - 1) * n + i);
+      x[q][0] = p[0];
+      x[q][1] = p[1];
     }
-  }
-  uint32_t keep = 0xFFu;
-  if (a.drop.thr) {
-    const DropKey dk = drop_key(a.drop);
-    uint32_t w[4];
-    philox7((uint64_t)i, dk, w);
-    keep = keep_bits8(w, dk.thr2);
-  }
-  if (a.r)
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (keep >> e & 1u) v[e] += a.drop.c * t[e];
-  u32x4 o;
-  o.x = pack_bf16x2(v[0], v[1]); o.y = pack_bf16x2(v[2], v[3]);
-  o.z = pack_bf16x2(v[4], v[5]); o.w = pack_bf16x2(v[6], v[7]);
-  *reinterpret_cast<u32x4 *>(a.dX + m * a.K + k) = o;
+    for (int q = 0; q < 4; ++q)
+      if (q0 + q < a.splits) {
+        v0 += x[q][0];
+        v1 += x[q][1];
+      }
+  }
+  *reinterpret_cast<u32x4 *>(a.dX + i) = u32x4{pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
+                                               pack_bf16x2(v1[0], v1[1]), pack_bf16x2(v1[2], v1[3])};
 }
 
-// 256 x 256 tiles when they fill half the GPU or more, else 64 x 256 tiles, cut
-// over the contraction until they do (at least four steps per cut).
+// Rows of the tiles and cuts of the contraction, by the time of a launch: rounds
+// of workgroups over the CUs (one fits each) times a step's time (64 rows of W,
+// measured at 8192 x 8192) times the steps, and for cuts the partial products'
+// way to memory and back at 4.5 TB/s (their launch is there anyway: it reduces
+// the column sums too).
 struct DxPlan {
-  bool big;
-  int splits;
+  int rows, splits;
 };
 DxPlan dx_plan(int64_t M, int64_t N, int64_t K) {
-  const int64_t cus = device_cus(), cols = cdiv(K, 256);
-  if (cdiv(M, 256) * cols * 2 > cus) return DxPlan{true, 1};
-  const int64_t t = cdiv(M, 64) * cols;
-  int splits = 1;
-  while (splits < 8 && t * splits * 2 <= cus && N / 64 / (splits * 2) >= 4) splits *= 2;
-  return DxPlan{false, splits};
+  const int64_t cus = device_cus(), cols = cdiv(K, 256), steps = N / 64;
+  const struct { int rows; double us; } tile[3] = {{256, 1.62}, {128, 0.95}, {64, 0.62}};
+  DxPlan p{256, 1};
+  double best = 1e300;
+  for (const auto &t : tile)
+    for (int s = 1; s <= 8 && (s == 1 || steps / s >= 4); ++s) {
+      const double us = t.us * (double)cdiv(cdiv(M, t.rows) * cols * s, cus) * (double)cdiv(steps, s) +
+                        (s == 1 ? 0.0 : 0.5 + (double)(s * M * K) * 8.0 / 4.5e6);
+      if (us < best) { best = us; p = DxPlan{t.rows, s}; }
+    }
+  return p;
 }
 
 template <int TM, int TN, int WR, int WC>
@@ -388,16 +377,14 @@ hipError_t launch_tiles(const MxDxArgs &a, hipStream_t st) {
   const int gm = std::max(1, std::min(tiles_m, 4));
   const dim3 grid((unsigned)T, (unsigned)a.splits), block(512);
   TraceScope tr(QN_TRACE_MX_DX, st);
-  if constexpr (TM == 1) {
-    if (a.splits > 1) {
-      hipLaunchKernelGGL((mx_dx_kernel<TM, TN, WR, WC, false, true>), grid, block, 0, st, a, tiles_m, tiles_n, gm);
-      return hipGetLastError();
-    }
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, a, tiles_m, tiles_n, gm); };
+  if (a.splits > 1) {
+    if (a.drop.thr) go(mx_dx_kernel<TM, TN, WR, WC, true, true>);
+    else go(mx_dx_kernel<TM, TN, WR, WC, false, true>);
+  } else {
+    if (a.drop.thr) go(mx_dx_kernel<TM, TN, WR, WC, true, false>);
+    else go(mx_dx_kernel<TM, TN, WR, WC, false, false>);
   }
-  if (a.drop.thr)
-    hipLaunchKernelGGL((mx_dx_kernel<TM, TN, WR, WC, true, false>), grid, block, 0, st, a, tiles_m, tiles_n, gm);
-  else
-    hipLaunchKernelGGL((mx_dx_kernel<TM, TN, WR, WC, false, false>), grid, block, 0, st, a, tiles_m, tiles_n, gm);
   return hipGetLastError();
 }
 
@@ -412,7 +399,9 @@ hipError_t launch_mx_dx(const MxDxArgs &in, const ColSumArgs *sums, hipStream_t 
   MxDxArgs a = in;
   const DxPlan p = dx_plan(a.M, a.N, a.K);
   a.splits = p.splits;
-  const hipError_t e = p.big ? launch_tiles<4, 2, 2, 4>(a, st) : launch_tiles<1, 2, 2, 4>(a, st);
+  const hipError_t e = p.rows == 256   ? launch_tiles<4, 2, 2, 4>(a, st)
+                       : p.rows == 128 ? launch_tiles<2, 2, 2, 4>(a, st)
+                                       : launch_tiles<1, 2, 2, 4>(a, st);
   if (e != hipSuccess) return e;
   if (p.splits == 1) return sums ? launch_colsum_reduce(sums[0], sums[1], st) : hipSuccess;
   const int blocks = (int)cdiv(a.M * (a.K / 8), 256);

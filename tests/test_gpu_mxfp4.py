@@ -192,6 +192,15 @@ def test_large_tiles(r, p):
     run_mx(2100, 320, 4160, r, p, seed=r + 1)
 
 
+@pytest.mark.parametrize("M, N, K, r, p", [(100, 512, 320, 16, 0.3), (801, 512, 704, 9, None), (2700, 3584, 320, 40, 0.1),
+                                           (2650, 3584, 320, 5, None), (3290, 512, 1088, 16, 0.5), (3300, 3584, 1088, 8, 0.2),
+                                           (3270, 3584, 1088, 0, None), (3570, 512, 2304, 24, None)])
+def test_dX_tile_heights_and_cuts(M, N, K, r, p):
+    """dX on tiles of 64, 128 and 256 rows, cut over N or not, with and without a mask."""
+    say(f"mx dX plans M={M} N={N} K={K} r={r} p={p}")
+    run_mx(M, N, K, r, p, seed=r)
+
+
 @pytest.mark.parametrize("r, p", [(16, 0.2), (0, None)])
 def test_large_and_small_tiles_in_one_call(r, p):
     """A last round that is mostly empty: whole columns of it go to the small tiles, a second launch at column offsets."""
