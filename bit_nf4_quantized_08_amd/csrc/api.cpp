@@ -114,6 +114,8 @@ int drop_args(const qn_dropout_config *d, qn::DropArgs &out) {
   return QN_OK;
 }
 
+constexpr int64_t kMaxRows = (int64_t)1 << 24;   // rows of the MXFP4 linear and of a backward with dropout
+
 int check_mx(const qn_mx_matrix *W) {
   if (!W || !W->codes || !W->scales) return QN_ERR_NULL;
   if (W->rows <= 0 || W->cols <= 0 || W->cols > kMaxElems || W->rows > INT32_MAX / qn::mx_chunks(W->cols))
@@ -129,7 +131,8 @@ bool mx_shapes_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
   // dX; all of W's codes).
   if (K > (int64_t)1 << 22 || N > (int64_t)1 << 22) return false;
   if (N * 128 * qn::mx_chunks(K) > (int64_t)INT32_MAX) return false;
-  return M <= INT32_MAX / 64 && M <= ((int64_t)1 << 28) / qn::mx_chunks(K);   // X's scale bytes too
+  // X's scale bytes; the backward's factors, 128 ranks of M values.
+  return M <= kMaxRows && M <= ((int64_t)1 << 28) / qn::mx_chunks(K);
 }
 
 }  // namespace
@@ -474,6 +477,7 @@ int qlora_linear_bwd_dropout(const void *dY, const void *X, const float *H, int6
                              const void *A, const void *B, int64_t r, float alpha, const qn_dropout_config *drop,
                              void *dX, void *dA, void *dB, void *workspace, size_t ws_bytes, void *stream) {
   if (!drop) return QN_ERR_NULL;
+  if (M > kMaxRows) return QN_ERR_SHAPE;
   return linear_bwd(dY, X, H, M, W, A, B, r, alpha, drop, dX, dA, dB, workspace, ws_bytes, stream);
 }
 

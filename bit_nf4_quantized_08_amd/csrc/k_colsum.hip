@@ -1,22 +1,27 @@
-// Column sums over rows on the matrix cores (gfx950): out[j][c] = sum_m Lt[j][m] *
+// Column sums over rows on the matrix cores (gfx950): out[j][c] = sum_m L[j][m] *
 // Q[m][c] for j < R <= 64, the contraction of dA = dH^T (keep * X) and dB^T = (s
-// H)^T dY, which runs down the rows of row-major activations.  Lt is [rows, Mp]
-// bf16, zero beyond R and M.
+// H)^T dY, which runs down the rows of row-major activations.  L is fp32 given as
+// two bf16 pieces, the rounded value and the rounded rest (2^-17 of it is left
+// over), [2][rows, Mp] with rows = R rounded up to 32, zero beyond R and M: with
+// one piece the rounding of L would be as large as that of the bf16 result.
 //
-// Bound by reading Q once (4096 x 8192 bf16: 64 MiB); the products are 64 MACs
-// per element of Q, too many for vector dot products (the v_dot2 kernel of
-// k_lowrank.hip takes 150 us for the two sums at R = 64) and little for the
-// matrix cores.  The MFMA wants eight consecutive rows of one column, so a
-// 64-row x 256-column stage of Q goes through LDS as it lies and comes back by
-// the transposing read (ds_read_b64_tr_b16), as in k_mxdx.hip.  The stage is
-// filled through registers, not by direct loads: a 16-byte piece there is one
-// call of the dropout generator, so the mask is applied on the way.
+// Bound by reading Q once (4096 x 8192 bf16: 64 MiB); the products are 128 MACs
+// per element of Q at R = 64, too many for vector dot products (the v_dot2
+// kernel of k_lowrank.hip, with one piece, takes 150 us for the two sums of 4096
+// rows of 8192) and little for the matrix cores.  The MFMA wants eight
+// consecutive rows of one column, so a 64-row x 256-column stage of Q goes
+// through LDS as it lies and comes back by the transposing read
+// (ds_read_b64_tr_b16), as in k_mxdx.hip.  The stage is filled through registers,
+// not by direct loads: a 16-byte piece there is one call of the dropout
+// generator, so the mask is applied on the way.
 //
 // A workgroup (8 waves) owns 256 columns and a range of rows; wave w multiplies
 // columns 32 w .. + 31 with all ranks.  Stage of Q: row m (512 bytes), piece u of
 // 8 columns at slot u ^ 4 (m & 3), so that a transposing read's four rows fall
-// on different banks.  Stage of Lt: 64 ranks x 64 rows (128 bytes per rank),
-// direct loads, piece k of rank j at slot k ^ ((j >> 1) & 7).  Two stages each.
+// on different banks.  Stage of L: rank j (128 bytes), direct loads, piece k at
+// slot k ^ ((j >> 1) & 7), two stages.  Q has one stage, refilled between two
+// barriers from registers that were loaded a step earlier: with two, 64 ranks
+// would leave room for one workgroup on a CU, and half the loads in flight.
 // The partial sums of the row ranges go to `part` and are added in order by
 // the reduce kernel, so results depend on the shape alone.
 
@@ -35,10 +40,9 @@ constexpr int CS_COLS = 256;
 template <int RT, bool DROP>   // 32-rank tiles
 __global__ __launch_bounds__(CS_THREADS) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
-  __shared__ __attribute__((aligned(16))) uint8_t qs0[64 * 512];
-  __shared__ __attribute__((aligned(16))) uint8_t qs1[64 * 512];
-  __shared__ __attribute__((aligned(16))) uint8_t ls0[32 * RT * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t ls1[32 * RT * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t qs[64 * 512];
+  __shared__ __attribute__((aligned(16))) uint8_t ls0[64 * RT * 128];   // both pieces
+  __shared__ __attribute__((aligned(16))) uint8_t ls1[64 * RT * 128];
   const ColSumArgs a = blockIdx.z ? a1 : a0;
   const int64_t c0 = (int64_t)blockIdx.x * CS_COLS;
   if (c0 >= a.Ncols) return;   // the other sum is wider
@@ -66,7 +70,7 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
   if constexpr (DROP)
     if (dropping) dk = drop_key(a.drop);
   const uint64_t call0 = (uint64_t)qr * (uint64_t)(a.Ncols / 8) + (uint64_t)(c0 / 8 + qu);
-  auto store_q = [&](int s, uint8_t *dst) {
+  auto store_q = [&](int s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (DROP) {
@@ -77,16 +81,24 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
                          keep_mask2(w[3], dk.thr2)};
         }
       }
-      *reinterpret_cast<u32x4 *>(dst + qst + 8192 * i) = qv[i];
+      *reinterpret_cast<u32x4 *>(qs + qst + 8192 * i) = qv[i];
     }
   };
-  // Lt: direct load g covers ranks 8 g .. + 7, 64 rows (128 bytes); RT * 4 loads.
-  const int lj = 8 * wave + (lane >> 3);
-  const uint32_t lo = lj < a.R ? (uint32_t)(lj * a.Mp * 2 + 16 * ((lane & 7) ^ ((lj >> 1) & 7))) : kOutOfRange;
+  // L: direct load g covers stage rows 8 g .. + 7, 64 rows of Q (128 bytes); RT per
+  // wave.  Stage rows 0 .. 32 RT - 1 are the first piece's ranks, the others the
+  // second's, as in memory.
+  const int lj = 8 * RT * wave + (lane >> 3);
+  uint32_t lo[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int j = lj + 8 * i;
+    lo[i] = (uint32_t)(j * a.Mp * 2 + 16 * ((lane & 7) ^ ((j >> 1) & 7)));
+  }
   auto issue_l = [&](uint8_t *dst, int s) {
-    const rsrc_t rl = make_rsrc_u(a.Lt + (int64_t)s * 64, (a.R * a.Mp - (int64_t)s * 64) * 2);
-    if (wave < 4 * RT)
-      load_lds16(rl, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(dst)) + wave * 1024, lo, 0);
+    const rsrc_t rl = make_rsrc_u(a.Lt + (int64_t)s * 64, (64 * RT * a.Mp - (int64_t)s * 64) * 2);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      load_lds16(rl, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(dst)) + (wave * RT + i) * 1024, lo[i], 0);
   };
 
   f32x16 acc[RT];
@@ -102,44 +114,45 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
   for (int c = 0; c < 4; ++c) fl[c] = (uint32_t)(lr * 128 + 16 * ((4 * lh + c) ^ ((lr >> 1) & 7)));
   const int tr = (lane & 15) >> 2, tc = 32 * wave + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
   const uint32_t fq = (uint32_t)((32 * lh + tr) * 512 + 16 * ((tc >> 3) ^ (4 * tr)) + 2 * (tc & 7));
-  auto multiply = [&](const uint8_t *q, const uint8_t *l) {
+  auto multiply = [&](const uint8_t *l) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const bf16x8 b = read_transposed(q + fq + c * 4096, q + fq + c * 4096 + 2048);
+      const bf16x8 b = read_transposed(qs + fq + c * 4096, qs + fq + c * 4096 + 2048);
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8 *>(l + t * 32 * 128 + fl[c]), b,
-                                                         acc[t], 0, 0, 0);
+      for (int t = 0; t < 2 * RT; ++t)
+        acc[t % RT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            *reinterpret_cast<const bf16x8 *>(l + t * 32 * 128 + fl[c]), b, acc[t % RT], 0, 0, 0);
     }
   };
 
-  // Step s reads stage (s - s0) & 1; the other (last read before the previous
-  // barrier) receives step s + 1, whose rows of Q are in registers, and step s + 2
-  // is requested.  Those four loads stay in flight across the barrier: it waits
-  // for the direct load of Lt, issued before them, and for LDS only.
+  // Step s: L's stage of step s + 1 is asked for; Q's stage is multiplied; between
+  // the barriers it is refilled with step s + 1 from registers, and step s + 2 is
+  // requested.  Those four loads stay in flight across the second barrier,
+  // which waits for L's direct loads, issued before them.
   const int last = s1 - 1;
-  auto step = [&](int s, const uint8_t *q, const uint8_t *l, uint8_t *qn, uint8_t *ln) {
-    store_q(min(s + 1, last), qn);
-    __builtin_amdgcn_sched_barrier(0);
+  auto step = [&](int s, const uint8_t *l, uint8_t *ln) {
     issue_l(ln, min(s + 1, last));
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(l);
+    stage_barrier<15>();   // reads of the stage are done; any number of loads in flight
+    store_q(min(s + 1, last));
     __builtin_amdgcn_sched_barrier(0);
     load_q(min(s + 2, last));
     __builtin_amdgcn_sched_barrier(0);
-    multiply(q, l);
     stage_barrier<4>();
   };
   if (s0 < s1) {
     load_q(s0);
     issue_l(ls0, s0);
-    store_q(s0, qs0);
+    store_q(s0);
     __builtin_amdgcn_sched_barrier(0);
     load_q(min(s0 + 1, last));
     __builtin_amdgcn_sched_barrier(0);
     stage_barrier<4>();
     for (int s = s0; s < s1; s += 2) {
-      step(s, qs0, ls0, qs1, ls1);
+      step(s, ls0, ls1);
       if (s + 1 >= s1) break;
-      step(s + 1, qs1, ls1, qs0, ls0);
+      step(s + 1, ls1, ls0);
     }
   }
   // The loads past the end land before the wave ends (they write only its own

@@ -757,8 +757,8 @@ size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
   const int64_t Mp = align_up(M, BK);
   c.take<uint16_t>(rp * N);                 // B^T
   c.take<uint16_t>(M * rp);                 // dH bf16 [M, rp]
-  c.take<uint16_t>(rp * Mp);                // dH^T bf16 [rp, Mp]
-  c.take<uint16_t>(rp * Mp);                // (sH)^T bf16 [rp, Mp]
+  c.take<uint16_t>(2 * rp * Mp);            // dH^T bf16 [rp, Mp], two pieces on the newer paths
+  c.take<uint16_t>(2 * rp * Mp);            // (sH)^T likewise
   c.take<float>((int64_t)colred_splits(M) * r * N);   // dB partials
   c.take<float>((int64_t)colred_splits(M) * r * K);   // dA partials
   c.take<char>((int64_t)lowrank_part_bytes(M, N, r));  // dH partial products
@@ -777,8 +777,8 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   const int64_t Mp = align_up(a.M, BK);
   uint16_t *Bt = c.take<uint16_t>(rp * a.N);
   uint16_t *dHb = c.take<uint16_t>(a.M * rp);
-  uint16_t *dHt = c.take<uint16_t>(rp * Mp);
-  uint16_t *sHt = c.take<uint16_t>(rp * Mp);
+  uint16_t *dHt = c.take<uint16_t>(2 * rp * Mp);
+  uint16_t *sHt = c.take<uint16_t>(2 * rp * Mp);
   float *bpart = c.take<float>((int64_t)colred_splits(a.M) * a.r * a.N);
   float *apart = c.take<float>((int64_t)colred_splits(a.M) * a.r * a.K);
   float *dhpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(a.M, a.N, a.r)));
@@ -807,6 +807,7 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
       ld.P = a.B;
       ld.p_transposed = true;
       lh.given = a.H;   // (sH)^T from it, or H formed here
+      ld.t_pieces = lh.t_pieces = 2;
       QN_TRY(launch_lowrank2(ld, &lh, st));
     } else {
       QN_TRY(launch_lowrank2(ld, a.H ? nullptr : &lh, st));

@@ -342,8 +342,12 @@ __global__ __launch_bounds__(256) void lowrank_finish_kernel(LowRankGroup grp) {
     for (int idx = tid; idx < FIN_ROWS * 64; idx += 256) {
       const int jj = idx / FIN_ROWS, r = idx % FIN_ROWS;
       const int64_t m = m0 + r;
-      if (jj < a.ldt_rows && m < a.Mp)
-        a.out_t[(int64_t)jj * a.Mp + m] = (jj < a.R && m < a.M) ? f32_to_bf16(tile[r][jj] * a.scale) : (uint16_t)0;
+      if (jj < a.ldt_rows && m < a.Mp) {
+        const float v = (jj < a.R && m < a.M) ? tile[r][jj] * a.scale : 0.0f;
+        const uint16_t hi = f32_to_bf16(v);
+        a.out_t[(int64_t)jj * a.Mp + m] = hi;
+        if (a.t_pieces == 2) a.out_t[(a.ldt_rows + jj) * a.Mp + m] = f32_to_bf16(v - bf16_to_f32(hi));
+      }
     }
   }
 }

@@ -184,6 +184,7 @@ struct LowRankArgs {
   DropArgs drop = kNoDrop;   // thr > 0: L is read as keep * L and C scaled by c
   uint8_t *qc = nullptr;     // non-null (a launch of one product): MXFP4 of L (before dropout) is written
   uint8_t *qs = nullptr;     // too, codes [M, 128 C] and scales [C][M][8]
+  int t_pieces = 1;          // 2: out_t is [2][ldt_rows, Mp], the rounded value and the rounded rest
   bool p_transposed = false; // P is [Kc, R] (ldp not used)
   const float *given = nullptr;   // C itself, fp32 [M, R], scaled by drop.c already: the outputs only
 };
@@ -217,7 +218,7 @@ hipError_t launch_colred2(const ColRedArgs &a, const ColRedArgs *b, hipStream_t 
 // The same sums on the matrix cores (k_colsum.hip), for the MXFP4 linear and for
 // dropout: `part` holds splits * R * Ncols floats, Ncols % 64 == 0.
 struct ColSumArgs {
-  const uint16_t *Lt;
+  const uint16_t *Lt;  // [2][R rounded up to 32, Mp]: two bf16 pieces
   int64_t Mp;
   const uint16_t *Q;   // [M, Ncols]
   int64_t M, Ncols, R;

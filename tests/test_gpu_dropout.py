@@ -3,8 +3,9 @@ dropout on the adapter's input against the fp64 oracle.
 
 Tolerances of the linear are sums of what the kernels round: a bf16 output is
 off by at most 2^-8 of its value (half a step is eps/2 = 2^-8 with a step of
-2^-7), a bf16 operand of a product by 2^-8 of each term, and an fp32 sum of n
-terms by n 2^-23 of the sum of its terms' magnitudes (each addition rounds
+2^-7), a bf16 operand of a product (s H in Y, dH in dX) by 2^-8 of each term, an
+operand in two bf16 pieces (dH in dA, s H in dB) by 2^-16, and an fp32 sum of
+n terms by n 2^-23 of the sum of its terms' magnitudes (each addition rounds
 once, 2^-24; the factor 2 covers the products' own grouping).
 """
 
@@ -22,6 +23,7 @@ pytestmark = pytest.mark.gpu
 
 SEED, OFF = 0xFEDCBA9876543210, 0x0123456789ABCDEF
 HALF, EPS = 2.0 ** -8, 2.0 ** -23
+PIECES = 2.0 ** -16   # two bf16 pieces: 2^-8 of the rest, itself at most 2^-8 of the value
 
 
 def _bits(t):
@@ -97,7 +99,7 @@ def _inputs(M, N, K, r, seed):
     return W, X, A, B, G
 
 
-def check_step(Y, H, grads, G, X, base_in, What, A, B, alpha, keep, c, given_H):
+def check_step(Y, H, grads, G, X, base_in, What, A, B, alpha, keep, c, given_H, pieces=PIECES):
     """A forward's (Y, H) and a backward's (dX, dA, dB) within the rounding they do (see the top)."""
     ref_Y, ref_H = MX.linear_forward(base_in, X, What, A, B, alpha, keep, c)
     ab = np.abs
@@ -118,16 +120,17 @@ def check_step(Y, H, grads, G, X, base_in, What, A, B, alpha, keep, c, given_H):
     dX, dA, dB = grads
     rX, rA, rB = MX.linear_backward(G, X, What, A, B, alpha, keep, c, H=given_H)
     dH = s * (G @ B)
-    dH_err = HALF * ab(dH) + N * EPS * s * (ab(G) @ ab(B))
+    dH_sum = N * EPS * s * (ab(G) @ ab(B))
+    dH_err = HALF * ab(dH) + dH_sum
     if dX is not None:
         tol = HALF * ab(rX) + N * EPS * (ab(G) @ ab(What)) + km * (dH_err @ ab(A) + r * EPS * (ab(dH) @ ab(A)))
         e = ab(host(dX).astype(np.float64) - rX)
         assert np.all(e <= tol), f"dX off by {(e / tol).max():.2f} of its tolerance"
-    tol = HALF * ab(rA) + (dH_err.T @ kx) + M * EPS * (ab(dH).T @ kx)
+    tol = HALF * ab(rA) + ((pieces * ab(dH) + dH_sum).T @ kx) + M * EPS * (ab(dH).T @ kx)
     e = ab(host(dA).astype(np.float64) - rA)
     assert np.all(e <= tol), f"dA off by {(e / tol).max():.2f} of its tolerance"
     Hb = ref_H if given_H is None else given_H
-    tol = HALF * ab(rB) + s * (ab(G).T @ (HALF * ab(Hb) + (H_err if given_H is None else 0.0))) \
+    tol = HALF * ab(rB) + s * (ab(G).T @ (pieces * ab(Hb) + (H_err if given_H is None else 0.0))) \
         + M * EPS * s * (ab(G).T @ ab(Hb))
     e = ab(host(dB).astype(np.float64) - rB)
     assert np.all(e <= tol), f"dB off by {(e / tol).max():.2f} of its tolerance"
@@ -156,7 +159,8 @@ def run_nf4(M, N, K, r, p, variant=0, dq=True, give_H=True, want_dX=True, seed=0
     keep = D.keep(M * K, p, SEED + seed, OFF).reshape(M, K)
     Xv, Av, Bv, Gv = (synth.bf16_values(t).astype(np.float64) for t in (X, A, B, G))
     check_step(Y, H, grads, Gv, Xv, Xv, What.astype(np.float64), Av, Bv, alpha, keep, D.scale(p),
-               host(H).astype(np.float64) if give_H else None)
+               host(H).astype(np.float64) if give_H else None,
+               pieces=PIECES if D.threshold(p) else HALF)   # p = 0 runs the plain backward, one piece
     return Y, H, grads
 
 

@@ -61,6 +61,8 @@ def test_mx_workspace_size_rules():
         assert f(op, 0, 64, 64, 8) == f(op, 8, 63, 64, 8) == f(op, 8, 64, 96, 8) == f(op, 8, 64, 64, 65) == 0
         assert f(op, 8, 64, 64, -1) == f(op, 8, (1 << 22) + 64, 64, 8) == f(op, 8, 64, (1 << 22) + 64, 8) == 0
         assert f(op, 8, 1 << 20, 1 << 20, 8) == 0 and f(op, 1 << 40, 64, 64, 8) == 0
+        assert f(op, 1 << 24, 64, 64, 8) > 0 and f(op, (1 << 24) + 1, 64, 64, 8) == 0
+        assert f(op, (1 << 28) // 128 + 1, 64, 1 << 15, 8) == 0
     assert f(2, 8, 64, 64, 8) == 0
     assert lib.workspace_size(lib.QN_OP_FWD_DROPOUT, 1, 64, 64, 8) > 0
     assert lib.workspace_size(lib.QN_OP_FWD_DROPOUT, 1, 64, 60, 8) == 0
@@ -111,7 +113,7 @@ def test_nf4_dropout_refusals():
         vp(FAKE), vp(FAKE), vp(0), M, ctypes.byref(w), vp(FAKE), vp(FAKE), 8, 16.0, d, vp(FAKE), vp(dA), vp(FAKE),
         vp(FAKE), n, vp(0))
     assert b(d=None) == b(dA=0) == NULL
-    assert b(M=0) == SHAPE and b(d=drop(float("nan"))) == VALUE and b(n=16) == WORKSPACE
+    assert b(M=0) == b(M=(1 << 24) + 1) == SHAPE and b(d=drop(float("nan"))) == VALUE and b(n=16) == WORKSPACE
 
 
 def test_python_refusals():
