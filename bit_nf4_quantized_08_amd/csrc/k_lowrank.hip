@@ -202,9 +202,10 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
   // Step cb + d reads register slot d and LDS buffer d & 1 (LR_DEPTH is even).
   static_assert(LR_DEPTH % 2 == 0, "LDS buffer parity follows the slot");
   const int64_t n = c1 - c0;
-  uint32_t qb[4] = {};
-  const int64_t qpitch = (a.Kc + QN_MX_CHUNK - 1) / QN_MX_CHUNK * (QN_MX_CHUNK / 8);   // dwords per row of codes
+  uint32_t qb[4] = {}, qv[4][LR_DEPTH];
+  const int64_t qpitch = (a.Kc + QN_MX_CHUNK - 1) / QN_MX_CHUNK * (QN_MX_CHUNK / 2);   // bytes per row of codes
   (void)qb;
+  (void)qv;
   (void)qpitch;
   if (n > 0) {
     const int64_t np = (n + LR_DEPTH - 1) / LR_DEPTH * LR_DEPTH;
@@ -222,9 +223,7 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
             const u32x4 u[1] = {xr[d][i]};
             const uint32_t b = scale_byte<true>(quad_max(unit_amax<true>(u)));
             qb[i] = d == 0 ? b : qb[i] | b << (8 * d);
-            const int64_t m = m0 + 32 * wave + 8 * i + (lane >> 3);
-            if (m < a.M)
-              reinterpret_cast<uint32_t *>(a.qc)[m * qpitch + (c0 + cb + d) * (LR_CK / 8) + (lane & 7)] = unit_codes<true>(u, b);
+            qv[i][d] = unit_codes<true>(u, b);
           }
         }
         if constexpr (DROP) {
@@ -257,8 +256,25 @@ __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup g
         __syncthreads();
       }
       if constexpr (QUANT) {
+        // The chunk's codes, 128 bytes a row, through the wave's LDS region (its
+        // slab of the last step has been read) into whole 16-byte stores; stored
+        // a step at a time they would be 32-byte pieces of lines.
         // qb: the first quad of a row's eight lanes holds the even blocks' bytes
         // of the chunk, the second the odd ones'.
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int d = 0; d < LR_DEPTH; ++d)
+            *reinterpret_cast<uint32_t *>(xslab + (8 * i + (lane >> 3)) * 128 + 32 * d + 4 * (lane & 7)) = qv[i][d];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rho = 8 * i + (lane >> 3);
+          if (m0 + 32 * wave + rho < a.M)
+            *reinterpret_cast<u32x4 *>(a.qc + (m0 + 32 * wave + rho) * qpitch + (c0 + cb) / LR_DEPTH * 128 + 16 * (lane & 7)) =
+                *reinterpret_cast<const u32x4 *>(xslab + rho * 128 + 16 * (lane & 7));
+        }
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t odd = (uint32_t)__builtin_amdgcn_ds_bpermute((lane | 4) * 4, (int)qb[i]);
