@@ -7,15 +7,23 @@
 // codes go from memory to the matrix cores without any expansion.  A product
 // of two codes is exact and every sum is fp32.
 //
-// Kernels:
-//   mx_quantize_kernel   fp32 or bf16 rows -> codes and scales (bound by memory)
-//   mx_dequant_kernel    codes and scales -> fp32 or bf16 (bound by memory)
-//   mx_gemm_kernel       tiles of mx(X) W^T with the adapter term (bound by the
-//                        matrix cores and the clock they sustain), optionally
-//                        over a part of K with fp32 partial sums
-//   mx_prep_kernel       M <= 32: X^ and the adapter's H partials
-//   mx_decode_kernel     M <= 32: streams the weights (bound by memory)
-//   mx_finish_kernel     adds partial products and the adapter term
+// Kernels, with times on their own (a traced launch) where the bound shows:
+//   mx_quantize_kernel   fp32 or bf16 rows -> codes and scales; bound by memory
+//                        (4096 x 8192 bf16: 85 MB, 15.3 us, 5.5 TB/s)
+//   mx_dequant_kernel    codes and scales -> fp32 or bf16; bound by memory (the
+//                        same to bf16: 15.7 us, 5.4 TB/s)
+//   mx_gemm_kernel       tiles of mx(X) W^T with the adapter term, optionally over
+//                        a part of K with fp32 partial sums; bound by the matrix
+//                        cores and the clock they sustain (4096 x 8192 x 8192, r =
+//                        64: 134 to 138 us, 4.1 PFLOP/s; matrix pipes busy 57 % of
+//                        the cycles at 1.75 GHz, loads into LDS next)
+//   mx_prep_kernel       few rows: X^ and the adapter's H partials; bound by its
+//                        launch and one memory latency (M = 1, K = 8192, r = 64: 4.0 us)
+//   mx_decode_kernel     M <= 32: streams the weights; bound by memory (M = 13, 28672
+//                        x 8192: 125 MB, 22 us, 5.7 TB/s; M = 1, 8192 x 8192: 36 MB,
+//                        8.7 us, 4.1 TB/s, a third of it start and end)
+//   mx_finish_kernel     adds partial products and the adapter term; bound by its
+//                        launch at the sizes that cut K (about 5 us)
 
 #include <algorithm>
 
@@ -459,25 +467,25 @@ void mx_gemm_kernel(MxGemmArgs a) {
 
 // ------------------------------------------------------------------ few rows
 // M <= 32, two launches.  The first quantises X and forms partial sums of H = X
-// A^T; the second streams the weights and, when a workgroup's waves cover all
-// of K (up to 8192 columns), finishes Y.
+// A^T (in the streaming kernel every workgroup would repeat both: 11.4 + 9.8 us
+// against 5.2 + 8.9 at M = 1, 8192 x 8192, r = 64); the second streams the weights
+// and, when a workgroup's waves cover all of K (up to 8192 columns), finishes Y.
 //
 // Streaming: a wave owns 16 weight rows x 1024 columns at a time, eight
 // sub-steps of v_mfma_scale_f32_16x16x128 with the weights as the first operand
 // (lane: row lane % 16, block lane / 16 of the sub-step's four) and X^ in groups
-// of 16 rows, held in registers, as the second.  The codes come through LDS by direct loads of two rows x
-// 512 contiguous bytes each: read straight into the fragments they would come
-// as 64-byte pieces of 16 rows (8192 x 8192, M = 1: 10.4 against 12.1 us).  The
-// wave reads a group's eight fragments into registers and asks for the next
-// group before it multiplies, so its 8 KB of LDS are always on their way.  16-byte
-// piece p of row r sits at slot p ^ r, which spreads a fragment read's 16 rows
-// over the banks.
+// of 16 rows, held in registers, as the second.  The codes come through LDS by
+// direct loads of two rows x 512 contiguous bytes each: read straight into the
+// fragments they would come as 64-byte pieces of 16 rows (8192 x 8192, M = 1, when
+// this was measured: 10.4 against 12.1 us).  The wave reads a group's eight
+// fragments into registers and asks for the next group before it multiplies, so
+// its 8 KB of LDS are always on their way.  16-byte piece p of row r sits at slot
+// p ^ r, which spreads a fragment read's 16 rows over the banks.
 // A workgroup's 8 waves cover nk (a power of two) column segments of 8 / nk
 // sets of row groups; partial sums meet in LDS.
 constexpr int DW = 8;                 // waves
 constexpr int DSEG = 1024;            // columns per wave
 constexpr int DSUB = DSEG / 128;      // sub-steps
-constexpr int HSEG = 256;             // columns per wave of the H partials
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
 
@@ -497,7 +505,8 @@ struct MxPrepArgs {
 
 // H partials: workgroup b of them takes 16 rows of X, 16 ranks of A and 8 x HSEG
 // columns.
-__device__ void prep_h(const MxPrepArgs &a, int b, float (*red)[256]) {
+template <int HSEG>
+__device__ __forceinline__ void prep_h(const MxPrepArgs &a, int b, float (*red)[256]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, kb = lane >> 4;
   const int mg = b % a.mgroups, jt = b / a.mgroups / a.hsplits, hs = b / a.mgroups % a.hsplits, j = 16 * jt + l16;
   const int64_t m = 16 * mg + l16;
@@ -538,13 +547,14 @@ __device__ void prep_h(const MxPrepArgs &a, int b, float (*red)[256]) {
   }
 }
 
+template <int HSEG>
 __global__ __launch_bounds__(64 * DW) void mx_prep_kernel(MxPrepArgs a) {
   __shared__ float red[DW][256];
   if ((int)blockIdx.x < a.qblocks)
     quantize_units<true, true, 64 * DW, 1>(reinterpret_cast<const uint8_t *>(a.X), (uint32_t)a.M, a.K, a.cd, a.chunks,
                                            blockIdx.x * (64 * DW / 32), a.xc, a.xs);
   else
-    prep_h(a, (int)blockIdx.x - a.qblocks, red);
+    prep_h<HSEG>(a, (int)blockIdx.x - a.qblocks, red);
 }
 
 // Adapter operands of a 16 x 16 block of Y (v_mfma_f32_16x16x32_bf16, B's rows
@@ -564,35 +574,39 @@ struct AdapterArgs {
   float *H_out;        // or null
 };
 
-// `store`: this lane's ranks of row m go to H_out.
-__device__ __forceinline__ HPieces load_h(const AdapterArgs &a, int64_t M, int64_t m, int j0, bool store) {
-  float h[8];
+// c * the sum of H's partial sums first .. end - 1, ranks j0 .. + 7 of row m.
+__device__ __forceinline__ void sum_h(const AdapterArgs &a, int64_t M, int64_t m, int j0, int first, int end, float (&h)[8]) {
 #pragma unroll
   for (int t = 0; t < 8; ++t) h[t] = 0.0f;
   // Batches of four partial sums, loaded without a condition (past the last
   // one it is read again and dropped), so that a batch waits once.
   const int jc = j0 < a.ldh ? j0 : 0;
-  for (int q0 = 0; q0 < a.hsplits; q0 += 4) {
+  for (int q0 = first; q0 < end; q0 += 4) {
     f32x4 v[4][2];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.hp + ((int64_t)min(q0 + q, a.hsplits - 1) * M + m) * a.ldh + jc);
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.hp + ((int64_t)min(q0 + q, end - 1) * M + m) * a.ldh + jc);
       v[q][0] = p[0];
       v[q][1] = p[1];
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (q0 + q < a.hsplits)
+      if (q0 + q < end)
 #pragma unroll
         for (int t = 0; t < 8; ++t) h[t] += v[q][t >> 2][t & 3];
   }
-  uint32_t hi[4], lo[4];
 #pragma unroll
   for (int t = 0; t < 8; ++t) h[t] = j0 + t < a.r ? h[t] * a.c : 0.0f;
-  if (store)
+}
+
+__device__ __forceinline__ void store_h(const AdapterArgs &a, int64_t m, int j0, const float (&h)[8]) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if (j0 + t < a.r) a.H_out[m * a.r + j0 + t] = h[t];
+  for (int t = 0; t < 8; ++t)
+    if (j0 + t < a.r) a.H_out[m * a.r + j0 + t] = h[t];
+}
+
+__device__ __forceinline__ HPieces pieces_of(const AdapterArgs &a, const float (&h)[8]) {
+  uint32_t hi[4], lo[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const float x = a.s * h[2 * t], y = a.s * h[2 * t + 1];
@@ -703,6 +717,21 @@ __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4)))
           0, 0);
   };
   load_w(0);
+  // With one group of each, the adapter's operands are requested here too, behind
+  // the weights.
+  constexpr bool PRE = G == 1 && MB == 1;
+  f32x4 ph[2][2] = {};
+  bf16x8 pb[2] = {};
+  if (PRE && a.out && a.ad.hp && seg < a.ad.hsplits) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (32 * q >= a.ad.r) break;
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.ad.hp + ((int64_t)seg * a.M + min((int64_t)l16, a.M - 1)) * a.ad.ldh + 32 * q + 8 * kb);
+      ph[q][0] = p[0];
+      ph[q][1] = p[1];
+      pb[q] = load_b(a.ad, min(n0 + l16, a.N - 1), 32 * q + 8 * kb);
+    }
+  }
 
   f32x4 acc[G][MB];
 #pragma unroll
@@ -737,16 +766,32 @@ __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4)))
     }
   }
   // acc[g][b][e]: weight row 16 g + 4 kb + e, row 16 b + l16 of X.
-  if (a.out && a.ad.hp && seg == 0) {
+  // The adapter term is linear in H, so each wave adds that of the partial sums
+  // its segment index selects (with one workgroup over K there is one per
+  // segment), and none stands at all of them.
+  if (a.out && a.ad.hp && seg < a.ad.hsplits) {
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
       const int64_t m = 16 * b + l16, mc = min(m, a.M - 1);
-#pragma unroll 1
-      for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32) {
-        const HPieces h = load_h(a.ad, a.M, mc, j0, a.ad.H_out && rb == 0 && rg == 0 && m < a.M);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int j0 = 32 * q + 8 * kb;
+        if (32 * q >= a.ad.r) break;
+        float h[8];
+        if (PRE) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) h[t] = j0 + t < a.ad.r ? ph[q][t >> 2][t & 3] * a.ad.c : 0.0f;
+        } else {
+          sum_h(a.ad, a.M, mc, j0, seg, seg + 1, h);
+        }
+        const HPieces p = pieces_of(a.ad, h);
 #pragma unroll
         for (int g = 0; g < G; ++g)
-          acc[g][b] = add_adapter(acc[g][b], load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0), h);
+          acc[g][b] = add_adapter(acc[g][b], PRE ? pb[q] : load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0), p);
+        if (a.ad.H_out && rb == 0 && rg == 0 && seg == 0) {
+          sum_h(a.ad, a.M, mc, j0, 0, a.ad.hsplits, h);
+          if (m < a.M) store_h(a.ad, m, j0, h);
+        }
       }
     }
   }
@@ -808,7 +853,10 @@ __global__ __launch_bounds__(256) void mx_finish_kernel(MxFinishArgs a) {
   } else if (a.ad.hp) {
     for (int j0 = 8 * kb; j0 - 8 * kb < a.ad.r; j0 += 32) {
       const bf16x8 b = load_b(a.ad, n0 + l16, j0);
-      acc = add_adapter(acc, b, load_h(a.ad, a.M, mc, j0, a.ad.H_out && blockIdx.x == 0 && wave == 0 && in));
+      float h[8];
+      sum_h(a.ad, a.M, mc, j0, 0, a.ad.hsplits, h);
+      if (a.ad.H_out && blockIdx.x == 0 && wave == 0 && in) store_h(a.ad, m, j0, h);
+      acc = add_adapter(acc, b, pieces_of(a.ad, h));
     }
   }
   // acc[e]: column n0 + 4 kb + e, row m.
@@ -891,7 +939,12 @@ struct FwdPieces {
   uint16_t *sH;            // bf16 s H (tiles that finish Y themselves)
   size_t bytes;
 };
-int prep_hsplits(int64_t K);
+// Columns per wave of a partial sum of H: 128 where the streaming kernel finishes
+// Y, so that there is one sum per segment and each wave adds its own (M = 1, 8192 x
+// 8192, r = 64: 4.0 + 8.7 us against 5.1 + 9.0 with 256 columns and one wave adding
+// them all); 256, half the sums to add, where another kernel finishes it.
+int prep_hseg(int64_t M, int64_t N, int64_t K) { return M <= kDecodeRows && decode_plan(M, N, K).ksplits == 1 ? 128 : 256; }
+int prep_hsplits(int64_t M, int64_t N, int64_t K) { return (int)cdiv(K, DW * prep_hseg(M, N, K)); }
 // Rows up to which split tiles take X^ and H from the few-row path's first launch
 // and leave H's partial sums to their finishing kernel (each of its waves reads
 // them for its rows): the low-rank kernel has one workgroup per 128 rows and
@@ -907,7 +960,7 @@ FwdPieces fwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r) {
   const int splits = M <= kDecodeRows ? decode_plan(M, N, K).ksplits : gemm_plan(M, N, C).splits;
   if (splits > 1) p.y_part = c.take<float>((int64_t)splits * M * N);
   if (r && (M <= kDecodeRows || (M <= kPrepRows && splits > 1))) {
-    p.h_part = c.take<float>((int64_t)prep_hsplits(K) * M * 64);
+    p.h_part = c.take<float>((int64_t)prep_hsplits(M, N, K) * M * 64);
   } else if (r) {
     p.h_part = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
     p.sH = c.take<uint16_t>(M * 64);
@@ -939,15 +992,16 @@ hipError_t launch_finish(const MxFinishArgs &f, hipStream_t st) {
 }
 
 // X^ and H's partial sums (h_part [prep_hsplits][M][64]).
-int prep_hsplits(int64_t K) { return (int)cdiv(K, DW * HSEG); }
 hipError_t launch_prep(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
   const int64_t C = mx_chunks(a.K);
   const uint32_t chunks = (uint32_t)(a.M * C);
-  const int qblocks = (int)cdiv(chunks, 64 * DW / 32), mgroups = (int)cdiv(a.M, 16), hsplits = prep_hsplits(a.K);
+  const int qblocks = (int)cdiv(chunks, 64 * DW / 32), mgroups = (int)cdiv(a.M, 16), hsplits = prep_hsplits(a.M, a.N, a.K);
   const int hblocks = a.r ? (int)cdiv(a.r, 16) * hsplits * mgroups : 0;
   const MxPrepArgs q{a.X, a.M, a.K, fast_div((uint32_t)C), chunks, w.xc, w.xs, qblocks, a.A, a.r, a.drop,
                      w.h_part, hsplits, mgroups};
-  hipLaunchKernelGGL(mx_prep_kernel, dim3((unsigned)(qblocks + hblocks)), dim3(64 * DW), 0, st, q);
+  const dim3 grid((unsigned)(qblocks + hblocks)), block(64 * DW);
+  if (prep_hseg(a.M, a.N, a.K) == 128) hipLaunchKernelGGL(mx_prep_kernel<128>, grid, block, 0, st, q);
+  else hipLaunchKernelGGL(mx_prep_kernel<256>, grid, block, 0, st, q);
   return hipGetLastError();
 }
 
@@ -956,7 +1010,7 @@ hipError_t run_decode(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
   const int64_t C = mx_chunks(a.K);
   const dim3 block(64 * DW);
   QN_TRY(launch_prep(a, w, st));
-  const AdapterArgs ad{nullptr, a.r ? w.h_part : nullptr, prep_hsplits(a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
+  const AdapterArgs ad{nullptr, a.r ? w.h_part : nullptr, prep_hsplits(a.M, a.N, a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
   const MxDecodeArgs d{w.xc, w.xs, a.M, a.N, C, a.codes, a.scales, ad, p.ksplits == 1 ? a.Y : nullptr, w.y_part,
                        p.nk, p.row_blocks};
   const dim3 grid((unsigned)(p.row_blocks * p.ksplits));
@@ -1022,7 +1076,6 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
   } else if (!w.sH) {
     QN_TRY(launch_prep(a, w, st));
   } else {   // one pass over X: its low-rank product and its quantisation
-
     LowRankArgs l{};
     l.L = a.X; l.ldl = a.K; l.M = a.M; l.Kc = a.K;
     l.P = a.A; l.ldp = a.K; l.R = a.r; l.scale = a.s; l.drop = a.drop;
@@ -1047,7 +1100,7 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
   }
   if (p.splits == 1) return launch_tiles<2, 2, 2, 2, false>(g, st);
   QN_TRY((launch_tiles<2, 2, 2, 2, true>(g, st)));
-  const AdapterArgs ad{w.sH, a.r ? w.h_part : nullptr, prep_hsplits(a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
+  const AdapterArgs ad{w.sH, a.r ? w.h_part : nullptr, prep_hsplits(a.M, a.N, a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
   return launch_finish(MxFinishArgs{w.y_part, p.splits, ad, a.M, a.N, a.Y}, st);
 }
 

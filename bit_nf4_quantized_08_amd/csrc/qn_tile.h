@@ -31,12 +31,6 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t lds, uint32_t voff
                                            0, 0);
 }
 
-// The same with 4 bytes per lane.
-__device__ __forceinline__ void load_lds4(rsrc_t r, uint32_t lds, uint32_t voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(size_t)lds, 4, voff, soff,
-                                           0, 0);
-}
-
 // Barrier that publishes a stage: before it arrives, the wave's LDS accesses are
 // done and all but the last IN_FLIGHT of its global loads (direct-to-LDS loads
 // among them) have landed.  The loads that may stay in flight must be the last
