@@ -290,7 +290,7 @@ size_t qlora_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t r) 
   if (K % QN_BLOCK != 0 || N % QN_BLOCK != 0) return 0;
   if (M > kMaxElems / K || M > kMaxElems / N) return 0;
   if (op == QN_OP_FWD) return qn::fwd_workspace(M, N, K, r);
-  if (op == QN_OP_BWD) return qn::bwd_workspace(M, N, K, r);
+  if (op == QN_OP_BWD) return qn::bwd_workspace(M, N, K, r) + qn::qgemm_part_bytes(M, K, N);   // with dropout or without
   if (op == QN_OP_FWD_DROPOUT) return qn::fwd_dropout_workspace(M, N, K, r);
   return 0;
 }
@@ -445,7 +445,7 @@ static int linear_bwd(const void *dY, const void *X, const float *H, int64_t M, 
   qn::DropArgs d;
   st = drop_args(drop, d);
   if (st != QN_OK) return st;
-  const size_t need = qn::bwd_workspace(M, W->N, W->K, r);
+  const size_t need = qn::bwd_workspace(M, W->N, W->K, r) + (d.thr ? qn::qgemm_part_bytes(M, W->K, W->N) : 0);
   if (!workspace || ws_bytes < need) return QN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QN_ERR_ALIGN;
   if (!qn::codec_tables_ok()) return QN_ERR_VALUE;

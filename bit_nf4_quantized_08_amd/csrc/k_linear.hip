@@ -590,6 +590,7 @@ size_t fwd_dropout_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
   Carve c(nullptr);
   c.take<uint16_t>(M * align_up(r, 8));
   c.take<char>((int64_t)lowrank_part_bytes(M, K, r));
+  c.take<char>((int64_t)qgemm_part_bytes(M, N, K));
   return c.off;
 }
 
@@ -710,7 +711,15 @@ hipError_t run_fwd_dropout(const FwdArgs &a, hipStream_t st) {
   QGemmArgs g;
   fwd_mfma_args(a, la, g);
   QN_TRY(launch_lowrank(la, st));
-  return launch_qgemm_fwd(g, st);
+  // Without dropping the result is the plain linear's, bit for bit: not cut.
+  g.splits = a.drop.thr ? qgemm_splits(a.M, a.N, a.K) : 1;
+  if (g.splits == 1) return launch_qgemm_fwd(g, st);
+  Carve c(a.ws);
+  c.take<uint16_t>(a.M * align_up(a.r, 8));
+  c.take<char>((int64_t)lowrank_part_bytes(a.M, a.K, a.r));
+  g.part = c.take<float>((int64_t)g.splits * a.M * a.N);
+  QN_TRY(launch_qgemm_split(g, false, st));
+  return launch_split_sum(g.part, g.splits, a.M * a.N, a.Y, nullptr, st);
 }
 
 hipError_t run_fwd_group(const FwdArgs *a, int n, hipStream_t st) {
@@ -823,7 +832,7 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     sums[0] = ColSumArgs{sHt, Mp, a.dY, a.M, a.N, a.r, bpart, splits, a.dB, true, kNoDrop};
     sums[1] = ColSumArgs{dHt, Mp, a.X, a.M, a.K, a.r, apart, splits, a.dA, false, a.drop};
     QN_TRY(launch_colsum2(sums[0], sums[1], st, QN_TRACE_GEMM_DB));
-    if (!a.dX || !a.mx_scales) QN_TRY(launch_colsum_reduce(sums[0], sums[1], st));
+    if (!a.dX) return launch_colsum_reduce(sums[0], sums[1], st);
   } else {
     ColRedArgs cb{}, ca{};
     cb.Lt = sHt; cb.Mp = Mp; cb.Q = a.dY; cb.ldq = a.N; cb.M = a.M; cb.Ncols = a.N; cb.R = a.r;
@@ -845,6 +854,13 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     g.qtype = a.sc.qtype;
     g.L2 = dHb; g.ldl2 = rp; g.R2 = a.A; g.ldr2 = a.K; g.r = a.r;
     g.out = a.dX; g.ldo = a.K; g.drop = a.drop;
+    g.splits = fused ? qgemm_splits(a.M, a.K, a.N) : 1;
+    if (g.splits > 1) {
+      g.part = c.take<float>((int64_t)g.splits * a.M * a.K);
+      QN_TRY(launch_qgemm_split(g, true, st));
+      return launch_split_sum(g.part, g.splits, a.M * a.K, a.dX, sums, st);
+    }
+    if (fused) QN_TRY(launch_colsum_reduce(sums[0], sums[1], st));
     QN_TRY(launch_qgemm_dx(g, st));
   }
   return hipSuccess;

@@ -315,36 +315,38 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
   }
 }
 
-// dX = bf16(sum of the splits' partial products), one thread per 8 columns.  The
-// workgroups past dX's (`blocks`) reduce the call's two column sums: launches are
-// what a small call costs.
-__global__ __launch_bounds__(256) void mx_dx_finish_kernel(MxDxArgs a, ColSumArgs c0, ColSumArgs c1, int blocks) {
+// out = bf16(sum of the splits' partial products), one thread per 8 of its n
+// elements (dX, and the NF4 linear's split products).  The workgroups past
+// out's (`blocks`) reduce the call's two column sums: launches are what a small
+// call costs.
+__global__ __launch_bounds__(256) void split_sum_kernel(const float *part, int splits, int64_t n, uint16_t *out,
+                                                        ColSumArgs c0, ColSumArgs c1, int blocks) {
   __shared__ float tile[64 * 17];
   if ((int)blockIdx.x >= blocks) {
     const int b = (int)blockIdx.x - blocks, n0 = (int)colsum_reduce_blocks(c0);
     colsum_reduce(b < n0 ? c0 : c1, b < n0 ? b : b - n0, tile);
     return;
   }
-  const int64_t n = a.M * a.K, i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (i >= n) return;
   f32x4 v0 = {0.0f, 0.0f, 0.0f, 0.0f}, v1 = v0;
-  for (int q0 = 0; q0 < a.splits; q0 += 4) {   // four loads at a time, past the last one again
+  for (int q0 = 0; q0 < splits; q0 += 4) {   // four loads at a time, past the last one again
     f32x4 x[4][2];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part + (int64_t)min(q0 + q, a.splits - 1) * n + i);
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(part + (int64_t)min(q0 + q, splits - 1) * n + i);
       x[q][0] = p[0];
       x[q][1] = p[1];
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (q0 + q < a.splits) {
+      if (q0 + q < splits) {
         v0 += x[q][0];
         v1 += x[q][1];
       }
   }
-  *reinterpret_cast<u32x4 *>(a.dX + i) = u32x4{pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
-                                               pack_bf16x2(v1[0], v1[1]), pack_bf16x2(v1[2], v1[3])};
+  *reinterpret_cast<u32x4 *>(out + i) = u32x4{pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
+                                             pack_bf16x2(v1[0], v1[1]), pack_bf16x2(v1[2], v1[3])};
 }
 
 // Rows of the tiles and cuts of the contraction, by the time of a launch: rounds
@@ -404,11 +406,16 @@ hipError_t launch_mx_dx(const MxDxArgs &in, const ColSumArgs *sums, hipStream_t 
                                        : launch_tiles<1, 2, 2, 4>(a, st);
   if (e != hipSuccess) return e;
   if (p.splits == 1) return sums ? launch_colsum_reduce(sums[0], sums[1], st) : hipSuccess;
-  const int blocks = (int)cdiv(a.M * (a.K / 8), 256);
+  return launch_split_sum(a.part, p.splits, a.M * a.K, a.dX, sums, st);
+}
+
+hipError_t launch_split_sum(const float *part, int splits, int64_t n, uint16_t *out, const ColSumArgs *sums,
+                            hipStream_t st) {
+  const int blocks = (int)cdiv(n / 8, 256);
   const ColSumArgs none{};
   const int64_t more = sums ? colsum_reduce_blocks(sums[0]) + colsum_reduce_blocks(sums[1]) : 0;
-  hipLaunchKernelGGL(mx_dx_finish_kernel, dim3((unsigned)(blocks + more)), dim3(256), 0, st, a, sums ? sums[0] : none,
-                     sums ? sums[1] : none, blocks);
+  hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)(blocks + more)), dim3(256), 0, st, part, splits, n, out,
+                     sums ? sums[0] : none, sums ? sums[1] : none, blocks);
   return hipGetLastError();
 }
 

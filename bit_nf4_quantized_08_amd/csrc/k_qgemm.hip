@@ -462,7 +462,7 @@ __device__ __forceinline__ void lds_barrier() {
 // Exactly one workgroup (2 waves per SIMD) fits a CU, so tell the compiler
 // that higher occupancy is not reachable: it may then keep a whole step's
 // operands in registers instead of re-reading them one by one.
-template <bool KN, bool DQ, bool EPI_NK, bool Q4, bool DROP = false>
+template <bool KN, bool DQ, bool EPI_NK, bool Q4, bool DROP = false, bool PART = false>
 __global__ __launch_bounds__(kThreads, 1) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void qgemm_kernel(QGemmGroup grp, Code16 cb) {
   // The problem this workgroup belongs to (a grouped launch runs several
@@ -494,7 +494,13 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool producer = wave >= 4;
-  const int64_t steps = __builtin_amdgcn_readfirstlane((int)(a.Kc / BK));
+  // PART: this workgroup's range of the weight steps, from step sb; the adapter
+  // term belongs to the first range (the others see r = 0 and a zero left
+  // operand).
+  const int split = PART ? (int)blockIdx.y : 0;
+  const int sb = PART ? (int)(a.Kc / BK * split / a.splits) : 0;
+  const int64_t steps =
+      __builtin_amdgcn_readfirstlane(PART ? (int)(a.Kc / BK * (split + 1) / a.splits) - sb : (int)(a.Kc / BK));
   // Contraction steps of 64: Kc / 64 weight steps, then one adapter step
   // (left operand L2, zero beyond ldl2; right operand R2 restricted to j < r).
   const int64_t total = steps + 1;
@@ -508,7 +514,7 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
     Scale4 q4;
     if constexpr (Q4) q4.init(a, tid, n0);
     const int nsteps = __builtin_amdgcn_readfirstlane((int)steps), last = nsteps - 1;   // nsteps >= 1
-    const int ntotal = nsteps + 1;   // contraction steps including the adapter step
+    const int ntotal = nsteps + (PART && split ? 0 : 1);   // contraction steps including the adapter step
 
     // Activation stages.  Producer wave p moves the 64 rows of MMA wave p from
     // global memory into LDS with direct-to-LDS loads (the compiler sees them,
@@ -522,7 +528,7 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
     // at or beyond ldl2) the same way.
     const int pw = wave - 4;
     const int64_t wrow0 = m0 + (int64_t)pw * WM;
-    const rsrc_t xr = make_rsrc(a.L + wrow0 * a.ldl, (a.M - wrow0) * a.ldl * 2);
+    const rsrc_t xr = make_rsrc(a.L + wrow0 * a.ldl + sb * BK, (a.M - wrow0) * a.ldl * 2 - sb * BK * 2);
     const rsrc_t l2r = make_rsrc(a.L2 + wrow0 * a.ldl2, (a.M - wrow0) * a.ldl2 * 2);
     const uint32_t c0 = (uint32_t)((lane & 7) ^ (lane >> 4));   // chunk for even g; odd g: c0 ^ 4
     const uint32_t xbase0 = (uint32_t)((lane >> 3) * a.ldl * 2 + c0 * 16);
@@ -570,10 +576,16 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
     // order of its back edge and the compiler's own waits for the code sets
     // stay exact.
     uint32_t adapter[32];
-    load_adapter_right<EPI_NK>(a, n0, tid, adapter);
+    if constexpr (PART) {
+      QGemmArgs b = a;
+      if (split) b.r = 0;
+      load_adapter_right<EPI_NK>(b, n0, tid, adapter);
+    } else {
+      load_adapter_right<EPI_NK>(a, n0, tid, adapter);
+    }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (Q4) q4.issue(0);   // Scale4 dword 0, in nxt
-    P.issue(s0, 0);
+    P.issue(s0, sb);
     __builtin_amdgcn_sched_barrier(0);
     {
       // Stage 0 is always a weight step (nsteps >= 1): the same eight loads as
@@ -587,7 +599,7 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
                                                  ((g & 1) ? xbase1 : xbase0) + (uint32_t)g * xrow8, 0, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-    P.issue(s1, __builtin_amdgcn_readfirstlane(min(1, last)));
+    P.issue(s1, __builtin_amdgcn_readfirstlane(sb + min(1, last)));
     __builtin_amdgcn_sched_barrier(0);
     // The eight activation loads are spread over the dequantisation: issued
     // back to back, the four producer waves' loads fill the CU's vector memory
@@ -622,7 +634,7 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
       else
         P.store(set, wdst, pair, cb.v, lane, [&](int q) { issue_x(t + 1, q); });
       __builtin_amdgcn_sched_barrier(0);
-      P.issue(set, min(t + 2, last));
+      P.issue(set, sb + min(t + 2, last));
       __builtin_amdgcn_sched_barrier(0);
       if (tail) __builtin_amdgcn_s_waitcnt(vmcnt_only(kReload + 8 + kScale));
       else __builtin_amdgcn_s_waitcnt(vmcnt_only(kReload + 8 + kScale + kReload));
@@ -787,6 +799,22 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
       }
     }
     lds_barrier();   // pairs with the producers' last barrier
+  }
+
+  if constexpr (PART) {
+    float *part = a.part + (int64_t)split * a.M * a.Nout;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int64_t gn = n0 + (KN ? kn_col(32 * j + lr) : 32 * j + lr);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t m = m0 + wave_u * WM + 32 * i + 8 * (e >> 2) + 4 * lh + (e & 3);
+          if (m < a.M && gn < a.Nout) part[m * a.Nout + gn] = acc[i][j][e];
+        }
+      }
+    return;
   }
 
   // ---- store bf16 through LDS.  Element e of a 32 x 32 accumulator tile is
@@ -1734,7 +1762,58 @@ hipError_t launch(const QGemmArgs *in, int n, hipStream_t st, int trace_kind) {
   return launch_tiling<KN, EPI_NK>(na, nnw, false, wide_kind, st);
 }
 
+template <bool KN>
+hipError_t launch_split(const QGemmArgs &in, hipStream_t st) {
+  QGemmGroup grp{};
+  grp.p[0] = in;
+  if (in.splits < 2 || in.Kc / BK < in.splits || !plan(grp.p[0])) return hipErrorInvalidValue;
+  const int64_t total = ((int64_t)grp.p[0].tiles_m * grp.p[0].tiles_n + 7) / 8 * 8;
+  if (total > INT32_MAX) return hipErrorInvalidValue;
+  for (int k = 1; k <= QN_MAX_GROUP; ++k) grp.start[k] = (int)total;
+  grp.n = 1;
+  const dim3 grid((unsigned)total, (unsigned)in.splits);
+  TraceScope tr(KN ? QN_TRACE_GEMM_DX : QN_TRACE_GEMM_FWD, st);
+  if (in.absmax_q) hipLaunchKernelGGL((qgemm_kernel<KN, true, !KN, false, KN, true>), grid, dim3(kThreads), 0, st, grp, code16(in.qtype));
+  else hipLaunchKernelGGL((qgemm_kernel<KN, false, !KN, false, KN, true>), grid, dim3(kThreads), 0, st, grp, code16(in.qtype));
+  return hipGetLastError();
+}
+
+// Ranges of the contraction for a product whose tiles leave CUs idle, by the time
+// of a launch: rounds of workgroups times the range's steps (0.75 us a step with
+// few workgroups, 1.15 with all CUs busy), plus the partial sums' launch and way to
+// memory and back.  Each range keeps at least four steps, below which the
+// prologue costs more than it hides.  NF4, p = 0.1, r = 16, a whole call, uncut
+// against cut: forward of 16 x 4096 x 4096 59 -> 29 us, 512 x 4096 x 4096 65 -> 46,
+// 1024 x 4096 x 4096 68 -> 64, 61 x 512 x 3584 51 -> 29; backward of the first three
+// 79 -> 44, 87 -> 63, 89 -> 83.
+int split_plan(int64_t M, int64_t Nout, int64_t Kc) {
+  const int64_t cus = device_cus(), tiles = cdiv(M, BM) * cdiv(Nout, BN), steps = Kc / BK;
+  if (tiles >= cus) return 1;
+  int best = 1;
+  double best_us = 1e300;
+  for (int s = 1; s <= 8 && (s == 1 || steps / s >= 4); ++s) {
+    const double us = (0.75 + 0.4 * std::min(1.0, (double)(tiles * s) / (double)cus)) * (double)cdiv(tiles * s, cus) *
+                          (double)cdiv(steps, s) +
+                      (s == 1 ? 0.0 : 4.0 + (double)(s * M * Nout) * 8.0 / 4.5e6);
+    if (us < best_us) { best_us = us; best = s; }
+  }
+  return best;
+}
+
 }  // namespace
+
+int qgemm_splits(int64_t M, int64_t Nout, int64_t Kc) {
+  return g_variant.load(std::memory_order_relaxed) ? 1 : split_plan(M, Nout, Kc);   // a forced tiling is not cut
+}
+
+size_t qgemm_part_bytes(int64_t M, int64_t Nout, int64_t Kc) {
+  const int s = split_plan(M, Nout, Kc);
+  return s > 1 ? (size_t)s * (size_t)M * (size_t)Nout * sizeof(float) : 0;
+}
+
+hipError_t launch_qgemm_split(const QGemmArgs &a, bool dx, hipStream_t st) {
+  return dx ? launch_split<true>(a, st) : launch_split<false>(a, st);
+}
 
 hipError_t launch_qgemm_fwd(const QGemmArgs &a, hipStream_t st) {
   return launch<false, true>(&a, 1, st, QN_TRACE_GEMM_FWD);

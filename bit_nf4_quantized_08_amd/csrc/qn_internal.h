@@ -142,7 +142,16 @@ struct QGemmArgs {
   int64_t ldo;
   int tiles_m, tiles_n, group_m;
   DropArgs drop;   // dX only: thr > 0 adds c keep(m, n) * (adapter term), keep over [M, Nout]
+  float *part;     // launch_qgemm_split: fp32 [splits][M, Nout] partial products, instead of out
+  int splits;
 };
+// The calls with dropout, whose sums no earlier result pins, cut the contraction
+// into ranges where the tiles alone leave most CUs idle.  qgemm_splits: how
+// many (1: none; part takes qgemm_part_bytes); launch_qgemm_split: the partial
+// products of a.splits > 1 ranges, for launch_split_sum.
+int qgemm_splits(int64_t M, int64_t Nout, int64_t Kc);
+size_t qgemm_part_bytes(int64_t M, int64_t Nout, int64_t Kc);
+hipError_t launch_qgemm_split(const QGemmArgs &a, bool dx, hipStream_t s);
 hipError_t launch_qgemm_fwd(const QGemmArgs &a, hipStream_t s);
 hipError_t launch_qgemm_dx(const QGemmArgs &a, hipStream_t s);
 // Several independent forward products in one launch (n <= QN_MAX_GROUP); the
@@ -233,6 +242,11 @@ hipError_t launch_colsum2(const ColSumArgs &a, const ColSumArgs &b, hipStream_t 
 // Their reduction over the splits, a launch of its own (the MXFP4 dX's finishing
 // pass, when there is one, takes it along: launch_mx_dx).
 hipError_t launch_colsum_reduce(const ColSumArgs &a, const ColSumArgs &b, hipStream_t s);
+
+// out (bf16, n elements, n % 8 == 0) = the sum of the fp32 partial products [splits][n]; with sums non-null also
+// the reduction of those two column sums.
+hipError_t launch_split_sum(const float *part, int splits, int64_t n, uint16_t *out, const ColSumArgs *sums,
+                            hipStream_t s);
 
 // Forward pieces.
 struct FwdArgs {

@@ -376,10 +376,10 @@ int qn_dropout(const void *x, int dtype, int64_t n, const qn_dropout_config *dro
  *     dH = s G B,  dB = s G^T H,  dA = c dH^T (keep * X),
  *     dX = G bf16(dequant(W)) + c keep * (dH A)
  * keep over [M, K] (element m K + k).  Arguments and shape rules as there; drop
- * is required (its p may be 0).  The forward's workspace is
- * qlora_workspace_size(QN_OP_FWD_DROPOUT, ...) bytes (every M takes the MFMA
- * path), the backward's that of QN_OP_BWD, which takes M <= 2^24.  A given H is the dropped one, as
- * this forward wrote it. */
+ * is required; with p = 0 the results are the plain linear's on its MFMA path.
+ * The forward's workspace is qlora_workspace_size(QN_OP_FWD_DROPOUT, ...) bytes
+ * (every M takes the MFMA path), the backward's that of QN_OP_BWD; the backward
+ * takes M <= 2^24.  A given H is the dropped one, as this forward wrote it. */
 #define QN_OP_FWD_DROPOUT 2
 int qlora_linear_fwd_dropout(const void *X, int64_t M, const qn_nf4_weight *W, const void *A, const void *B,
                              int64_t r, float alpha, const qn_dropout_config *drop, void *Y, float *H_out,
@@ -440,9 +440,11 @@ size_t qlora_mx_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t 
  * dropout (keep = 1, c = 1).  r = 0 with A, B and H_out NULL: the base alone
  * (alpha and drop are not used).  Otherwise arguments as qlora_linear_fwd.
  * Shape rules: M >= 1, N % 64 == 0, K % 64 == 0, N * 128 C <= INT32_MAX,
- * N and K <= 2^22, M <= 2^24, M * C <= 2^28, 0 <= r <= QN_MAX_RANK.  A non-finite block of X makes its row of Y
- * NaN.  M <= 32 streams the weights once (both operands on the matrix cores),
- * larger M runs tiles. */
+ * N and K <= 2^22, M <= 2^24, M * C <= 2^28, 0 <= r <= QN_MAX_RANK.  A
+ * non-finite block of X makes its row of Y NaN.  M <= 32 streams the weights once
+ * (both operands on the matrix cores), larger M runs tiles.  The workspace is
+ * written by the call: calls that may run at the same time, captured graphs
+ * among them, need one each. */
 int qlora_mx_linear_fwd(const void *X, int64_t M, const qn_mx_matrix *W, const void *A, const void *B, int64_t r,
                         float alpha, const qn_dropout_config *drop, void *Y, float *H_out, void *workspace,
                         size_t ws_bytes, void *stream);

@@ -136,26 +136,38 @@ def check_step(Y, H, grads, G, X, base_in, What, A, B, alpha, keep, c, given_H, 
     assert np.all(e <= tol), f"dB off by {(e / tol).max():.2f} of its tolerance"
 
 
-def run_nf4(M, N, K, r, p, variant=0, dq=True, give_H=True, want_dX=True, seed=0):
+def _poisoned(nbytes):
+    """A workspace of NaN bytes (0xFF) in guard bands: a value read before it is written shows."""
+    full, view = guarded(nbytes, torch.uint8)
+    view.fill_(0xFF)
+    return full, view
+
+
+def run_nf4(M, N, K, r, p, variant=0, dq=True, give_H=True, want_dX=True, seed=0, quant_type="nf4"):
     alpha = 2.0 * r
     W, X, A, B, G = _inputs(M, N, K, r, seed)
-    w = lib.quantize_weight(to_dev(W))
+    w = lib.quantize_weight(to_dev(W), quant_type=quant_type)
     d = lib.Dropout(p, SEED + seed, OFF)
+    sizes = [lib.workspace_size(op, M, N, K, r) for op in (lib.QN_OP_FWD_DROPOUT, lib.QN_OP_BWD)]
+    spaces = [_poisoned(n) for n in sizes]
     Xd, Ad, Bd, Gd = (t.to(dev()) for t in (X, A, B, G))
     nb = M * N * 2
     full, view = guarded(nb, torch.bfloat16)
     lib.set_gemm_variant(variant)
     try:
         Y, H = lib.qlora_linear_fwd_dropout(Xd, w, Ad, Bd, alpha, d, want_H=True, use_double_quant=dq,
-                                            Y=view.view(M, N))
+                                            Y=view.view(M, N), ws=spaces[0][1])
         grads = lib.qlora_linear_bwd_dropout(Gd, Xd, w, Ad, Bd, alpha, d, want_dX=want_dX, use_double_quant=dq,
-                                             H=H if give_H else None)
+                                             H=H if give_H else None, ws=spaces[1][1])
         torch.cuda.synchronize()
     finally:
         lib.set_gemm_variant(0)
     assert guards_intact(full, nb)
-    p_, a_, _ = oracle.quantize(W)
-    What = oracle.dequant_bf16_weight(p_, N, K, oracle.dq_absmax(*oracle.double_quant(a_)) if dq else a_)
+    for n, (buf, _) in zip(sizes, spaces):
+        assert guards_intact(buf, n), "workspace"
+    p_, a_, _ = oracle.quantize(W, quant_type=quant_type)
+    What = oracle.dequant_bf16_weight(p_, N, K, oracle.dq_absmax(*oracle.double_quant(a_)) if dq else a_,
+                                      quant_type=quant_type)
     keep = D.keep(M * K, p, SEED + seed, OFF).reshape(M, K)
     Xv, Av, Bv, Gv = (synth.bf16_values(t).astype(np.float64) for t in (X, A, B, G))
     check_step(Y, H, grads, Gv, Xv, Xv, What.astype(np.float64), Av, Bv, alpha, keep, D.scale(p),
@@ -213,3 +225,53 @@ def test_masked_infinities_reach_nothing():
         res.append((H, dA, dB))
     for a, b in zip(*res):
         assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M, N, K, r, p", [
+    (61, 1088, 1344, 24, 0.25), (1, 1024, 1024, 1, 0.1), (5, 704, 2112, 8, 0.5), (260, 1216, 1152, 40, 0.1),
+    (300, 4160, 576, 64, 0.05),
+])
+@pytest.mark.parametrize("dq", [True, False])
+def test_nf4_dropout_with_cut_contractions(M, N, K, r, p, dq):
+    """Few tiles: the contraction of Y, of dX or of both runs in several ranges, of unequal length among them."""
+    say(f"nf4 dropout, cut contractions M={M} N={N} K={K} r={r} p={p} dq={dq}")
+    run_nf4(M, N, K, r, p, dq=dq, seed=M + r)
+
+
+@pytest.mark.parametrize("M, N, K, r, variant", [(70, 1088, 1088, 16, 0), (70, 1088, 1088, 16, 1), (300, 320, 256, 33, 2)])
+def test_fp4_linear_with_dropout(M, N, K, r, variant):
+    say(f"fp4 dropout step M={M} N={N} K={K} r={r} variant={variant}")
+    run_nf4(M, N, K, r, 0.2, variant=variant, quant_type="fp4", give_H=False)
+
+
+def test_non_finite_adapter_stays_in_its_columns():
+    """Infinities in one row of B and one column of A: the same outputs are non-finite, and the same others
+    finite, with the contractions cut and whole."""
+    M, N, K, r, p = 40, 1088, 1088, 8, 0.25
+    say("nf4 dropout, infinite adapter entries")
+    W, X, A, B, G = _inputs(M, N, K, r, 5)
+    A[:, 17] = float("inf")
+    B[33, :] = float("inf")
+    w = lib.quantize_weight(to_dev(W))
+    d = lib.Dropout(p, SEED, OFF)
+    X, A, B, G = (t.to(dev()) for t in (X, A, B, G))
+    H = torch.from_numpy(synth.gaussian((M, r), 1.0, 3)).to(dev())
+    res = []
+    for variant in (0, 1):
+        lib.set_gemm_variant(variant)
+        try:
+            Af = torch.where(torch.isinf(A), torch.zeros_like(A), A)
+            Y = lib.qlora_linear_fwd_dropout(X, w, Af, B, 16.0, d)   # an infinite A would reach every column of Y
+            Bf = torch.where(torch.isinf(B), torch.zeros_like(B), B)
+            dX, _, _ = lib.qlora_linear_bwd_dropout(G, X, w, A, Bf, 16.0, d, H=H)
+            torch.cuda.synchronize()
+            res.append((host(Y), host(dX)))
+        finally:
+            lib.set_gemm_variant(0)
+    (Y0, dX0), (Y1, dX1) = res
+    assert not np.isfinite(Y0[:, 33]).any() and np.isfinite(np.delete(Y0, 33, axis=1)).all()
+    np.testing.assert_array_equal(Y0[:, 33], Y1[:, 33])
+    keep = D.keep(M * K, p, SEED, OFF).reshape(M, K)[:, 17]
+    assert np.isfinite(np.delete(dX0, 17, axis=1)).all()
+    np.testing.assert_array_equal(np.isfinite(dX0[:, 17]), ~keep)
+    np.testing.assert_array_equal(np.isfinite(dX1[:, 17]), ~keep)

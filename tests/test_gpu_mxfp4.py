@@ -104,6 +104,7 @@ def _ws(op, M, N, K, r):
     n = lib.mx_workspace_size(op, M, N, K, r)
     assert n % 256 == 0
     full, view = guarded(n, torch.uint8)
+    view.fill_(0xFF)   # NaN bytes: a value read before it is written shows
     return n, full, view
 
 
