@@ -7,7 +7,9 @@
 // store for bf16, two for fp32.  Memory bound with a second limit close by:
 // one generator call is 14 quarter-rate multiplies and about 50 other vector
 // instructions.  Each thread takes kUnroll groups a workgroup's width apart,
-// loads first, so that the generator runs while they are in flight.
+// loads first, so that the generator runs while they are in flight.  4096 x 8192
+// bf16 (134 MB): 20.7 us, 6.5 TB/s (part of it in the 256 MB cache), what a plain
+// copy of as many bytes takes within a tenth.
 
 #include <algorithm>
 

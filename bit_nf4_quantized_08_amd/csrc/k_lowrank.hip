@@ -28,13 +28,16 @@
 // Dropout of L (the adapter's input): a 16-byte piece of L is one call of the
 // generator of qn_philox.h, so each lane masks the pieces it loaded, in
 // registers, before they go to LDS; the kept values stay unscaled bf16 and the
-// factor 1/(1-p) is applied to the fp32 sums, so dropout adds no rounding.
+// factor 1/(1-p) is applied to the fp32 sums, so dropout adds no rounding (nor
+// time where the loads bound it: 9 us at 2048 x 4096, r = 16, with and without).
 //
 // Quantisation of L to MXFP4 in the same pass (the MXFP4 linear's activations):
 // the piece is also a quarter of a 32-element block, its quad holds the block, and the
 // LR_DEPTH steps of a loop turn are one 256-column chunk, whose eight scale
 // bytes of a row are collected and stored together.  The ranges then start at
-// whole chunks.  Against a quantisation pass of its own, X is read once.
+// whole chunks.  Against a quantisation pass of its own, X is read once: 4096 x
+// 8192, r = 64, 21 to 25 us against 15 + 19.  Bound by memory (85 MB, 4 TB/s at
+// best) and, for few rows, by the latency of a workgroup's only loop turn.
 
 #include <algorithm>
 
@@ -78,7 +81,8 @@ struct LowRankGroup {
 // launch drops elements of its L.  QUANT: L is quantised too (one product).
 // PT: some product's factor is given transposed (P is [Kc, R], as B is for dH =
 // dY B): its 64 x R slab is loaded along its rows and written to the staged
-// layout two bytes at a time, which saves a launch that would transpose it.
+// layout two bytes at a time, which saves a launch that would transpose it (4 us;
+// the kernel takes what it takes with P given row by row, 9 us at 2048 x 4096, r = 16).
 template <int RT, bool DROP, bool QUANT, bool PT>
 __global__ __launch_bounds__(LR_THREADS) void lowrank_part_kernel(LowRankGroup grp) {
   __shared__ __attribute__((aligned(16))) uint8_t ps[2][32 * RT * LR_PITCH];
