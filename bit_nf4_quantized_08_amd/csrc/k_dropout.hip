@@ -3,15 +3,14 @@
 // The mask comes from the generator of qn_philox.h and is not stored; the
 // same call on a gradient is the backward.
 //
-// Eight elements (one generator call) per thread and step: a 16-byte load and
-// store for bf16, two for fp32.  Memory bound with a second limit close by:
-// one generator call is 14 quarter-rate multiplies and about 50 other vector
-// instructions.  Each thread takes kUnroll groups a workgroup's width apart,
-// loads first, so that the generator runs while they are in flight.  4096 x 8192
-// bf16 (134 MB): 20.7 us, 6.5 TB/s (part of it in the 256 MB cache), what a plain
-// copy of as many bytes takes within a tenth.
-
-#include <algorithm>
+// Eight elements (one generator call) per thread: a 16-byte load and store for
+// bf16, two for fp32.  Memory bound with a second limit close by: one generator
+// call is 14 quarter-rate multiplies and about 50 other vector instructions.  4096 x
+// 8192 bf16 (134 MB, part of it in the 256 MB cache): 19.7 us, 6.8 TB/s; a plain copy
+// takes 17 to 19.  Two or four groups per thread, loads first, take 20.7 and 21.2;
+// fp32 in one 16-byte piece per lane, each call made by two neighbours, 48 against
+// 42 at 33.5 M elements; stores marked as not read again gain here (134 M
+// elements: 89 -> 74) what the reader of y then loses.
 
 #include "qn_philox.h"
 
@@ -19,7 +18,7 @@ namespace qn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;
+constexpr int64_t kMaxGridX = 1 << 22;
 
 template <bool BF16, bool DROP>
 __device__ __forceinline__ void drop8(const DropArgs &d, const DropKey &k, uint64_t g, const u32x4 (&x)[BF16 ? 1 : 2],
@@ -55,45 +54,34 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const uint8_t *x, uin
   constexpr int V = BF16 ? 1 : 2;
   constexpr int ES = BF16 ? 2 : 4;
   const DropKey k = drop_key(d);
-  const int64_t full = n >> 3;
-  const int64_t g0 = (int64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  u32x4 xv[kUnroll][V], yv[V];
+  const int64_t full = n >> 3, g = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  u32x4 xv[V], yv[V];
+  if (g < full) {
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t g = g0 + u * kThreads;
-    if (g < full)
+    for (int v = 0; v < V; ++v) xv[v] = *reinterpret_cast<const u32x4 *>(x + g * 8 * ES + 16 * v);
+    drop8<BF16, DROP>(d, k, (uint64_t)g, xv, yv);
 #pragma unroll
-      for (int v = 0; v < V; ++v) xv[u][v] = *reinterpret_cast<const u32x4 *>(x + g * 8 * ES + 16 * v);
-  }
+    for (int v = 0; v < V; ++v) *reinterpret_cast<u32x4 *>(y + g * 8 * ES + 16 * v) = yv[v];
+  } else if (g == full && (n & 7)) {   // the last, partial group
+    const int left = (int)(n & 7);
+    uint32_t e[4 * V] = {};
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t g = g0 + u * kThreads;
-    if (g < full) {
-      drop8<BF16, DROP>(d, k, (uint64_t)g, xv[u], yv);
+    for (int t = 0; t < 8; ++t) {
+      if (t >= left) break;
+      if constexpr (BF16) e[t >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(x)[g * 8 + t] << (16 * (t & 1));
+      else e[t] = reinterpret_cast<const uint32_t *>(x)[g * 8 + t];
+    }
 #pragma unroll
-      for (int v = 0; v < V; ++v) *reinterpret_cast<u32x4 *>(y + g * 8 * ES + 16 * v) = yv[v];
-    } else if (g == full && (n & 7)) {   // the last, partial group
-      uint32_t e[4 * V] = {};
-      const int64_t left = n & 7;
+    for (int v = 0; v < V; ++v) xv[v] = u32x4{e[4 * v], e[4 * v + 1], e[4 * v + 2], e[4 * v + 3]};
+    drop8<BF16, DROP>(d, k, (uint64_t)g, xv, yv);
+    uint32_t o[4 * V];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t >= left) break;
-        if constexpr (BF16) e[t >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(x)[g * 8 + t] << (16 * (t & 1));
-        else e[t] = reinterpret_cast<const uint32_t *>(x)[g * 8 + t];
-      }
-      u32x4 ev[V];
+    for (int v = 0; v < V; ++v) { o[4 * v] = yv[v].x; o[4 * v + 1] = yv[v].y; o[4 * v + 2] = yv[v].z; o[4 * v + 3] = yv[v].w; }
 #pragma unroll
-      for (int v = 0; v < V; ++v) ev[v] = u32x4{e[4 * v], e[4 * v + 1], e[4 * v + 2], e[4 * v + 3]};
-      drop8<BF16, DROP>(d, k, (uint64_t)g, ev, yv);
-      uint32_t o[4 * V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) { o[4 * v] = yv[v].x; o[4 * v + 1] = yv[v].y; o[4 * v + 2] = yv[v].z; o[4 * v + 3] = yv[v].w; }
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t >= left) break;
-        if constexpr (BF16) reinterpret_cast<uint16_t *>(y)[g * 8 + t] = (uint16_t)(o[t >> 1] >> (16 * (t & 1)));
-        else reinterpret_cast<uint32_t *>(y)[g * 8 + t] = o[t];
-      }
+    for (int t = 0; t < 8; ++t) {
+      if (t >= left) break;
+      if constexpr (BF16) reinterpret_cast<uint16_t *>(y)[g * 8 + t] = (uint16_t)(o[t >> 1] >> (16 * (t & 1)));
+      else reinterpret_cast<uint32_t *>(y)[g * 8 + t] = o[t];
     }
   }
 }
@@ -101,8 +89,9 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const uint8_t *x, uin
 }  // namespace
 
 hipError_t launch_dropout(const void *x, int is_bf16, int64_t n, const DropArgs &d, void *y, hipStream_t st) {
-  const int64_t groups = (n + 7) / 8, per = kThreads * kUnroll;
-  const dim3 grid((unsigned)((groups + per - 1) / per));
+  // A grid dimension holds less than 2^32 threads (n <= 2^40 needs up to 2^37).
+  const int64_t blocks = ((n + 7) / 8 + kThreads - 1) / kThreads, wide = blocks < kMaxGridX ? blocks : kMaxGridX;
+  const dim3 grid((unsigned)wide, (unsigned)((blocks + wide - 1) / wide));
   const auto *xs = static_cast<const uint8_t *>(x);
   auto *ys = static_cast<uint8_t *>(y);
   TraceScope tr(QN_TRACE_DROPOUT, st);

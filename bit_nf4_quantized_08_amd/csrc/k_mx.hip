@@ -64,6 +64,10 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, FastDiv f) { return (__um
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;
 
+// A grid dimension holds less than 2^32 threads; 2^31 chunks need 2^34.
+constexpr int64_t kMaxGridX = 1 << 22;
+__device__ __forceinline__ uint32_t codec_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // VEC: cols is a multiple of 8, so that a unit is aligned and whole.  T threads
 // take chunks `first` .. of the matrix, U units each.
 template <bool BF16, bool VEC, int T, int U>
@@ -118,7 +122,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint8_t *__
                                                                int64_t cols, FastDiv cd, uint32_t chunks,
                                                                uint8_t *__restrict__ codes,
                                                                uint8_t *__restrict__ scales) {
-  quantize_units<BF16, VEC, kThreads, kUnits>(x, rows, cols, cd, chunks, blockIdx.x * (kThreads / 32 * kUnits), codes,
+  quantize_units<BF16, VEC, kThreads, kUnits>(x, rows, cols, cd, chunks, codec_block() * (kThreads / 32 * kUnits), codes,
                                               scales);
 }
 
@@ -130,7 +134,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequant_kernel(const uint8_t *__r
   constexpr int ES = BF16 ? 2 : 4;
   const int tid = threadIdx.x;
   uint32_t cw[kUnits], sb[kUnits], ch[kUnits], row[kUnits];
-  const uint32_t c0 = blockIdx.x * (kThreads / 32 * kUnits) + (tid >> 5);
+  const uint32_t c0 = codec_block() * (kThreads / 32 * kUnits) + (tid >> 5);
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const uint32_t c = c0 + i * (kThreads / 32);
@@ -1032,7 +1036,8 @@ hipError_t launch_codec(const void *x, int bf16, int64_t rows, int64_t cols, con
                         uint8_t *co, uint8_t *so, void *out, hipStream_t st) {
   const int64_t C = mx_chunks(cols), chunks = rows * C;
   const FastDiv cd = fast_div((uint32_t)C);
-  const dim3 grid((unsigned)cdiv(chunks, kThreads / 32 * kUnits)), block(kThreads);
+  const int64_t blocks = cdiv(chunks, kThreads / 32 * kUnits), wide = std::min(blocks, kMaxGridX);
+  const dim3 grid((unsigned)wide, (unsigned)cdiv(blocks, wide)), block(kThreads);
   const bool vec = cols % 8 == 0;
   const auto *xb = static_cast<const uint8_t *>(x);
   auto *ob = static_cast<uint8_t *>(out);

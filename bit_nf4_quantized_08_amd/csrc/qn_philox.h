@@ -51,11 +51,16 @@ __device__ __forceinline__ void philox7(uint64_t g, const DropKey &k, uint32_t (
   w[0] = c0; w[1] = c1; w[2] = c2; w[3] = c3;
 }
 
-// Two fields -> 0xFFFF in the half of each kept element, 0 in the other's.
+// Two fields -> 0xFFFF in the half of each kept element, 0 in the other's: field -
+// (thr - 1) saturating at 0, at most 1, negated.  In asm because the compiler
+// turns the same three packed operations into compares, selects and a permute
+// per pair.
 __device__ __forceinline__ uint32_t keep_mask2(uint32_t w, uint32_t thr2) {
-  const u16x2 d = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w), __builtin_bit_cast(u16x2, thr2));
-  const u16x2 one = {1, 1}, zero = {0, 0};
-  return __builtin_bit_cast(uint32_t, (u16x2)(zero - __builtin_elementwise_min(d, one)));
+  uint32_t d;
+  asm("v_pk_sub_u16 %0, %1, %2 clamp" : "=v"(d) : "v"(w), "s"(thr2));
+  asm("v_pk_min_u16 %0, %0, %1" : "+v"(d) : "s"(0x00010001u));
+  asm("v_pk_sub_i16 %0, 0, %0" : "+v"(d));
+  return d;
 }
 
 // Bit t set when element t of the call's eight is kept.

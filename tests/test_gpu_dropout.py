@@ -275,3 +275,24 @@ def test_non_finite_adapter_stays_in_its_columns():
     assert np.isfinite(np.delete(dX0, 17, axis=1)).all()
     np.testing.assert_array_equal(np.isfinite(dX0[:, 17]), ~keep)
     np.testing.assert_array_equal(np.isfinite(dX1[:, 17]), ~keep)
+
+
+def test_elementwise_beyond_32_bits():
+    """2^32 generator calls and more (in place, 69 GB): offsets, the grid and the counter's high word."""
+    n, p = (1 << 35) + 8 * 700 + 3, 0.3
+    say(f"dropout n={n}")
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of device memory")
+    x = torch.full((n,), 1.5, dtype=torch.bfloat16, device=dev())
+    lib.dropout(x, lib.Dropout(p, SEED, OFF), out=x)
+    one = float(torch.tensor(1.5 * np.float32(D.scale(p)), dtype=torch.float32).to(torch.bfloat16))
+    for first in (0, (1 << 34) - 4096, (1 << 35) - 4096, n - 5600 - 3):
+        w = x[first:first + 8192]
+        m = w.numel()
+        g = np.arange(first // 8, (first + m + 7) // 8, dtype=np.uint64)
+        off = [np.full_like(g, OFF & 0xFFFFFFFF), np.full_like(g, OFF >> 32)]
+        v = D.philox4x32([g & np.uint64(0xFFFFFFFF), g >> np.uint64(32)] + off, (SEED & 0xFFFFFFFF, SEED >> 32), 7)
+        f = np.stack([h for q in v for h in (q & np.uint64(0xFFFF), q >> np.uint64(16))], axis=1).reshape(-1)[:m]
+        np.testing.assert_array_equal(host(w), np.where(f >= D.threshold(p), np.float32(one), np.float32(0.0)))
+    del x
+    torch.cuda.empty_cache()

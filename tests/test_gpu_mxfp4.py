@@ -74,6 +74,25 @@ def test_codec_edge_blocks(dtype, cols):
     _check_codec(x.to(dtype))
 
 
+def test_codec_of_very_many_rows():
+    """2^29 rows of one column and some (75 GB): the grid and the offsets beyond 32 bits."""
+    rows = (1 << 29) + 7
+    say(f"codec rows={rows} cols=1")
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of device memory")
+    x = torch.randn((rows, 1), device=dev(), dtype=torch.bfloat16)
+    q = lib.mxfp4_quantize(x)
+    y = lib.mxfp4_dequant(q)
+    for first in (0, (1 << 24) - 50, (1 << 25) - 50, (1 << 29) - 100, rows - 100):
+        sl = slice(first, first + 100)
+        want_c, want_s = MX.quantize(host(x[sl]))
+        np.testing.assert_array_equal(q.codes[sl].cpu().numpy(), want_c)
+        np.testing.assert_array_equal(q.scales[:, sl].cpu().numpy(), want_s)
+        np.testing.assert_array_equal(host(y[sl]), MX.values(host(x[sl])).astype(np.float32))
+    del x, q, y
+    torch.cuda.empty_cache()
+
+
 def test_dequant_of_every_code_and_scale():
     """All 16 codes under all 256 scale bytes, to fp32 and bf16 (rounded as the value is: only bytes 253, 254 overflow)."""
     say("mxfp4 dequant of every byte")
