@@ -11,8 +11,8 @@ import torch
 from bit_nf4_quantized_08_amd import lib, synth
 from oracle import dropout as D
 from oracle import mxfp4 as MX
-from tests.gpu_util import dev, guarded, guards_intact, host, say, to_dev
-from tests.test_gpu_dropout import OFF, SEED, check_step
+from tests.gpu_util import REL_FRO_TOL, dev, guarded, guards_intact, host, rel_fro, say, to_dev
+from tests.test_gpu_dropout import EPS, HALF, OFF, SEED, check_step
 
 pytestmark = pytest.mark.gpu
 
@@ -383,3 +383,35 @@ def test_python_refusals_on_the_device():
     with pytest.raises(ValueError):
         lib.qlora_mx_linear_bwd(torch.zeros((4, 64), dtype=torch.bfloat16, device=dev()), X, w, A, B, 1.0,
                                 out=(None, None, None))
+
+
+def test_rows_beyond_32_bits():
+    """X and dX of more than 2^32 bytes: sampled rows of Y, H and dX, all of dA and dB."""
+    M, N, K, r = (1 << 20) + 77, 64, 2048, 8
+    say(f"mx linear M={M} N={N} K={K}")
+    W, _, A, B, _ = _inputs(1, N, K, r, 2)
+    w = lib.mxfp4_quantize(to_dev(W))
+    gen = torch.Generator(device=dev()).manual_seed(7)
+    X = torch.randn((M, K), generator=gen, device=dev(), dtype=torch.bfloat16)
+    G = torch.randn((M, N), generator=gen, device=dev(), dtype=torch.bfloat16)
+    A, B, alpha = A.to(dev()), B.to(dev()), 16.0
+    Y, H = lib.qlora_mx_linear_fwd(X, w, A, B, alpha, want_H=True)
+    dX, dA, dB = lib.qlora_mx_linear_bwd(G, X, w, A, B, alpha, H=H)
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 1, 255, 256, (1 << 19) - 1, 1 << 19, (1 << 20) - 1, 1 << 20, M - 78, M - 2, M - 1], device=dev())
+    Xv, Gv, Av, Bv = (host(t).astype(np.float64) for t in (X[rows], G[rows], A, B))
+    Hv, What = host(H[rows]).astype(np.float64), MX.values(W)
+    check_step(Y[rows], H[rows], None, Gv, Xv, MX.values(Xv), What, Av, Bv, alpha, None, 1.0, Hv)
+    s, ab = alpha / r, np.abs
+    dH = s * (Gv @ Bv)
+    # dX: its own rounding, fp32 sums of N and r terms, dH rounded to bf16
+    tol = HALF * ab(Gv @ What + dH @ Av) + N * EPS * (ab(Gv) @ ab(What)) + (HALF + (N + r) * EPS) * ((s * (ab(Gv) @ ab(Bv))) @ ab(Av))
+    assert np.all(ab(host(dX[rows]).astype(np.float64) - (Gv @ What + dH @ Av)) <= tol)
+    # dA = dH^T X and dB = s G^T H in 64 bits, a slab of rows at a time
+    rA, rB = (torch.zeros(t, dtype=torch.float64, device=dev()) for t in ((r, K), (N, r)))
+    for m in range(0, M, 1 << 17):
+        x, g, h = (t[m:m + (1 << 17)].double() for t in (X, G, H))
+        rA += (s * (g @ B.double())).t() @ x
+        rB += s * (g.t() @ h)
+    assert rel_fro(host(dA), rA.cpu().numpy()) <= REL_FRO_TOL
+    assert rel_fro(host(dB), rB.cpu().numpy()) <= REL_FRO_TOL
