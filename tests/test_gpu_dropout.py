@@ -296,3 +296,50 @@ def test_elementwise_beyond_32_bits():
         np.testing.assert_array_equal(host(w), np.where(f >= D.threshold(p), np.float32(one), np.float32(0.0)))
     del x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M, N, K, r", [(61, 1088, 1344, 24), (300, 192, 128, 8)])
+def test_nf4_step_captured_replayed_and_on_two_streams(M, N, K, r):
+    """One mask per replay through offset_dev, against the same calls made eagerly on two other streams at once."""
+    say(f"nf4 dropout step under capture M={M} N={N} K={K} r={r}")
+    W, X, A, B, G = (t if isinstance(t, np.ndarray) else t.to(dev()) for t in _inputs(M, N, K, r, 4))
+    w = lib.quantize_weight(to_dev(W))
+    bf = dict(dtype=torch.bfloat16, device=dev())
+
+    def setup():
+        step = torch.zeros(1, dtype=torch.int64, device=dev())
+        return dict(step=step, d=lib.Dropout(0.2, SEED, OFF, offset_dev=step), Y=torch.zeros((M, N), **bf),
+                    H=torch.zeros((M, r), device=dev()), g=tuple(torch.zeros(t, **bf) for t in ((M, K), (r, K), (N, r))),
+                    wf=lib.workspace(lib.QN_OP_FWD_DROPOUT, M, N, K, r, dev()),
+                    wb=lib.workspace(lib.QN_OP_BWD, M, N, K, r, dev()))
+
+    def body(st):
+        lib.qlora_linear_fwd_dropout(X, w, A, B, 16.0, st["d"], Y=st["Y"], H=st["H"], ws=st["wf"])
+        lib.qlora_linear_bwd_dropout(G, X, w, A, B, 16.0, st["d"], out=st["g"], ws=st["wb"], H=st["H"])
+        st["step"].add_(1)
+
+    cap, one, two = setup(), setup(), setup()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def eager():
+        for st, s in ((one, s1), (two, s2)):
+            with torch.cuda.stream(s):
+                body(st)
+
+    body(cap)
+    eager()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        body(cap)
+    last = None
+    for rep in range(3):
+        graph.replay()
+        eager()
+        torch.cuda.synchronize()
+        for st in (one, two):
+            for a, b in zip((cap["Y"], cap["H"], cap["step"]) + cap["g"], (st["Y"], st["H"], st["step"]) + st["g"]):
+                assert torch.equal(a, b), rep
+        assert last is None or not torch.equal(cap["H"], last)
+        last = cap["H"].clone()
