@@ -57,6 +57,7 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
   __shared__ __attribute__((aligned(16))) uint8_t gs1[BM * 128];
   __shared__ __attribute__((aligned(16))) uint8_t ws0[kWStage];
   __shared__ __attribute__((aligned(16))) uint8_t ws1[kWStage];
+  __shared__ uint32_t keep[DROP ? BM * 8 : 1];   // the tile's mask (make_mask)
 
   int tm, tn;
   xcd_tile((int)blockIdx.x, tiles_m, tiles_n, group_m, tm, tn);
@@ -150,6 +151,30 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) f.b[j] = read_w(wst_, j, c);
   };
+  // The mask of the tile, BM x 256 bits, one generator call to a byte: row R's byte
+  // 8 w + n holds tile columns 8 n .. + 7 of the waves wc = w.  Call c of the
+  // workgroup, thread t's k-th (c = 512 k + t, k < kCalls), is byte c % 32 of row
+  // c / 32.  The calls run under the main loop, one a step while they last, in
+  // four parts between the third sub-step's MFMAs; run after it, before the
+  // masked add, they cost what the matrix cores then wait (4096 rows: N = 512, K =
+  // 8192 61 against 55 us, N = 3584, K = 18944 493 against 478; nothing at 8192 x 8192,
+  // where the clock takes the gain back).
+  constexpr int kCalls = BM / 16;
+  DropKey dk{};
+  if constexpr (DROP) dk = drop_key(a.drop);
+  const int byte = tid & 31, unit = byte & 7;
+  const uint64_t call0 = (uint64_t)(m0 + (tid >> 5)) * (uint64_t)(a.K / 8) +
+                         (uint64_t)(k0 / 8 + 4 * (UW * (byte >> 3) + unit % UW) + unit / UW);
+  Philox ph;
+  int calls = 0;
+  auto make_mask = [&](int q) {
+    if (q == 0) ph.start(call0 + (uint64_t)(16 * calls) * (uint64_t)(a.K / 8), dk);
+    ph.rounds<2>(dk, 2 * q);   // 2, 2, 2 and 1 of the seven
+    if (q == 3) {
+      reinterpret_cast<uint8_t *>(keep)[512 * calls + tid] = (uint8_t)keep_bits8(ph.c, dk.thr2);
+      ++calls;
+    }
+  };
   // A sub-step's MFMAs, with hook(0) .. hook(3) spread between them.
   auto mma = [&](const Frag &f, auto &&hook) {
     constexpr int n = TM * TN, per = n >= 4 ? n / 4 : 1;
@@ -159,14 +184,14 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
       if (m % per == per - 1) {
         __builtin_amdgcn_sched_barrier(0);
-        hook(m / per);
-        if (n < 4) hook(m + n);   // two MFMAs: two hooks after each
+        hook(n < 4 ? 2 * m : m / per);
+        if (n < 4) hook(2 * m + 1);   // two MFMAs: two hooks after each
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
   auto step = [&](int s, uint8_t *gc, const uint8_t *wc_, const uint8_t *gn, uint8_t *wn_, Frag &f0, Frag &f1,
-                  const Set &t, Set &t2) {
+                  const Set &t, Set &t2, auto &&third) {
     Set nt;
     read_f(f1, gc, wc_, 1);
     __builtin_amdgcn_sched_barrier(0);
@@ -183,7 +208,7 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
     });
     read_f(f1, gc, wc_, 3);
     __builtin_amdgcn_sched_barrier(0);
-    mma(f0, [](int) {});
+    mma(f0, third);
     t2 = nt;
     stage_barrier<2>();
     read_f(f0, gn, wn_, 0);
@@ -207,11 +232,25 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
   for (int i = 0; i < GL; ++i) issue_g(gs1, min(s0 + 1, last), i);
   __builtin_amdgcn_sched_barrier(0);
   read_f(f0, gs0, ws0, 0);
-  for (int s = s0; s < s1; s += 2) {
-    step(s, gs0, ws0, gs1, ws1, f0, f1, t1, t0);
+  int s = s0;
+  const bool masked = DROP && a.r && (!PART || split == 0);   // of split products, the first carries the adapter
+  if constexpr (DROP)
+    if (masked)
+      for (; s + 1 < s1 && calls < kCalls; s += 2) {
+        step(s, gs0, ws0, gs1, ws1, f0, f1, t1, t0, make_mask);
+        step(s + 1, gs1, ws1, gs0, ws0, f0, f1, t0, t1, make_mask);
+      }
+  auto none = [](int) {};
+  for (; s < s1; s += 2) {
+    step(s, gs0, ws0, gs1, ws1, f0, f1, t1, t0, none);
     if (s + 1 >= s1) break;
-    step(s + 1, gs1, ws1, gs0, ws0, f0, f1, t0, t1);
+    step(s + 1, gs1, ws1, gs0, ws0, f0, f1, t0, t1, none);
   }
+  if constexpr (DROP)
+    if (masked)
+      while (calls < kCalls)   // short contractions leave some
+#pragma unroll
+        for (int q = 0; q < 4; ++q) make_mask(q);
   // The loads past the end must land, and the last reads past it end, before the
   // stages are written again.
   stage_barrier();
@@ -249,18 +288,17 @@ void mx_dx_kernel(MxDxArgs a, int tiles_m, int tiles_n, int group_m) {
       }
     __syncthreads();
     if constexpr (DROP) {
-      const DropKey dk = drop_key(a.drop);
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
+          const uint32_t row = keep[(wr * 32 * TM + 32 * i + lr) * 8 + wc * TN + j];   // of lane lr and lr + 32
           f32x16 t;
 #pragma unroll
           for (int e = 0; e < 16; ++e) t[e] = 0.0f;
 #pragma unroll
           for (int c = 0; c < 4; ++c) t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i][c], read_w(ws0, j, c), t, 0, 0, 0);
-          add_dropped(acc[i][j], t, dk, a.drop.c, row0 + 32 * i, a.K, lane,
-                      [&](int x) { return k0 + col_of(32 * j + x); });
+          add_kept(acc[i][j], t, a.drop.c, row);
         }
     } else {
 #pragma unroll

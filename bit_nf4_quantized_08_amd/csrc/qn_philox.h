@@ -35,20 +35,34 @@ __device__ __forceinline__ DropKey drop_key(const DropArgs &d) {
   return k;
 }
 
+// A generator call in parts: start, then the seven rounds in order.
+struct Philox {
+  uint32_t c[4];
+  __device__ __forceinline__ void start(uint64_t g, const DropKey &k) {
+    c[0] = (uint32_t)g; c[1] = (uint32_t)(g >> 32); c[2] = k.o0; c[3] = k.o1;
+  }
+  // Rounds `first` .. first + N - 1 of the seven.
+  template <int N>
+  __device__ __forceinline__ void rounds(const DropKey &k, int first) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (first + i >= 7) break;
+      const uint32_t n = (uint32_t)(first + i);
+      const uint64_t p0 = (uint64_t)0xD2511F53u * c[0], p1 = (uint64_t)0xCD9E8D57u * c[2];
+      c[0] = (uint32_t)(p1 >> 32) ^ c[1] ^ (k.k0 + n * 0x9E3779B9u);
+      c[1] = (uint32_t)p1;
+      c[2] = (uint32_t)(p0 >> 32) ^ c[3] ^ (k.k1 + n * 0xBB67AE85u);
+      c[3] = (uint32_t)p0;
+    }
+  }
+};
+
 // The four words of generator call g.
 __device__ __forceinline__ void philox7(uint64_t g, const DropKey &k, uint32_t (&w)[4]) {
-  uint32_t c0 = (uint32_t)g, c1 = (uint32_t)(g >> 32), c2 = k.o0, c3 = k.o1, k0 = k.k0, k1 = k.k1;
-#pragma unroll
-  for (int i = 0; i < 7; ++i) {
-    const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
-    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
-    c1 = (uint32_t)p1;
-    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
-    c3 = (uint32_t)p0;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
-  w[0] = c0; w[1] = c1; w[2] = c2; w[3] = c3;
+  Philox p;
+  p.start(g, k);
+  p.rounds<7>(k, 0);
+  w[0] = p.c[0]; w[1] = p.c[1]; w[2] = p.c[2]; w[3] = p.c[3];
 }
 
 // Two fields -> 0xFFFF in the half of each kept element, 0 in the other's: field -
@@ -74,6 +88,22 @@ __device__ __forceinline__ uint32_t keep_bits8(const uint32_t (&w)[4], uint32_t 
   return b;
 }
 
+// acc += c keep * t for one 32 x 32 tile, row lr's 32 mask bits in lanes lr and lr
+// + 32 (elements as below): an element's lane mask is two rows' words, read out
+// of their lanes into a scalar pair.
+__device__ __forceinline__ void add_kept(f32x16 &acc, const f32x16 &t, float c, uint32_t row) {
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int ra = 8 * (e >> 2) + (e & 3);
+    const uint64_t mask = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)row, ra + 4) << 32 |
+                          (uint32_t)__builtin_amdgcn_readlane((int)row, ra);
+    const float v = __builtin_fmaf(c, t[e], acc[e]);
+    acc[e] = __builtin_amdgcn_inverse_ballot_w64(mask) ? v : acc[e];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // acc += c keep * t for one 32 x 32 tile of dX's adapter term (a lane's element
 // e is row 8 (e / 4) + 4 (lane / 32) + e % 4, column lane % 32): rows row0 .. +31
 // of a tensor of ncols columns, tile columns x .. x + 7 (x a multiple of 8)
@@ -81,9 +111,9 @@ __device__ __forceinline__ uint32_t keep_bits8(const uint32_t (&w)[4], uint32_t 
 // calls of row lr, x = 16 lh and 16 lh + 8, which puts the 32 x 32 mask in the
 // wave row by row; an element's lane mask is then two rows' words, read out of
 // their lanes into a scalar pair.  Elements that are not kept add nothing,
-// whatever t holds.  It costs dX about 6 us on the NF4 tiles and 4 us on the
-// MXFP4 ones (2048 x 4096 x 4096, r = 16: 75 -> 81 and 64 -> 68 us).  The key passes
-// through an empty asm per tile and the tile
+// whatever t holds.  It costs the NF4 linear's dX about 6 us (2048 x 4096 x 4096, r =
+// 16: 75 -> 81; its producer waves leave the main loop no room for the generator,
+// as the MXFP4 dX's does).  The key passes through an empty asm per tile and the tile
 // is fenced: hoisted out of the adapter step or run ahead of each other, the
 // tiles' generator calls would spill the accumulators.
 template <typename Col>
