@@ -445,7 +445,7 @@ static int linear_bwd(const void *dY, const void *X, const float *H, int64_t M, 
   qn::DropArgs d;
   st = drop_args(drop, d);
   if (st != QN_OK) return st;
-  const size_t need = qn::bwd_workspace(M, W->N, W->K, r) + (d.thr ? qn::qgemm_part_bytes(M, W->K, W->N) : 0);
+  const size_t need = qn::bwd_workspace(M, W->N, W->K, r) + (drop ? qn::qgemm_part_bytes(M, W->K, W->N) : 0);
   if (!workspace || ws_bytes < need) return QN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QN_ERR_ALIGN;
   if (!qn::codec_tables_ok()) return QN_ERR_VALUE;
@@ -464,6 +464,7 @@ static int linear_bwd(const void *dY, const void *X, const float *H, int64_t M, 
   a.dB = static_cast<uint16_t *>(dB);
   a.ws = workspace; a.ws_bytes = ws_bytes;
   a.drop = d;
+  a.dropout = drop != nullptr;
   return hip_status(qn::run_bwd(a, static_cast<hipStream_t>(stream)));
 }
 

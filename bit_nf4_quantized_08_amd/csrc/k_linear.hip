@@ -711,8 +711,7 @@ hipError_t run_fwd_dropout(const FwdArgs &a, hipStream_t st) {
   QGemmArgs g;
   fwd_mfma_args(a, la, g);
   QN_TRY(launch_lowrank(la, st));
-  // Without dropping the result is the plain linear's, bit for bit: not cut.
-  g.splits = a.drop.thr ? qgemm_splits(a.M, a.N, a.K) : 1;
+  g.splits = qgemm_splits(a.M, a.N, a.K);
   if (g.splits == 1) return launch_qgemm_fwd(g, st);
   Carve c(a.ws);
   c.take<uint16_t>(a.M * align_up(a.r, 8));
@@ -793,7 +792,7 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   float *dhpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(a.M, a.N, a.r)));
   float *hpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(a.M, a.K, a.r)));
 
-  const bool fused = a.mx_scales || a.drop.thr;   // the newer paths: B read as it is, sums on the matrix cores
+  const bool fused = a.mx_scales || a.dropout;   // the newer paths: B read as it is, sums on the matrix cores
   // B^T [rp, N] (rows >= r zero) so that dH = dY (B^T)^T runs on the low-rank
   // kernel; with the forward's H given, (sH)^T from it in the same launch.
   if (!fused) {
@@ -824,8 +823,8 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   }
 
   // One launch: dB [N, r] = ((sH)^T dY)^T and dA [r, K] = dH^T X, contractions over
-  // M: on the matrix cores for the MXFP4 base and under dropout; without either
-  // the vector kernel, whose sums (and so whose results) those calls keep.
+  // M: on the matrix cores for the MXFP4 base and for the calls with dropout; the
+  // plain linear keeps the vector kernel, its sums and so its results.
   ColSumArgs sums[2];
   if (fused) {
     const int splits = colsum_splits(a.M, a.N + a.K);

@@ -1773,8 +1773,9 @@ hipError_t launch_split(const QGemmArgs &in, hipStream_t st) {
   grp.n = 1;
   const dim3 grid((unsigned)total, (unsigned)in.splits);
   TraceScope tr(KN ? QN_TRACE_GEMM_DX : QN_TRACE_GEMM_FWD, st);
-  if (in.absmax_q) hipLaunchKernelGGL((qgemm_kernel<KN, true, !KN, false, KN, true>), grid, dim3(kThreads), 0, st, grp, code16(in.qtype));
-  else hipLaunchKernelGGL((qgemm_kernel<KN, false, !KN, false, KN, true>), grid, dim3(kThreads), 0, st, grp, code16(in.qtype));
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, grp, code16(in.qtype)); };
+  if (KN && in.drop.thr) in.absmax_q ? go(qgemm_kernel<KN, true, !KN, false, KN, true>) : go(qgemm_kernel<KN, false, !KN, false, KN, true>);
+  else in.absmax_q ? go(qgemm_kernel<KN, true, !KN, false, false, true>) : go(qgemm_kernel<KN, false, !KN, false, false, true>);
   return hipGetLastError();
 }
 

@@ -292,6 +292,7 @@ struct BwdArgs {
   void *ws;
   size_t ws_bytes;
   DropArgs drop = kNoDrop;
+  bool dropout = false;                 // a call with dropout (whose p may be 0)
   const uint8_t *mx_scales = nullptr;   // non-null: the base is MXFP4 (codes, mx_scales)
 };
 size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r);

@@ -376,7 +376,7 @@ int qn_dropout(const void *x, int dtype, int64_t n, const qn_dropout_config *dro
  *     dH = s G B,  dB = s G^T H,  dA = c dH^T (keep * X),
  *     dX = G bf16(dequant(W)) + c keep * (dH A)
  * keep over [M, K] (element m K + k).  Arguments and shape rules as there; drop
- * is required; with p = 0 the results are the plain linear's on its MFMA path.
+ * is required (its p may be 0: the same sums, nothing dropped).
  * The forward's workspace is qlora_workspace_size(QN_OP_FWD_DROPOUT, ...) bytes
  * (every M takes the MFMA path), the backward's that of QN_OP_BWD; the backward
  * takes M <= 2^24.  A given H is the dropped one, as this forward wrote it. */
