@@ -189,9 +189,15 @@ def qn_table(quant_type="nf4"):
 
 
 # ------------------------------------------------------------------ torch glue
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
@@ -552,7 +558,7 @@ def _operand(t, name, dtype, shape=None):
     comes first: these calls are short, and a full report is made only to raise."""
     if not (getattr(t, "is_cuda", False) and t.dtype == dtype and t.is_contiguous()):
         _need(t, name, dtype)
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
@@ -560,29 +566,36 @@ def _operand(t, name, dtype, shape=None):
 def _launch(tensors, fn, *args):
     """Call fn(*args, stream) on the current stream of the one GPU that all the
     tensors (None skipped) lie on."""
-    torch = _torch()
     dev = None
     for t in tensors:
         if t is not None:
             d = t.get_device()
-            if dev is None:
+            if d != dev:
+                if dev is not None:
+                    raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
                 dev = d
-            elif d != dev:
-                raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
     call = getattr(_lib or load(), fn)
-    if dev == torch.cuda.current_device():
-        _check(fn, call(*args, _raw_stream(dev)))
+    device, stream = _cuda_lookups or _find_lookups()
+    if dev == device():
+        _check(fn, call(*args, stream(dev)))
     else:
-        with torch.cuda.device(dev):
-            _check(fn, call(*args, _raw_stream(dev)))
+        with _torch().cuda.device(dev):
+            _check(fn, call(*args, stream(dev)))
 
 
-def _raw_stream(dev):
-    """hipStream_t of the device's current stream (torch's own lookup, without
-    the Stream object that torch.cuda.current_stream builds around it)."""
+_cuda_lookups = None   # (current device, hipStream_t of a device's current stream)
+
+
+def _find_lookups():
+    """torch's own lookups where it has them: without the initialisation check of
+    torch.cuda.current_device and the Stream object of torch.cuda.current_stream
+    (a GPU tensor is at hand, so the runtime is up)."""
+    global _cuda_lookups
     torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
+    _cuda_lookups = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                     getattr(torch._C, "_cuda_getCurrentRawStream",
+                             lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    return _cuda_lookups
 
 
 @dataclass
@@ -616,23 +629,27 @@ def _drop_ref(drop):
 def dropout(x, drop: Dropout, out=None):
     """qn_dropout of a contiguous fp32 or bf16 tensor of any shape; ``out`` may be
     ``x``.  Applied to a gradient with the same ``drop`` it is the backward."""
-    torch = _torch()
-    _need(x, "x")
-    dt = _codec_type(x, "x")
+    px, dt = _codec_operand(x, "x")
     if out is None:
-        out = torch.empty_like(x)
-    po = _operand(out, "out", x.dtype, tuple(x.shape))
-    _launch((x, out, drop.offset_dev), "qn_dropout", x.data_ptr(), dt, x.numel(), _drop_ref(drop), po)
+        out = _torch().empty_like(x)
+    po = _operand(out, "out", x.dtype, x.shape)
+    _launch((x, out, drop.offset_dev), "qn_dropout", px, dt, x.numel(), _drop_ref(drop), po)
     return out
 
 
-def _codec_type(t, name):
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return QN_BF16
-    if t.dtype == torch.float32:
-        return QN_F32
-    raise ValueError(f"{name} must be float32 or bfloat16")
+_codec_types = {}   # torch type -> QN type
+
+
+def _codec_operand(t, name, shape=None):
+    """Check an fp32 or bf16 operand; (its address, its QN type)."""
+    if not _codec_types:
+        torch = _torch()
+        _codec_types.update({torch.bfloat16: QN_BF16, torch.float32: QN_F32})
+    dt = _codec_types.get(getattr(t, "dtype", None))
+    if dt is None:
+        _need(t, name)
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return _operand(t, name, t.dtype, shape), dt
 
 
 @dataclass
@@ -659,37 +676,41 @@ class MXMatrix:
     def K(self):
         return self.cols
 
-    def struct(self):
+    def addresses(self):
+        """Check the tensors; the addresses of codes and scales."""
         u8 = _torch().uint8
         C = -(-self.cols // QN_MX_CHUNK)
-        return MXMatrixStruct(_operand(self.codes, "codes", u8, (self.rows, 128 * C)),
-                              _operand(self.scales, "scales", u8, (C, self.rows, 8)), self.rows, self.cols)
+        return (_operand(self.codes, "codes", u8, (self.rows, 128 * C)),
+                _operand(self.scales, "scales", u8, (C, self.rows, 8)))
+
+    def struct(self):
+        return MXMatrixStruct(*self.addresses(), self.rows, self.cols)
 
 
 def mxfp4_quantize(X, out: Optional[MXMatrix] = None):
     """qn_mxfp4_quantize of a 2-D fp32 or bf16 device tensor -> MXMatrix."""
-    _need(X, "X", ndim=2)
-    dt = _codec_type(X, "X")
+    px, dt = _codec_operand(X, "X")
+    if X.dim() != 2:
+        _need(X, "X", ndim=2)
     rows, cols = X.shape
     if out is None:
         out = MXMatrix.empty(rows, cols, X.device)
-    if (out.rows, out.cols) != (rows, cols):
+    if out.rows != rows or out.cols != cols:
         raise ValueError("out must have X's shape")
-    st = out.struct()
-    _launch((X, out.codes, out.scales), "qn_mxfp4_quantize", X.data_ptr(), dt, rows, cols, st.codes, st.scales)
+    codes, scales = out.addresses()
+    _launch((X, out.codes, out.scales), "qn_mxfp4_quantize", px, dt, rows, cols, codes, scales)
     return out
 
 
 def mxfp4_dequant(w: MXMatrix, out_dtype="bf16", out=None):
     """The values an MXMatrix stands for, [rows, cols] bf16 (or fp32); a given
     ``out`` decides the type."""
-    torch = _torch()
     st = w.struct()
     if out is None:
+        torch = _torch()
         out = torch.empty((w.rows, w.cols), dtype={"bf16": torch.bfloat16, "f32": torch.float32}[out_dtype],
                           device=w.codes.device)
-    dt = _codec_type(out, "out")
-    po = _operand(out, "out", out.dtype, (w.rows, w.cols))
+    po, dt = _codec_operand(out, "out", (w.rows, w.cols))
     _launch((w.codes, w.scales, out), "qn_mxfp4_dequant", ctypes.byref(st), po, dt)
     return out
 
