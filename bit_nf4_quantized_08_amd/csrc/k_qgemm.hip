@@ -34,7 +34,11 @@
 //
 // dX with dropout on the adapter's input needs c keep(m, n) times the adapter
 // term alone, so that step then multiplies into a zeroed 32 x 32 tile at a time
-// and adds the kept elements to the accumulators (add_dropped).
+// and adds the kept elements to the accumulators: on 256 x 128 tiles with the mask
+// generated there (add_dropped), on 256 x 256 ones with one made before the main
+// loop, while the first loads are on their way (4096 rows, N = 512, K = 8192, r = 16: 86
+// against 76 us; 8192 x 8192, r = 64: 536 against 528; on the narrow tiles the same
+// made the compiler spill the accumulators inside the loop).
 //
 // Weight layouts:
 //   NK (forward): output column n reads weight row n, contraction along K; a
@@ -884,6 +888,25 @@ constexpr int BM2 = 256, BN2 = 256;
 constexpr int R_TILE2 = BN2 * LD;
 constexpr int XSTAGE2 = BM2 * BK;
 
+// A wave's dropout mask, 64 rows x 128 tile columns from row0 of a tensor of ncols
+// columns: row R's 16 bytes at keep + R * pitch, byte b for tile columns first + 8 b
+// .. + 7 (tensor columns n0 + kn_col of them), one generator call.  Only this wave
+// reads it.
+__device__ __forceinline__ void make_wave_mask(uint8_t *keep, int pitch, const DropArgs &d, int64_t row0, int64_t ncols,
+                                               int64_t n0, int first, int lane) {
+  const DropKey dk = drop_key(d);
+  const int b = lane & 15;
+  const uint64_t call0 = (uint64_t)(row0 + (lane >> 4)) * (uint64_t)(ncols / 8) +
+                         (uint64_t)((n0 + kn_col(first + 8 * b)) >> 3);
+  const uint64_t four = (uint64_t)(ncols / 8) * 4;   // calls from a row to the fourth after it
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    uint32_t w[4];
+    philox7(call0 + (uint64_t)k * four, dk, w);
+    keep[(4 * k + (lane >> 4)) * pitch + b] = (uint8_t)keep_bits8(w, dk.thr2);
+  }
+}
+
 template <bool DQ, bool Q4, bool KN, bool DROP = false>
 __global__ __launch_bounds__(kThreads2, 1) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void qgemm2_kernel(QGemmGroup grp, Code16 cb) {
@@ -902,6 +925,7 @@ void qgemm2_kernel(QGemmGroup grp, Code16 cb) {
   __shared__ __attribute__((aligned(16))) uint16_t ws1[R_TILE2];
   // Byte -> (row lo, row hi) table of the transposed-weight expansion (dX).
   __shared__ __attribute__((aligned(16))) float2 pair[KN ? 256 * kPairCopies : 1];
+  __shared__ uint32_t keep[DROP ? BM2 * BN2 / 32 : 1];
   if constexpr (KN) {
     for (int i = threadIdx.x; i < 256 * kPairCopies; i += kThreads2) {
       const int e = i / kPairCopies;
@@ -1008,6 +1032,9 @@ void qgemm2_kernel(QGemmGroup grp, Code16 cb) {
   __builtin_amdgcn_sched_barrier(0);
   P.issue(s1, __builtin_amdgcn_readfirstlane(min(1, last)));
   __builtin_amdgcn_sched_barrier(0);
+  if constexpr (DROP)
+    make_wave_mask(reinterpret_cast<uint8_t *>(keep) + rg * WM * (BN2 / 8) + 16 * cg, BN2 / 8, a.drop, m0 + rg * WM, a.Nout, n0,
+                   128 * cg, lane);
   if constexpr (Q4) P.store_scaled(s0, Scale4::scale(q4.nxt, q4.nxt_s, 0), ws0, nullptr, cb.v, lane, [&](int) {});
   else P.store(s0, ws0, KN ? pair : nullptr, cb.v, lane, [&](int) {});
   P.issue(s0, __builtin_amdgcn_readfirstlane(min(2, last)));
@@ -1239,11 +1266,11 @@ void qgemm2_kernel(QGemmGroup grp, Code16 cb) {
   __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
   lds_barrier();
   if constexpr (DROP) {
-    const DropKey dk = drop_key(a.drop);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
+        const uint32_t row = keep[(rg * WM + 32 * i + lr) * (BN2 / 32) + 4 * cg + j];   // of lanes lr and lr + 32
         f32x16 t;
 #pragma unroll
         for (int e = 0; e < 16; ++e) t[e] = 0.0f;
@@ -1253,8 +1280,7 @@ void qgemm2_kernel(QGemmGroup grp, Code16 cb) {
           const bf16x8 bf = *reinterpret_cast<const bf16x8 *>(&wa[rb + j * 32 * LD + (KN ? (bpos[j] ^ (8 * c)) : 8 * c)]);
           t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af, bf, t, 0, 0, 0);
         }
-        add_dropped(acc[i][j], t, dk, a.drop.c, m0 + rg * WM + 32 * i, a.Nout, lane,
-                    [&](int x) { return n0 + kn_col(128 * cg + 32 * j + x); });
+        add_kept(acc[i][j], t, a.drop.c, row);
       }
   } else {
     Frag f;

@@ -112,8 +112,7 @@ __device__ __forceinline__ void add_kept(f32x16 &acc, const f32x16 &t, float c, 
 // wave row by row; an element's lane mask is then two rows' words, read out of
 // their lanes into a scalar pair.  Elements that are not kept add nothing,
 // whatever t holds.  It costs the NF4 linear's dX about 6 us (2048 x 4096 x 4096, r =
-// 16: 75 -> 81; its producer waves leave the main loop no room for the generator,
-// as the MXFP4 dX's does).  The key passes through an empty asm per tile and the tile
+// 16: 75 -> 81).  The key passes through an empty asm per tile and the tile
 // is fenced: hoisted out of the adapter step or run ahead of each other, the
 // tiles' generator calls would spill the accumulators.
 template <typename Col>
