@@ -71,9 +71,9 @@ KERNEL_SOURCE = {
 # bytes.  Keyed by kernel and workload; `sha256` is that of the kernel's source
 # file and qn_device.h when the counters were taken.
 TRAFFIC = {
-    "gemm_fwd_70b": {"bytes": 1565569317, "sha256": "eeece9299dab90e57c0d8c85d8c243062b22dc01db76f699f6f807421ae217ea"},
-    "lowrank_70b": {"bytes": 176664927, "sha256": "a9720ed64701ca58a3adf8b5f53627d51383e3fd25feb52c5caef37c5c1ca6bb"},
-    "gemv_70b": {"bytes": 114969601, "sha256": "a5da0adfb8a87a342062662a46fde1812682acb87b6815a04b93989080b3022b"},
+    "gemm_fwd_70b": {"bytes": 1566224744, "sha256": "cede002049b0f836776bbdde505c03241c57ada356466e88a7bf1ffc088e87aa"},
+    "lowrank_70b": {"bytes": 176672392, "sha256": "8c54093717a28844c54ba54075b907ecf3182c20a214ab02e89c4f95303ed0b6"},
+    "gemv_70b": {"bytes": 114969662, "sha256": "049094bb4d2ded67c182ccae92b4642599c446d89f0aa5685596677bd807dc34"},
 }
 
 # The configurations (N, K) of the linear layers.
