@@ -238,8 +238,8 @@ typedef struct {
 int qn_adamw8_step_multi(int n_tensors, const qn_adamw_tensor *tensors, const qn_adamw_config *cfg,
                          void *stream);
 
-/* Workspace size in bytes for op = QN_OP_FWD or QN_OP_BWD at the given shape.
- * Returns 0 for an invalid op or shape. */
+/* Workspace size in bytes for op = QN_OP_FWD, QN_OP_FWD_DROPOUT or QN_OP_BWD (with
+ * dropout or without) at the given shape.  Returns 0 for an invalid op or shape. */
 #define QN_OP_FWD 0
 #define QN_OP_BWD 1
 size_t qlora_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t r);
