@@ -7,11 +7,10 @@
 // into LDS as it lies, and the fragments, which need eight consecutive
 // contraction rows of one column, come back through the transposing LDS read
 // (ds_read_b64_tr_b16: 16 lanes point at 4 rows x 16 columns and receive 16
-// columns x 4 rows).  Bound by the bf16 matrix rate at the clock it sustains;
-// LDS reads take about three quarters of the MFMAs' time at 256 x 256.  4096 x 8192 x
-// 8192, r = 64, p = 0.05: 435 to 465 us, 1.2 to 1.27 PFLOP/s, matrix pipes busy 61 %
-// of the cycles at 1.9 GHz; a dense bf16 library product of that shape, weights
-// ready in bf16, takes 408 us.
+// columns x 4 rows).  Bound by the bf16 matrix rate at the clock it sustains:
+// 4096 x 8192 x 8192, r = 64, p = 0.05: 420 to 465 us as the card's clock has it, 1.2
+// to 1.3 PFLOP/s, matrix pipes busy 63 % of the cycles at about 1.9 GHz, LDS a third;
+// a dense bf16 library product of that shape, weights ready in bf16, takes 408 us.
 //
 // A workgroup of 8 waves owns a (32 TM WR) x 256 tile of dX: one chunk of the
 // weight's columns, so a step's scale bytes are 512 contiguous bytes.  Step s
@@ -19,11 +18,13 @@
 // direct-to-LDS loads and the codes of step s + 1, loaded during step s - 1, are
 // expanded into it.
 //
-// Expanded stage: row n (pitch 576 bytes: four rows of a transposing read fall
-// on different banks), 16-byte units of 8 columns.  Thread (n, ch) expands one
-// block, columns 32 ch .. +31, as four units q = 0..3; unit (ch, q) sits at slot
-// 8 q + ch, so that the eight lanes of a write cycle store 128 contiguous
-// bytes.  A wave's columns are the units ch = UW wc .. + UW - 1 for all q (UW =
+// Expanded stage: row n (pitch 544 bytes, 32 past the banks' turn of 256: the eight
+// 32-byte pieces of 32 lanes' transposing reads, four rows at two places 128
+// bytes apart, fall on different banks; with 576 two of the rows met, 18 M
+// conflict cycles against 0.7 M), 16-byte units of 8 columns.  Thread (n, ch)
+// expands one block, columns 32 ch .. +31, as four units q = 0..3; unit (ch, q)
+// sits at slot 8 q + ch, so that the eight lanes of a write cycle store 128
+// contiguous bytes.  A wave's columns are the units ch = UW wc .. + UW - 1 for all q (UW =
 // 8 / WC): 32 UW consecutive columns of dX.  "Tile column" x of a wave is unit
 // (q, u) = (x / 8 / UW, x / 8 % UW).
 //
@@ -42,7 +43,7 @@ namespace {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kRowPitch = 576;           // bytes per expanded row
+constexpr int kRowPitch = 544;           // bytes per expanded row
 constexpr int kWStage = 64 * kRowPitch;  // bytes per expanded stage
 
 template <int TM, int TN, int WR, int WC, bool DROP, bool PART>
