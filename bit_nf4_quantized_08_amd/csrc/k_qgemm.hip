@@ -34,11 +34,10 @@
 //
 // dX with dropout on the adapter's input needs c keep(m, n) times the adapter
 // term alone, so that step then multiplies into a zeroed 32 x 32 tile at a time
-// and adds the kept elements to the accumulators: on 256 x 128 tiles with the mask
-// generated there (add_dropped), on 256 x 256 ones with one made before the main
-// loop, while the first loads are on their way (4096 rows, N = 512, K = 8192, r = 16: 86
-// against 76 us; 8192 x 8192, r = 64: 536 against 528; on the narrow tiles the same
-// made the compiler spill the accumulators inside the loop).
+// and adds the kept elements to the accumulators (add_kept).  A wave's mask is
+// made before the main loop, while the first loads are on their way; in that step,
+// tile by tile, the generator cost more (61 x 512 x 3584 22.3 against 19.2 us, 2048 x 4096
+// x 4096 83 against 79.5; 256 x 256 tiles, 4096 rows, N = 512, K = 8192: 85 against 75).
 //
 // Weight layouts:
 //   NK (forward): output column n reads weight row n, contraction along K; a
@@ -463,6 +462,25 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
+// A wave's dropout mask, 64 rows x 128 tile columns from row0 of a tensor of ncols
+// columns: row R's 16 bytes at keep + R * pitch, byte b for tile columns first + 8 b
+// .. + 7 (tensor columns n0 + kn_col of them), one generator call.  Only this wave
+// reads it.
+__device__ __forceinline__ void make_wave_mask(uint8_t *keep, int pitch, const DropArgs &d, int64_t row0, int64_t ncols,
+                                               int64_t n0, int first, int lane) {
+  const DropKey dk = drop_key(d);
+  const int b = lane & 15;
+  const uint64_t call0 = (uint64_t)(row0 + (lane >> 4)) * (uint64_t)(ncols / 8) +
+                         (uint64_t)((n0 + kn_col(first + 8 * b)) >> 3);
+  const uint64_t four = (uint64_t)(ncols / 8) * 4;   // calls from a row to the fourth after it
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    uint32_t w[4];
+    philox7(call0 + (uint64_t)k * four, dk, w);
+    keep[(4 * k + (lane >> 4)) * pitch + b] = (uint8_t)keep_bits8(w, dk.thr2);
+  }
+}
+
 // Exactly one workgroup (2 waves per SIMD) fits a CU, so tell the compiler
 // that higher occupancy is not reachable: it may then keep a whole step's
 // operands in registers instead of re-reading them one by one.
@@ -488,6 +506,7 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
   __shared__ __attribute__((aligned(16))) uint16_t ws1[R_TILE];
   // Byte -> (row lo, row hi) table for the transposed-weight producers.
   __shared__ __attribute__((aligned(16))) float2 pair[KN ? 256 * kPairCopies : 1];
+  __shared__ uint32_t keep[DROP ? BM * BN / 32 : 1];
   for (int i = threadIdx.x; KN && i < 256 * kPairCopies; i += kThreads) {
     const int e = i / kPairCopies;
     pair[i] = make_float2(cb.v[e & 15], cb.v[e >> 4]);
@@ -683,6 +702,10 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
   // ---------------------------------------------------------- MMA waves
   const int lr = lane & 31, lh = lane >> 5;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
+  if constexpr (DROP)
+    if (split == 0)
+      make_wave_mask(reinterpret_cast<uint8_t *>(keep) + wave_u * WM * (BN / 8), BN / 8, a.drop, m0 + wave_u * WM, a.Nout, n0,
+                     0, lane);
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -777,11 +800,16 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
     const uint16_t *xa = xi == 0 ? xs0 : (xi == 1 ? xs1 : xs2);
     const uint16_t *wa = (steps & 1) ? ws1 : ws0;
     if constexpr (DROP) {
-      const DropKey dk = drop_key(a.drop);
+      // The key is not used: without a branch in this loop's body, as the read of
+      // the device's offset is, the allocator spills the accumulators in the main
+      // loop (as it does with a constant trip count).
+      DropKey dk = drop_key(a.drop);
+      asm volatile("" : "+s"(dk.k0), "+s"(dk.o0));
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
+          const uint32_t row = keep[(wave_u * WM + 32 * i + lr) * (BN / 32) + j];   // of lanes lr and lr + 32
           f32x16 t;
 #pragma unroll
           for (int e = 0; e < 16; ++e) t[e] = 0.0f;
@@ -791,8 +819,7 @@ void qgemm_kernel(QGemmGroup grp, Code16 cb) {
             const bf16x8 bf = *reinterpret_cast<const bf16x8 *>(&wa[rb + j * 32 * LD + (KN ? (bpos[j] ^ (8 * c)) : 8 * c)]);
             t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af, bf, t, 0, 0, 0);
           }
-          add_dropped(acc[i][j], t, dk, a.drop.c, m0 + wave_u * WM + 32 * i, a.Nout, lane,
-                      [&](int x) { return n0 + kn_col(32 * j + x); });
+          add_kept(acc[i][j], t, a.drop.c, row);
         }
     } else {
 #pragma unroll
@@ -887,25 +914,6 @@ constexpr int kThreads2 = 512;
 constexpr int BM2 = 256, BN2 = 256;
 constexpr int R_TILE2 = BN2 * LD;
 constexpr int XSTAGE2 = BM2 * BK;
-
-// A wave's dropout mask, 64 rows x 128 tile columns from row0 of a tensor of ncols
-// columns: row R's 16 bytes at keep + R * pitch, byte b for tile columns first + 8 b
-// .. + 7 (tensor columns n0 + kn_col of them), one generator call.  Only this wave
-// reads it.
-__device__ __forceinline__ void make_wave_mask(uint8_t *keep, int pitch, const DropArgs &d, int64_t row0, int64_t ncols,
-                                               int64_t n0, int first, int lane) {
-  const DropKey dk = drop_key(d);
-  const int b = lane & 15;
-  const uint64_t call0 = (uint64_t)(row0 + (lane >> 4)) * (uint64_t)(ncols / 8) +
-                         (uint64_t)((n0 + kn_col(first + 8 * b)) >> 3);
-  const uint64_t four = (uint64_t)(ncols / 8) * 4;   // calls from a row to the fourth after it
-#pragma unroll 4
-  for (int k = 0; k < 16; ++k) {
-    uint32_t w[4];
-    philox7(call0 + (uint64_t)k * four, dk, w);
-    keep[(4 * k + (lane >> 4)) * pitch + b] = (uint8_t)keep_bits8(w, dk.thr2);
-  }
-}
 
 template <bool DQ, bool Q4, bool KN, bool DROP = false>
 __global__ __launch_bounds__(kThreads2, 1) __attribute__((amdgpu_waves_per_eu(2, 2)))

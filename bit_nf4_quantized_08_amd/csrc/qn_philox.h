@@ -88,9 +88,12 @@ __device__ __forceinline__ uint32_t keep_bits8(const uint32_t (&w)[4], uint32_t 
   return b;
 }
 
-// acc += c keep * t for one 32 x 32 tile, row lr's 32 mask bits in lanes lr and lr
-// + 32 (elements as below): an element's lane mask is two rows' words, read out
-// of their lanes into a scalar pair.
+// acc += c keep * t for one 32 x 32 tile of dX's adapter term (a lane's element
+// e is row 8 (e / 4) + 4 (lane / 32) + e % 4, column lane % 32), with row lr's 32
+// mask bits in lanes lr and lr + 32: an element's lane mask is two rows' words,
+// read out of their lanes into a scalar pair.  Elements that are not kept add
+// nothing, whatever t holds.  The tiles are fenced from each other: run ahead, they
+// would spill the accumulators.
 __device__ __forceinline__ void add_kept(f32x16 &acc, const f32x16 &t, float c, uint32_t row) {
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -98,46 +101,6 @@ __device__ __forceinline__ void add_kept(f32x16 &acc, const f32x16 &t, float c, 
     const int ra = 8 * (e >> 2) + (e & 3);
     const uint64_t mask = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)row, ra + 4) << 32 |
                           (uint32_t)__builtin_amdgcn_readlane((int)row, ra);
-    const float v = __builtin_fmaf(c, t[e], acc[e]);
-    acc[e] = __builtin_amdgcn_inverse_ballot_w64(mask) ? v : acc[e];
-  }
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-// acc += c keep * t for one 32 x 32 tile of dX's adapter term (a lane's element
-// e is row 8 (e / 4) + 4 (lane / 32) + e % 4, column lane % 32): rows row0 .. +31
-// of a tensor of ncols columns, tile columns x .. x + 7 (x a multiple of 8)
-// its columns col(x) .. col(x) + 7, one generator call.  Lane (lr, lh) runs the
-// calls of row lr, x = 16 lh and 16 lh + 8, which puts the 32 x 32 mask in the
-// wave row by row; an element's lane mask is then two rows' words, read out of
-// their lanes into a scalar pair.  Elements that are not kept add nothing,
-// whatever t holds.  It costs the NF4 linear's dX about 6 us (2048 x 4096 x 4096, r =
-// 16: 75 -> 81).  The key passes through an empty asm per tile and the tile
-// is fenced: hoisted out of the adapter step or run ahead of each other, the
-// tiles' generator calls would spill the accumulators.
-template <typename Col>
-__device__ __forceinline__ void add_dropped(f32x16 &acc, const f32x16 &t, DropKey dk, float c, int64_t row0,
-                                            int64_t ncols, int lane, Col &&col) {
-  const int lr = lane & 31, lh = lane >> 5;
-  uint32_t half = 0;
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" : "+s"(dk.k0), "+s"(dk.o0), "+v"(row0));
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int64_t n = col(16 * lh + 8 * q);
-    uint32_t w[4];
-    philox7((uint64_t)(row0 + lr) * (uint64_t)(ncols / 8) + (uint64_t)(n >> 3), dk, w);
-    half |= keep_bits8(w, dk.thr2) << (8 * q);
-  }
-  // The row's 32 bits: low 16 in lane lr, high 16 in lane lr + 32.
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int ra = 8 * (e >> 2) + (e & 3), rb = ra + 4;
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)half, ra) |
-                        (uint32_t)__builtin_amdgcn_readlane((int)half, ra + 32) << 16;
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)half, rb) |
-                        (uint32_t)__builtin_amdgcn_readlane((int)half, rb + 32) << 16;
-    const uint64_t mask = ((uint64_t)hi << 32) | lo;
     const float v = __builtin_fmaf(c, t[e], acc[e]);
     acc[e] = __builtin_amdgcn_inverse_ballot_w64(mask) ? v : acc[e];
   }
