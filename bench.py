@@ -71,9 +71,9 @@ KERNEL_SOURCE = {
 # bytes.  Keyed by kernel and workload; `sha256` is that of the kernel's source
 # file and qn_device.h when the counters were taken.
 TRAFFIC = {
-    "gemm_fwd_70b": {"bytes": 1566224744, "sha256": "cede002049b0f836776bbdde505c03241c57ada356466e88a7bf1ffc088e87aa"},
-    "lowrank_70b": {"bytes": 176672392, "sha256": "8c54093717a28844c54ba54075b907ecf3182c20a214ab02e89c4f95303ed0b6"},
-    "gemv_70b": {"bytes": 114969662, "sha256": "049094bb4d2ded67c182ccae92b4642599c446d89f0aa5685596677bd807dc34"},
+    "gemm_fwd_70b": {"bytes": 1562081494, "sha256": "091b33ddf00ec1a8719d9ccce2e16881e6b3be57649edc14f1a051fae19bf93b"},
+    "lowrank_70b": {"bytes": 176677707, "sha256": "8c54093717a28844c54ba54075b907ecf3182c20a214ab02e89c4f95303ed0b6"},
+    "gemv_70b": {"bytes": 114969718, "sha256": "049094bb4d2ded67c182ccae92b4642599c446d89f0aa5685596677bd807dc34"},
 }
 
 # The configurations (N, K) of the linear layers.
