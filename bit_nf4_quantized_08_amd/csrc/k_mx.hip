@@ -28,6 +28,7 @@
 #include <algorithm>
 
 #include "qn_mx.h"
+#include "qn_mx_scales.h"
 #include "qn_philox.h"
 #include "qn_tile.h"
 
@@ -258,12 +259,12 @@ void mx_gemm_kernel(MxGemmArgs a) {
   // Scales: load p covers rows 128 p .. of X^'s BM rows and then W's.  Every wave
   // makes one load, so some are made twice, with the same bytes to the same
   // place: a branch here would split the step's block, and the compiler would
-  // move the MFMAs past it.  Rows past the matrix get other rows' scales (or
-  // zero): their products are not stored.
+  // move the MFMAs past it.  Rows past the matrix get the last rows' scales: their
+  // products are not stored.
   const int erow = 128 * (wave % EP);
   const bool of_x = erow < BM;
   const rsrc_t re = of_x ? make_rsrc_u(a.xs, a.C * a.M * 8) : make_rsrc_u(a.ws, (a.C - 1) * a.ldn * 8 + a.N * 8);
-  const uint32_t eo = (uint32_t)((of_x ? m0 + erow : n0 + erow - BM) * 8 + lane * 16);
+  const uint32_t eo = mx_scale_pair((of_x ? m0 + erow : n0 + erow - BM) + 2 * lane, of_x ? a.M : a.N);
   const int estep = (int)((of_x ? a.M : a.ldn) * 8);
   // Load i of step s into a stage.
   constexpr int LOADS = XL + WL + 1;
@@ -961,8 +962,8 @@ FwdPieces fwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r) {
   FwdPieces p{};
   Carve c(ws);
   const int64_t C = mx_chunks(K);
+  p.xs = c.take<uint8_t>(M * 8 * C);   // the codes come after it: mx_scale_pair
   p.xc = c.take<uint8_t>(M * 128 * C);
-  p.xs = c.take<uint8_t>(M * 8 * C);
   const int splits = M <= kDecodeRows ? decode_plan(M, N, K).ksplits : gemm_plan(M, N, C).splits;
   if (splits > 1) p.y_part = c.take<float>((int64_t)splits * M * N);
   if (r && (M <= kDecodeRows || (M <= kPrepRows && splits > 1))) {

@@ -9,8 +9,10 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;  // a per-lane offset that always reads zero
 
-// Wave-uniform buffer resource over [base, base + bytes); accesses beyond
-// `bytes` (by the per-lane offset) read zero and store nothing.
+// Wave-uniform buffer resource over [base, base + bytes); accesses whose per-lane
+// offset lies beyond `bytes` read zero and store nothing.  A scalar offset is not
+// counted on to take part in that check: where one is used, every lane's offset is
+// out of range by itself or inside together with it.
 __device__ __forceinline__ rsrc_t make_rsrc_u(const void *base, int64_t bytes) {
   const int64_t cap = 0xFFFFFFF0LL;
   const uint64_t p = (uint64_t)base;
