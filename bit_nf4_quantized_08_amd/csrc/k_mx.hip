@@ -645,9 +645,16 @@ __device__ __forceinline__ bf16x8 load_sh(const AdapterArgs &a, int64_t m, int j
   return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(a.sH + m * 64 + j0));
 }
 
+// The rest's sum is kept apart and added where it is finite: an infinite s H (or
+// one that rounds to an infinite bf16) leaves the rest an opposite infinity or NaN,
+// and an infinite element of B an infinity of either sign, while the high pieces
+// alone give the infinity that the product has.
 __device__ __forceinline__ f32x4 add_adapter(f32x4 acc, bf16x8 b, const HPieces &h) {
+  const f32x4 rest = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, h.lo, zero4(), 0, 0, 0);
   acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, h.hi, acc, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, h.lo, acc, 0, 0, 0);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] += __builtin_isfinite(rest[e]) ? rest[e] : 0.0f;
+  return acc;
 }
 
 struct MxDecodeArgs {
@@ -775,15 +782,26 @@ __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4)))
   // acc[g][b][e]: weight row 16 g + 4 kb + e, row 16 b + l16 of X.
   // The adapter term is linear in H, so each wave adds that of the partial sums
   // its segment index selects (with one workgroup over K there is one per
-  // segment), and none stands at all of them.
+  // segment), and none stands at all of them.  Under an infinite element of B the
+  // parts' signs would meet as inf - inf: the first segment's wave then adds the
+  // term of all of H, the others none (every wave of the rows sees the same B).
   if (a.out && a.ad.hp && seg < a.ad.hsplits) {
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int64_t m = 16 * b + l16, mc = min(m, a.M - 1);
+    for (int q = 0; q < 2; ++q) {
+      const int j0 = 32 * q + 8 * kb;
+      if (32 * q >= a.ad.r) break;
+      bf16x8 bv[G];
+      uint32_t top = 0;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int j0 = 32 * q + 8 * kb;
-        if (32 * q >= a.ad.r) break;
+      for (int g = 0; g < G; ++g) {
+        bv[g] = PRE ? pb[q] : load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0);
+        const u32x4 u[1] = {__builtin_bit_cast(u32x4, bv[g])};
+        top = max(top, unit_amax<true>(u));
+      }
+      const bool whole = __any(top >= 0x7F80u);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const int64_t m = 16 * b + l16, mc = min(m, a.M - 1);
         float h[8];
         if (PRE) {
 #pragma unroll
@@ -791,10 +809,12 @@ __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4)))
         } else {
           sum_h(a.ad, a.M, mc, j0, seg, seg + 1, h);
         }
-        const HPieces p = pieces_of(a.ad, h);
+        if (whole) sum_h(a.ad, a.M, mc, j0, 0, seg == 0 ? a.ad.hsplits : 0, h);
+        if (!whole || seg == 0) {
+          const HPieces p = pieces_of(a.ad, h);
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-          acc[g][b] = add_adapter(acc[g][b], PRE ? pb[q] : load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0), p);
+          for (int g = 0; g < G; ++g) acc[g][b] = add_adapter(acc[g][b], bv[g], p);
+        }
         if (a.ad.H_out && rb == 0 && rg == 0 && seg == 0) {
           sum_h(a.ad, a.M, mc, j0, 0, a.ad.hsplits, h);
           if (m < a.M) store_h(a.ad, m, j0, h);
