@@ -38,6 +38,25 @@ namespace {
 constexpr int CS_THREADS = 512;
 constexpr int CS_COLS = 256;
 
+// Two bf16 values a dword with infinities and NaN as zero: (0x7F80 - exponent bits),
+// 0 for those only, at most 1, times the value.  In asm for what keep_mask2 says.
+__device__ __forceinline__ uint32_t finite_or_zero2(uint32_t w) {
+  uint32_t d = w & 0x7F807F80u;
+  asm("v_pk_sub_u16 %0, %1, %0" : "+v"(d) : "s"(0x7F807F80u));
+  asm("v_pk_min_u16 %0, %0, %1" : "+v"(d) : "s"(0x00010001u));
+  asm("v_pk_mul_lo_u16 %0, %0, %1" : "+v"(d) : "v"(w));
+  return d;
+}
+
+// What the second piece of L multiplies: an infinite element of Q times the first
+// piece gives the sum its infinity or NaN, times a rest of either sign it would
+// make every such sum NaN.
+__device__ __forceinline__ bf16x8 finite_or_zero(bf16x8 q) {
+  const u32x4 w = __builtin_bit_cast(u32x4, q);
+  return __builtin_bit_cast(bf16x8, (u32x4{finite_or_zero2(w.x), finite_or_zero2(w.y), finite_or_zero2(w.z),
+                                           finite_or_zero2(w.w)}));
+}
+
 template <int RT, bool DROP>   // 32-rank tiles
 __global__ __launch_bounds__(CS_THREADS) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
@@ -119,10 +138,11 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const bf16x8 b = read_transposed(qs + fq + c * 4096, qs + fq + c * 4096 + 2048);
+      const bf16x8 bf = finite_or_zero(b);
 #pragma unroll
       for (int t = 0; t < 2 * RT; ++t)
         acc[t % RT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            *reinterpret_cast<const bf16x8 *>(l + t * 32 * 128 + fl[c]), b, acc[t % RT], 0, 0, 0);
+            *reinterpret_cast<const bf16x8 *>(l + t * 32 * 128 + fl[c]), t < RT ? b : bf, acc[t % RT], 0, 0, 0);
     }
   };
 

@@ -366,7 +366,10 @@ __global__ __launch_bounds__(256) void lowrank_finish_kernel(LowRankGroup grp) {
         const float v = (jj < a.R && m < a.M) ? tile[r][jj] * a.scale : 0.0f;
         const uint16_t hi = f32_to_bf16(v);
         a.out_t[(int64_t)jj * a.Mp + m] = hi;
-        if (a.t_pieces == 2) a.out_t[(a.ldt_rows + jj) * a.Mp + m] = f32_to_bf16(v - bf16_to_f32(hi));
+        // An infinite first piece (of a value infinite itself or only in bf16) is all
+        // there is to say: the rest would be an opposite infinity or NaN.
+        if (a.t_pieces == 2)
+          a.out_t[(a.ldt_rows + jj) * a.Mp + m] = (hi & 0x7FFFu) < 0x7F80u ? f32_to_bf16(v - bf16_to_f32(hi)) : (uint16_t)0;
       }
     }
   }

@@ -1,14 +1,15 @@
 """Infinities in the adapter's path.  Where a factor is held as two bf16 pieces
 (the value and its rest), an infinite value or an infinite other factor must give
 what the product gives, an infinity of its sign, and not the NaN of inf - inf: Y of
-the MXFP4 forward for every row count against the signs of the exact result."""
+the MXFP4 forward for every row count against the signs of the exact result, dA and
+dB of the MXFP4 backward and of the dropout backward against the plain linear's."""
 
 import numpy as np
 import pytest
 import torch
 
 from bit_nf4_quantized_08_amd import lib, synth
-from tests.gpu_util import dev, host, say, to_dev
+from tests.gpu_util import REL_FRO_TOL, dev, host, rel_fro, say, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,40 @@ def test_mx_forward(M, N, K, kind):
         s = sign.float().numpy()
         assert np.isinf(Hv[:, j0]).all() if kind == "H" else np.isfinite(Hv).all()
         np.testing.assert_array_equal(got, np.sign(s[:, None] * B[:, j0].float().numpy()[None, :]) * np.float32(INF))
+
+
+def _spoil(kind, X, G, H):
+    """One non-finite spot in a backward's inputs."""
+    if kind == "H":
+        H[2, 3], H[1, 5], H[3, 0] = INF, -INF, 3.4e38   # the last is finite, its bf16 is not
+    elif kind == "nan":
+        H[2, 3] = float("nan")
+    elif kind == "G":
+        G[1, 7], G[3, 9] = INF, -INF
+    elif kind == "X":
+        X[3, 9], X[0, 17] = INF, -INF
+
+
+@pytest.mark.parametrize("kind", ["H", "nan", "G", "X"])
+@pytest.mark.parametrize("r", [8, 40])
+@pytest.mark.parametrize("M", [4, 100, 300])
+@pytest.mark.parametrize("base", ["mx", "nf4"])
+def test_adapter_gradients(base, M, r, kind):
+    """dA and dB: infinities, NaN and finite values where the plain backward has them."""
+    say(f"{base} backward, infinite {kind}, M={M} r={r}")
+    N, K = 192, 320
+    W, X, A, B, G = _inputs(M, N, K, r, M + r)
+    H = torch.from_numpy(synth.gaussian((M, r), 1.0, 9))
+    _spoil(kind, X, G, H)
+    X, A, B, G, H = (t.to(dev()) for t in (X, A, B, G, H))
+    w = lib.quantize_weight(to_dev(W))
+    _, dA0, dB0 = lib.qlora_linear_bwd(G, X, w, A, B, float(r), H=H)
+    if base == "mx":
+        _, dA, dB = lib.qlora_mx_linear_bwd(G, X, lib.mxfp4_quantize(to_dev(W)), A, B, float(r), H=H)
+    else:
+        _, dA, dB = lib.qlora_linear_bwd_dropout(G, X, w, A, B, float(r), lib.Dropout(0.0, 1), H=H)
+    for name, a, b in (("dA", host(dA), host(dA0)), ("dB", host(dB), host(dB0))):
+        np.testing.assert_array_equal(np.isnan(a), np.isnan(b), err_msg=name)
+        np.testing.assert_array_equal(np.isinf(a) * np.sign(a), np.isinf(b) * np.sign(b), err_msg=name)
+        f = np.isfinite(b)
+        assert rel_fro(a[f], b[f]) <= 2 * REL_FRO_TOL   # either is within REL_FRO_TOL of the exact one
