@@ -2,8 +2,8 @@
 // Q[m][c] for j < R <= 64, the contraction of dA = dH^T (keep * X) and dB^T = (s
 // H)^T dY, which runs down the rows of row-major activations.  L is fp32 given as
 // two bf16 pieces, the rounded value and the rounded rest (2^-17 of it is left
-// over), [2][rows, Mp] with rows = R rounded up to 32, zero beyond R and M: with
-// one piece the rounding of L would be as large as that of the bf16 result.
+// over), [2][R, Mp], zero beyond M: with one piece the rounding of L would be as
+// large as that of the bf16 result.
 //
 // Bound by reading Q once (both sums of 4096 rows of 8192, r = 64, with dropout:
 // 134 MB in 37 us, 3.6 TB/s, then 8 us for the reduction); the products are 128 MACs
@@ -106,16 +106,16 @@ void colsum_kernel(ColSumArgs a0, ColSumArgs a1) {
   };
   // L: direct load g covers stage rows 8 g .. + 7, 64 rows of Q (128 bytes); RT per
   // wave.  Stage rows 0 .. 32 RT - 1 are the first piece's ranks, the others the
-  // second's, as in memory.
+  // second's; ranks from R on are out of range and come as zeros.
   const int lj = 8 * RT * wave + (lane >> 3);
   uint32_t lo[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    const int j = lj + 8 * i;
-    lo[i] = (uint32_t)(j * a.Mp * 2 + 16 * ((lane & 7) ^ ((j >> 1) & 7)));
+    const int j = lj + 8 * i, rank = j & (32 * RT - 1), piece = j / (32 * RT);
+    lo[i] = rank < a.R ? (uint32_t)((piece * a.R + rank) * a.Mp * 2 + 16 * ((lane & 7) ^ ((j >> 1) & 7))) : kOutOfRange;
   }
   auto issue_l = [&](uint8_t *dst, int s) {
-    const rsrc_t rl = make_rsrc_u(a.Lt + (int64_t)s * 64, (64 * RT * a.Mp - (int64_t)s * 64) * 2);
+    const rsrc_t rl = make_rsrc_u(a.Lt + (int64_t)s * 64, (2 * a.R * a.Mp - (int64_t)s * 64) * 2);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
       load_lds16(rl, (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_offset(dst)) + (wave * RT + i) * 1024, lo[i], 0);

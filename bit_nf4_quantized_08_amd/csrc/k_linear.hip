@@ -757,21 +757,40 @@ hipError_t run_fwd_group(const FwdArgs *a, int n, hipStream_t st) {
 
 // ---------------------------------------------------------------- backward
 
-// r = 0 (the MXFP4 linear without an adapter) has dX only.
-size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r) {
-  Carve c(nullptr);
-  if (r == 0) return 0;
-  const int64_t rp = align_up(r, 32);
-  const int64_t Mp = align_up(M, BK);
-  c.take<uint16_t>(rp * N);                 // B^T
-  c.take<uint16_t>(M * rp);                 // dH bf16 [M, rp]
-  c.take<uint16_t>(2 * rp * Mp);            // dH^T bf16 [rp, Mp], two pieces on the newer paths
-  c.take<uint16_t>(2 * rp * Mp);            // (sH)^T likewise
-  c.take<float>((int64_t)colred_splits(M) * r * N);   // dB partials
-  c.take<float>((int64_t)colred_splits(M) * r * K);   // dA partials
-  c.take<char>((int64_t)lowrank_part_bytes(M, N, r));  // dH partial products
-  c.take<char>((int64_t)lowrank_part_bytes(M, K, r));  // H partial products (H not given)
-  return c.off;
+// The backward's workspace.  The fused paths (the MXFP4 base, and the calls with
+// dropout) read B as it is and have no B^T; they keep dH^T and (s H)^T in two bf16
+// pieces, and sum dA and dB over colsum_splits ranges, whose sums lie where the
+// low-rank products' were: those are read before they are written.
+struct BwdPieces {
+  uint16_t *Bt;            // plain: B^T [rp, N]
+  uint16_t *dHb;           // bf16 dH [M, rp]
+  uint16_t *dHt, *sHt;     // dH^T and (s H)^T: [rp, Mp], fused [2][r, Mp]
+  float *bpart, *apart;    // dB's and dA's sums by range
+  float *dhpart, *hpart;   // partial products of dH, of H
+  size_t bytes;
+};
+static BwdPieces bwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r, bool fused) {
+  BwdPieces p{};
+  if (r == 0) return p;   // the MXFP4 linear without an adapter has dX only
+  Carve c(ws);
+  const int64_t rp = align_up(r, 32), Mp = align_up(M, BK);
+  if (!fused) p.Bt = c.take<uint16_t>(rp * N);
+  p.dHb = c.take<uint16_t>(M * rp);
+  p.dHt = c.take<uint16_t>(2 * (fused ? r : rp) * Mp);
+  p.sHt = c.take<uint16_t>(2 * (fused ? r : rp) * Mp);
+  const int64_t ranges = fused ? colsum_splits(M, N + K) : colred_splits(M);
+  Carve sums = c;
+  p.bpart = sums.take<float>(ranges * r * N);
+  p.apart = sums.take<float>(ranges * r * K);
+  if (!fused) c = sums;
+  p.dhpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, N, r)));
+  p.hpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(M, K, r)));
+  p.bytes = std::max(c.off, sums.off);
+  return p;
+}
+
+size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r, bool fused) {
+  return bwd_pieces(nullptr, M, N, K, r, fused).bytes;
 }
 
 hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
@@ -780,25 +799,18 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
                static_cast<float *>(a.ws), 0};
     return a.dX ? launch_mx_dx(x, nullptr, st) : hipSuccess;
   }
-  Carve c(a.ws);
+  const bool fused = a.mx_scales || a.dropout;   // the newer paths: B read as it is, sums on the matrix cores
   const int64_t rp = align_up(a.r, 32);
   const int64_t Mp = align_up(a.M, BK);
-  uint16_t *Bt = c.take<uint16_t>(rp * a.N);
-  uint16_t *dHb = c.take<uint16_t>(a.M * rp);
-  uint16_t *dHt = c.take<uint16_t>(2 * rp * Mp);
-  uint16_t *sHt = c.take<uint16_t>(2 * rp * Mp);
-  float *bpart = c.take<float>((int64_t)colred_splits(a.M) * a.r * a.N);
-  float *apart = c.take<float>((int64_t)colred_splits(a.M) * a.r * a.K);
-  float *dhpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(a.M, a.N, a.r)));
-  float *hpart = reinterpret_cast<float *>(c.take<char>((int64_t)lowrank_part_bytes(a.M, a.K, a.r)));
+  const BwdPieces w = bwd_pieces(a.ws, a.M, a.N, a.K, a.r, fused);
+  float *xpart = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.bytes);   // dX's partial products
 
-  const bool fused = a.mx_scales || a.dropout;   // the newer paths: B read as it is, sums on the matrix cores
   // B^T [rp, N] (rows >= r zero) so that dH = dY (B^T)^T runs on the low-rank
   // kernel; with the forward's H given, (sH)^T from it in the same launch.
   if (!fused) {
     const int64_t elems = rp * a.N + (a.H ? rp * Mp : 0);
     hipLaunchKernelGGL(bwd_prep_kernel, dim3((unsigned)cdiv(elems, kThreads)), dim3(kThreads), 0, st, a.B, a.N,
-                       a.r, rp, Bt, a.H, a.M, Mp, a.s, sHt);
+                       a.r, rp, w.Bt, a.H, a.M, Mp, a.s, w.sHt);
     QN_TRY(hipGetLastError());
   }
   // One launch: dH = s dY B -> dHb [M, rp], dHt [rp, Mp]; without a given H also
@@ -806,11 +818,11 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   {
     LowRankArgs ld{}, lh{};
     ld.L = a.dY; ld.ldl = a.N; ld.M = a.M; ld.Kc = a.N;
-    ld.P = Bt; ld.ldp = a.N; ld.R = a.r; ld.scale = a.s;
-    ld.out_b = dHb; ld.ldb = rp; ld.out_t = dHt; ld.ldt_rows = rp; ld.Mp = Mp; ld.part = dhpart;
+    ld.P = w.Bt; ld.ldp = a.N; ld.R = a.r; ld.scale = a.s;
+    ld.out_b = w.dHb; ld.ldb = rp; ld.out_t = w.dHt; ld.ldt_rows = fused ? a.r : rp; ld.Mp = Mp; ld.part = w.dhpart;
     lh.L = a.X; lh.ldl = a.K; lh.M = a.M; lh.Kc = a.K;
     lh.P = a.A; lh.ldp = a.K; lh.R = a.r; lh.scale = a.s; lh.drop = a.drop;
-    lh.out_t = sHt; lh.ldt_rows = rp; lh.Mp = Mp; lh.part = hpart;
+    lh.out_t = w.sHt; lh.ldt_rows = fused ? a.r : rp; lh.Mp = Mp; lh.part = w.hpart;
     if (fused) {
       ld.P = a.B;
       ld.p_transposed = true;
@@ -828,22 +840,21 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
   ColSumArgs sums[2];
   if (fused) {
     const int splits = colsum_splits(a.M, a.N + a.K);
-    sums[0] = ColSumArgs{sHt, Mp, a.dY, a.M, a.N, a.r, bpart, splits, a.dB, true, kNoDrop};
-    sums[1] = ColSumArgs{dHt, Mp, a.X, a.M, a.K, a.r, apart, splits, a.dA, false, a.drop};
+    sums[0] = ColSumArgs{w.sHt, Mp, a.dY, a.M, a.N, a.r, w.bpart, splits, a.dB, true, kNoDrop};
+    sums[1] = ColSumArgs{w.dHt, Mp, a.X, a.M, a.K, a.r, w.apart, splits, a.dA, false, a.drop};
     QN_TRY(launch_colsum2(sums[0], sums[1], st, QN_TRACE_GEMM_DB));
     if (!a.dX) return launch_colsum_reduce(sums[0], sums[1], st);
   } else {
     ColRedArgs cb{}, ca{};
-    cb.Lt = sHt; cb.Mp = Mp; cb.Q = a.dY; cb.ldq = a.N; cb.M = a.M; cb.Ncols = a.N; cb.R = a.r;
-    cb.part = bpart; cb.out = a.dB; cb.transpose = true;
-    ca.Lt = dHt; ca.Mp = Mp; ca.Q = a.X; ca.ldq = a.K; ca.M = a.M; ca.Ncols = a.K; ca.R = a.r;
-    ca.part = apart; ca.out = a.dA; ca.transpose = false;
+    cb.Lt = w.sHt; cb.Mp = Mp; cb.Q = a.dY; cb.ldq = a.N; cb.M = a.M; cb.Ncols = a.N; cb.R = a.r;
+    cb.part = w.bpart; cb.out = a.dB; cb.transpose = true;
+    ca.Lt = w.dHt; ca.Mp = Mp; ca.Q = a.X; ca.ldq = a.K; ca.M = a.M; ca.Ncols = a.K; ca.R = a.r;
+    ca.part = w.apart; ca.out = a.dA; ca.transpose = false;
     QN_TRY(launch_colred2(cb, &ca, st, QN_TRACE_GEMM_DB));
   }
   // dX [M, K] = dY [M, N] * W_hat [N, K] + dH [M, r] * A [r, K]
   if (a.dX && a.mx_scales) {
-    MxDxArgs x{a.dY, a.M, a.N, a.K, a.codes, a.mx_scales, dHb, rp, a.A, a.r, a.drop, a.dX,
-               reinterpret_cast<float *>(c.take<char>((int64_t)mx_dx_part_bytes(a.M, a.N, a.K))), 0};
+    MxDxArgs x{a.dY, a.M, a.N, a.K, a.codes, a.mx_scales, w.dHb, rp, a.A, a.r, a.drop, a.dX, xpart, 0};
     return launch_mx_dx(x, sums, st);
   }
   if (a.dX) {
@@ -851,11 +862,11 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     g.L = a.dY; g.ldl = a.N; g.M = a.M; g.Nout = a.K; g.Kc = a.N;
     g.codes = a.codes; g.absmax = a.sc.absmax; g.absmax_q = a.sc.absmax_q; g.scale2 = a.sc.scale2;
     g.qtype = a.sc.qtype;
-    g.L2 = dHb; g.ldl2 = rp; g.R2 = a.A; g.ldr2 = a.K; g.r = a.r;
+    g.L2 = w.dHb; g.ldl2 = rp; g.R2 = a.A; g.ldr2 = a.K; g.r = a.r;
     g.out = a.dX; g.ldo = a.K; g.drop = a.drop;
     g.splits = fused ? qgemm_splits(a.M, a.K, a.N) : 1;
     if (g.splits > 1) {
-      g.part = c.take<float>((int64_t)g.splits * a.M * a.K);
+      g.part = xpart;
       QN_TRY(launch_qgemm_split(g, true, st));
       return launch_split_sum(g.part, g.splits, a.M * a.K, a.dX, sums, st);
     }

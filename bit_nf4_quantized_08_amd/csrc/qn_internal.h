@@ -227,7 +227,7 @@ hipError_t launch_colred2(const ColRedArgs &a, const ColRedArgs *b, hipStream_t 
 // The same sums on the matrix cores (k_colsum.hip), for the MXFP4 linear and for
 // dropout: `part` holds splits * R * Ncols floats, Ncols % 64 == 0.
 struct ColSumArgs {
-  const uint16_t *Lt;  // [2][R rounded up to 32, Mp]: two bf16 pieces
+  const uint16_t *Lt;  // [2][R, Mp]: two bf16 pieces
   int64_t Mp;
   const uint16_t *Q;   // [M, Ncols]
   int64_t M, Ncols, R;
@@ -295,7 +295,8 @@ struct BwdArgs {
   bool dropout = false;                 // a call with dropout (whose p may be 0)
   const uint8_t *mx_scales = nullptr;   // non-null: the base is MXFP4 (codes, mx_scales)
 };
-size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r);
+// Without dX's partial products; fused: the MXFP4 base and the calls with dropout.
+size_t bwd_workspace(int64_t M, int64_t N, int64_t K, int64_t r, bool fused);
 hipError_t run_bwd(const BwdArgs &a, hipStream_t s);
 
 // ---- MXFP4 (k_mx.hip, k_mxdx.hip).  Layouts as qn_mx_matrix.
