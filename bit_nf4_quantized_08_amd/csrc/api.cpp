@@ -124,10 +124,6 @@ int check_mx(const qn_mx_matrix *W) {
   return QN_OK;
 }
 
-size_t bwd_dropout_need(int64_t M, int64_t N, int64_t K, int64_t r) {
-  return qn::bwd_workspace(M, N, K, r, true) + qn::qgemm_part_bytes(M, K, N);
-}
-
 bool mx_shapes_ok(int64_t M, int64_t N, int64_t K, int64_t r) {
   if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > QN_MAX_RANK) return false;
   if (K % 64 != 0 || N % 64 != 0) return false;
@@ -294,8 +290,10 @@ size_t qlora_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t r) 
   if (K % QN_BLOCK != 0 || N % QN_BLOCK != 0) return 0;
   if (M > kMaxElems / K || M > kMaxElems / N) return 0;
   if (op == QN_OP_FWD) return qn::fwd_workspace(M, N, K, r);
-  if (op == QN_OP_BWD)   // with dropout or without
-    return std::max(qn::bwd_workspace(M, N, K, r, false), bwd_dropout_need(M, N, K, r));
+  if (op == QN_OP_BWD)   // the plain layout; enough for the call with dropout, whose own is the larger for some N = 64
+    return std::max(qn::bwd_workspace(M, N, K, r, false), qn::bwd_workspace(M, N, K, r, true));
+  if (op == QN_OP_BWD_DROPOUT)
+    return qn::bwd_workspace(M, N, K, r, true) + qn::qgemm_part_bytes(M, K, N);
   if (op == QN_OP_FWD_DROPOUT) return qn::fwd_dropout_workspace(M, N, K, r);
   return 0;
 }
@@ -450,7 +448,7 @@ static int linear_bwd(const void *dY, const void *X, const float *H, int64_t M, 
   qn::DropArgs d;
   st = drop_args(drop, d);
   if (st != QN_OK) return st;
-  const size_t need = drop ? bwd_dropout_need(M, W->N, W->K, r) : qn::bwd_workspace(M, W->N, W->K, r, false);
+  const size_t need = qn::bwd_workspace(M, W->N, W->K, r, drop != nullptr);
   if (!workspace || ws_bytes < need) return QN_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QN_ERR_ALIGN;
   if (!qn::codec_tables_ok()) return QN_ERR_VALUE;

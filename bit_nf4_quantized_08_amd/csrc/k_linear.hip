@@ -776,8 +776,8 @@ static BwdPieces bwd_pieces(void *ws, int64_t M, int64_t N, int64_t K, int64_t r
   const int64_t rp = align_up(r, 32), Mp = align_up(M, BK);
   if (!fused) p.Bt = c.take<uint16_t>(rp * N);
   p.dHb = c.take<uint16_t>(M * rp);
-  p.dHt = c.take<uint16_t>(2 * (fused ? r : rp) * Mp);
-  p.sHt = c.take<uint16_t>(2 * (fused ? r : rp) * Mp);
+  p.dHt = c.take<uint16_t>((fused ? 2 * r : rp) * Mp);
+  p.sHt = c.take<uint16_t>((fused ? 2 * r : rp) * Mp);
   const int64_t ranges = fused ? colsum_splits(M, N + K) : colred_splits(M);
   Carve sums = c;
   p.bpart = sums.take<float>(ranges * r * N);
@@ -864,7 +864,9 @@ hipError_t run_bwd(const BwdArgs &a, hipStream_t st) {
     g.qtype = a.sc.qtype;
     g.L2 = w.dHb; g.ldl2 = rp; g.R2 = a.A; g.ldr2 = a.K; g.r = a.r;
     g.out = a.dX; g.ldo = a.K; g.drop = a.drop;
-    g.splits = fused ? qgemm_splits(a.M, a.K, a.N) : 1;
+    // Cut only with room for the partial products: a workspace of QN_OP_BWD bytes has none.
+    const bool room = a.ws_bytes >= w.bytes + qgemm_part_bytes(a.M, a.K, a.N);
+    g.splits = fused && room ? qgemm_splits(a.M, a.K, a.N) : 1;
     if (g.splits > 1) {
       g.part = xpart;
       QN_TRY(launch_qgemm_split(g, true, st));

@@ -28,7 +28,7 @@ QN_OK = 0
 QN_F32, QN_BF16 = 0, 1
 QN_NF4, QN_FP4 = 0, 1
 QUANT_TYPES = {"nf4": QN_NF4, "fp4": QN_FP4}
-QN_OP_FWD, QN_OP_BWD, QN_OP_FWD_DROPOUT = 0, 1, 2
+QN_OP_FWD, QN_OP_BWD, QN_OP_FWD_DROPOUT, QN_OP_BWD_DROPOUT = 0, 1, 2, 3
 QN_ERR_SCRATCH = 8
 QN_ERR_MEMORY = 9
 QN_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -805,7 +805,9 @@ def qlora_linear_fwd_dropout(X, w: NF4Weight, A, B, alpha, drop: Dropout, want_H
 def qlora_linear_bwd_dropout(dY, X, w: NF4Weight, A, B, alpha, drop: Dropout, want_dX=True, use_double_quant=True,
                              out=None, ws=None, H=None):
     """Backward of qlora_linear_fwd_dropout: (dX or None, dA, dB).  ``H`` is the
-    (dropped) one that forward returned, or None to form it again."""
+    (dropped) one that forward returned, or None to form it again.  The workspace
+    is ``workspace(QN_OP_BWD_DROPOUT, ...)``; that of QN_OP_BWD does, slower where
+    dX's contraction would be cut."""
     if A is None or B is None:
         raise ValueError("A and B are required")
     if dY is None:
@@ -813,7 +815,7 @@ def qlora_linear_bwd_dropout(dY, X, w: NF4Weight, A, B, alpha, drop: Dropout, wa
     M, r = _linear_args(X, w, A, B, H, dY, "dY")
     dX, dA, dB = _grads(out, want_dX, X, w, M, r)
     if ws is None:
-        ws = workspace(QN_OP_BWD, M, w.N, w.K, r, X.device)
+        ws = workspace(QN_OP_BWD_DROPOUT, M, w.N, w.K, r, X.device)
     pw = _operand(ws, "ws", _torch().uint8)
     st = w.struct(use_double_quant)
     _launch((dY, X, A, B, H, ws, dX, dA, dB, w.codes, w.absmax, w.absmax_q, w.scale2, drop.offset_dev),

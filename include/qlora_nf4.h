@@ -238,8 +238,8 @@ typedef struct {
 int qn_adamw8_step_multi(int n_tensors, const qn_adamw_tensor *tensors, const qn_adamw_config *cfg,
                          void *stream);
 
-/* Workspace size in bytes for op = QN_OP_FWD, QN_OP_FWD_DROPOUT or QN_OP_BWD (with
- * dropout or without) at the given shape.  Returns 0 for an invalid op or shape. */
+/* Workspace size in bytes for op = QN_OP_FWD, QN_OP_BWD, QN_OP_FWD_DROPOUT or
+ * QN_OP_BWD_DROPOUT at the given shape.  Returns 0 for an invalid op or shape. */
 #define QN_OP_FWD 0
 #define QN_OP_BWD 1
 size_t qlora_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t r);
@@ -378,9 +378,13 @@ int qn_dropout(const void *x, int dtype, int64_t n, const qn_dropout_config *dro
  * keep over [M, K] (element m K + k).  Arguments and shape rules as there; drop
  * is required (its p may be 0: the same sums, nothing dropped).
  * The forward's workspace is qlora_workspace_size(QN_OP_FWD_DROPOUT, ...) bytes
- * (every M takes the MFMA path), the backward's that of QN_OP_BWD; the backward
- * takes M <= 2^24.  A given H is the dropped one, as this forward wrote it. */
+ * (every M takes the MFMA path), the backward's that of QN_OP_BWD_DROPOUT.  The
+ * backward also takes one of QN_OP_BWD bytes; below QN_OP_BWD_DROPOUT it has no room
+ * to cut dX's contraction where few tiles would leave compute units idle, and is
+ * slower there (dX then differs in the order of its fp32 sums).  It takes M <= 2^24.
+ * A given H is the dropped one, as this forward wrote it. */
 #define QN_OP_FWD_DROPOUT 2
+#define QN_OP_BWD_DROPOUT 3
 int qlora_linear_fwd_dropout(const void *X, int64_t M, const qn_nf4_weight *W, const void *A, const void *B,
                              int64_t r, float alpha, const qn_dropout_config *drop, void *Y, float *H_out,
                              void *workspace, size_t ws_bytes, void *stream);
