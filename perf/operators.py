@@ -277,7 +277,7 @@ def prepare(case, seed):
             st["drop"] = lib.Dropout(case["p"], *st["rng"])
             st["w"] = lib.NF4Weight(st["codes"], None, st["absmax_q"], st["scale2"], N, K)
             st["ws"] = lib.workspace(lib.QN_OP_FWD_DROPOUT, M, N, K, r, dev)
-            st["ws_b"] = lib.workspace(lib.QN_OP_BWD, M, N, K, r, dev)
+            st["ws_b"] = lib.workspace(lib.QN_OP_BWD_DROPOUT, M, N, K, r, dev)
         else:
             st["w"] = lib.MXMatrix(st["codes"], st["scales"], N, K)
             st["ws"] = lib.mx_workspace(lib.QN_OP_FWD if op == "mx_fwd" else lib.QN_OP_BWD, M, N, K, r, dev)
