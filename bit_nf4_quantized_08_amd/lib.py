@@ -622,6 +622,11 @@ class Dropout:
         return DropoutStruct(float(self.p), seed, offset, dev)
 
 
+def _need_drop(drop):
+    if drop is None:
+        raise ValueError("drop is required (p = 0 drops nothing)")
+
+
 def _drop_ref(drop):
     return ctypes.byref(drop.struct()) if drop is not None else None
 
@@ -629,6 +634,7 @@ def _drop_ref(drop):
 def dropout(x, drop: Dropout, out=None):
     """qn_dropout of a contiguous fp32 or bf16 tensor of any shape; ``out`` may be
     ``x``.  Applied to a gradient with the same ``drop`` it is the backward."""
+    _need_drop(drop)
     px, dt = _codec_operand(x, "x")
     if out is None:
         out = _torch().empty_like(x)
@@ -788,6 +794,7 @@ def qlora_linear_fwd_dropout(X, w: NF4Weight, A, B, alpha, drop: Dropout, want_H
     """qlora_linear_fwd with dropout on the adapter's input: H = c (keep * X) A^T,
     Y = X bf16(dequant(W))^T + (alpha/r) H B^T.  The workspace is
     ``workspace(QN_OP_FWD_DROPOUT, ...)``."""
+    _need_drop(drop)
     if A is None or B is None:
         raise ValueError("A and B are required")
     M, r = _linear_args(X, w, A, B, H, Y, "Y")
@@ -808,6 +815,7 @@ def qlora_linear_bwd_dropout(dY, X, w: NF4Weight, A, B, alpha, drop: Dropout, wa
     (dropped) one that forward returned, or None to form it again.  The workspace
     is ``workspace(QN_OP_BWD_DROPOUT, ...)``; that of QN_OP_BWD does, slower where
     dX's contraction would be cut."""
+    _need_drop(drop)
     if A is None or B is None:
         raise ValueError("A and B are required")
     if dY is None:
