@@ -46,6 +46,7 @@ import hashlib
 import json
 import os
 import platform
+import re
 import sys
 import time
 
@@ -68,8 +69,8 @@ KERNEL_SOURCE = {
 # 256 MiB copy in the same run, averaged over the step's four calls of the
 # kernel (a call's launches counted together).  The counters see the traffic between the L2 caches and the memory
 # fabric (reads served by the Infinity Cache included), an upper bound on HBM
-# bytes.  Keyed by kernel and workload; `sha256` is that of the kernel's source
-# file and qn_device.h when the counters were taken.
+# bytes.  Keyed by kernel and workload; `sha256` is source_sha of the kernel when
+# the counters were taken.
 TRAFFIC = {
     "gemm_fwd_70b": {"bytes": 1562081494, "sha256": "091b33ddf00ec1a8719d9ccce2e16881e6b3be57649edc14f1a051fae19bf93b"},
     "lowrank_70b": {"bytes": 176677707, "sha256": "8c54093717a28844c54ba54075b907ecf3182c20a214ab02e89c4f95303ed0b6"},
@@ -87,10 +88,19 @@ N2, K2, R2, ALPHA2, M2_DEC, M2_PRE = 4096, 4096, 16, 32.0, 1, 2048
 
 
 def source_sha(kind):
+    """Digest of a kernel's source file and of every header of csrc/ that it includes, directly or not."""
+    texts, todo = {}, [KERNEL_SOURCE[kind]]
+    while todo:
+        f = todo.pop()
+        path = os.path.join(CSRC, f)
+        if f in texts or not os.path.isfile(path):
+            continue
+        with open(path, "rb") as fh:
+            texts[f] = fh.read()
+        todo += re.findall(r'^#include "(qn_[^"]+)"', texts[f].decode(), re.M)
     h = hashlib.sha256()
-    for f in (KERNEL_SOURCE[kind], "qn_device.h"):
-        with open(os.path.join(CSRC, f), "rb") as fh:
-            h.update(fh.read())
+    for f in sorted(texts):
+        h.update(texts[f])
     return h.hexdigest()
 
 
