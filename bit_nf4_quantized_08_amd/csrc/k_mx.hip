@@ -573,8 +573,8 @@ struct HPieces {
 };
 struct AdapterArgs {
   const uint16_t *sH;  // bf16 s H [M, 64], zero beyond r: used as it is when non-null, else
-  const float *hp;     // [hsplits][M][ldh] unscaled (ldh 32 or 64; columns at or beyond r undefined), or null
-  int hsplits, ldh;
+  const float *hp;     // [hsplits][M][64] unscaled (columns at or beyond r undefined), or null
+  int hsplits;
   const uint16_t *B;   // bf16 [N, r]
   int64_t r;
   float s, c;
@@ -587,12 +587,11 @@ __device__ __forceinline__ void sum_h(const AdapterArgs &a, int64_t M, int64_t m
   for (int t = 0; t < 8; ++t) h[t] = 0.0f;
   // Batches of four partial sums, loaded without a condition (past the last
   // one it is read again and dropped), so that a batch waits once.
-  const int jc = j0 < a.ldh ? j0 : 0;
   for (int q0 = first; q0 < end; q0 += 4) {
     f32x4 v[4][2];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.hp + ((int64_t)min(q0 + q, end - 1) * M + m) * a.ldh + jc);
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.hp + ((int64_t)min(q0 + q, end - 1) * M + m) * 64 + j0);
       v[q][0] = p[0];
       v[q][1] = p[1];
     }
@@ -740,7 +739,7 @@ __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4)))
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (32 * q >= a.ad.r) break;
-      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.ad.hp + ((int64_t)seg * a.M + min((int64_t)l16, a.M - 1)) * a.ad.ldh + 32 * q + 8 * kb);
+      const f32x4 *p = reinterpret_cast<const f32x4 *>(a.ad.hp + ((int64_t)seg * a.M + min((int64_t)l16, a.M - 1)) * 64 + 32 * q + 8 * kb);
       ph[q][0] = p[0];
       ph[q][1] = p[1];
       pb[q] = load_b(a.ad, min(n0 + l16, a.N - 1), 32 * q + 8 * kb);
@@ -1037,7 +1036,7 @@ hipError_t run_decode(const MxFwdArgs &a, const FwdPieces &w, hipStream_t st) {
   const int64_t C = mx_chunks(a.K);
   const dim3 block(64 * DW);
   QN_TRY(launch_prep(a, w, st));
-  const AdapterArgs ad{nullptr, a.r ? w.h_part : nullptr, prep_hsplits(a.M, a.N, a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
+  const AdapterArgs ad{nullptr, a.r ? w.h_part : nullptr, prep_hsplits(a.M, a.N, a.K), a.B, a.r, a.s, a.drop.c, a.H_out};
   const MxDecodeArgs d{w.xc, w.xs, a.M, a.N, C, a.codes, a.scales, ad, p.ksplits == 1 ? a.Y : nullptr, w.y_part,
                        p.nk, p.row_blocks};
   const dim3 grid((unsigned)(p.row_blocks * p.ksplits));
@@ -1128,7 +1127,7 @@ hipError_t run_mx_fwd(const MxFwdArgs &a, hipStream_t st) {
   }
   if (p.splits == 1) return launch_tiles<2, 2, 2, 2, false>(g, st);
   QN_TRY((launch_tiles<2, 2, 2, 2, true>(g, st)));
-  const AdapterArgs ad{w.sH, a.r ? w.h_part : nullptr, prep_hsplits(a.M, a.N, a.K), 64, a.B, a.r, a.s, a.drop.c, a.H_out};
+  const AdapterArgs ad{w.sH, a.r ? w.h_part : nullptr, prep_hsplits(a.M, a.N, a.K), a.B, a.r, a.s, a.drop.c, a.H_out};
   return launch_finish(MxFinishArgs{w.y_part, p.splits, ad, a.M, a.N, a.Y}, st);
 }
 
