@@ -790,33 +790,36 @@ __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4)))
       const int j0 = 32 * q + 8 * kb;
       if (32 * q >= a.ad.r) break;
       bf16x8 bv[G];
+      float h[MB][8];
       uint32_t top = 0;
 #pragma unroll
+      for (int g = 0; g < G; ++g) bv[g] = PRE ? pb[q] : load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0);
+#pragma unroll
       for (int g = 0; g < G; ++g) {
-        bv[g] = PRE ? pb[q] : load_b(a.ad, min(n0 + 16 * g + l16, a.N - 1), j0);
         const u32x4 u[1] = {__builtin_bit_cast(u32x4, bv[g])};
         top = max(top, unit_amax<true>(u));
       }
-      const bool whole = __any(top >= 0x7F80u);
+      // Expected false, so that its code lies out of the way too.
+      const bool whole = __builtin_expect(__any(top >= 0x7F80u), 0);
 #pragma unroll
       for (int b = 0; b < MB; ++b) {
-        const int64_t m = 16 * b + l16, mc = min(m, a.M - 1);
-        float h[8];
         if (PRE) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) h[t] = j0 + t < a.ad.r ? ph[q][t >> 2][t & 3] * a.ad.c : 0.0f;
+          for (int t = 0; t < 8; ++t) h[b][t] = j0 + t < a.ad.r ? ph[q][t >> 2][t & 3] * a.ad.c : 0.0f;
         } else {
-          sum_h(a.ad, a.M, mc, j0, seg, seg + 1, h);
+          sum_h(a.ad, a.M, min((int64_t)(16 * b + l16), a.M - 1), j0, seg, seg + 1, h[b]);
         }
-        if (whole) sum_h(a.ad, a.M, mc, j0, 0, seg == 0 ? a.ad.hsplits : 0, h);
-        if (!whole || seg == 0) {
-          const HPieces p = pieces_of(a.ad, h);
+      }
+      if (__builtin_expect(whole, 0)) {
+#pragma unroll
+        for (int b = 0; b < MB; ++b) sum_h(a.ad, a.M, min((int64_t)(16 * b + l16), a.M - 1), j0, 0, a.ad.hsplits, h[b]);
+      }
+      if (!whole || seg == 0) {
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          const HPieces p = pieces_of(a.ad, h[b]);
 #pragma unroll
           for (int g = 0; g < G; ++g) acc[g][b] = add_adapter(acc[g][b], bv[g], p);
-        }
-        if (a.ad.H_out && rb == 0 && rg == 0 && seg == 0) {
-          sum_h(a.ad, a.M, mc, j0, 0, a.ad.hsplits, h);
-          if (m < a.M) store_h(a.ad, m, j0, h);
         }
       }
     }
@@ -844,6 +847,17 @@ __global__ __launch_bounds__(64 * DW) __attribute__((amdgpu_waves_per_eu(4, 4)))
       else a.y_part[((int64_t)ks * a.M + m) * a.N + n] = v;
     }
   }
+  // H itself, written by one wave, comes last: its code among the above, skipped by
+  // the others, costs them 0.3 us of fetching (one token, 8192 x 8192).
+  if (a.out && a.ad.hp && a.ad.H_out && rb == 0 && wave == 0)
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+      for (int j0 = 8 * kb; j0 < a.ad.r; j0 += 32) {
+        const int64_t m = 16 * b + l16;
+        float h[8];
+        sum_h(a.ad, a.M, min(m, a.M - 1), j0, 0, a.ad.hsplits, h);
+        if (m < a.M) store_h(a.ad, m, j0, h);
+      }
 }
 
 // Y = sum of the partial products + s H B^T; also writes H.  A wave owns 16
