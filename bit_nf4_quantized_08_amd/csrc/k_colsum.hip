@@ -24,7 +24,8 @@
 // barriers from registers that were loaded a step earlier: with two, 64 ranks
 // would leave room for one workgroup on a CU, and half the loads in flight.
 // The partial sums of the row ranges go to `part` and are added in order by
-// the reduce kernel, so results depend on the shape alone.
+// the reduce kernel, so results depend on the shape and, through the number of
+// ranges, on the device's CU count.
 
 #include <algorithm>
 

@@ -13,10 +13,11 @@
 //   mx_dequant_kernel    codes and scales -> fp32 or bf16; bound by memory (the
 //                        same to bf16: 15.7 us, 5.4 TB/s)
 //   mx_gemm_kernel       tiles of mx(X) W^T with the adapter term, optionally over
-//                        a part of K with fp32 partial sums; bound by the matrix
-//                        cores and the clock they sustain (4096 x 8192 x 8192, r =
-//                        64: 134 to 138 us, 4.1 PFLOP/s; matrix pipes busy 57 % of
-//                        the cycles at 1.75 GHz, loads into LDS next)
+//                        a part of K with fp32 partial sums; bound by LDS (a step's
+//                        196 KB of reads and 68 KB of writes, about 2080 cycles) and
+//                        the matrix cores (2048 cycles), which overlap little: 3700
+//                        cycles a step (4096 x 8192 x 8192, r = 64: 134 to 138 us, 4.1
+//                        PFLOP/s; matrix pipes busy 57 % of the cycles at 1.75 GHz)
 //   mx_prep_kernel       few rows: X^ and the adapter's H partials; bound by its
 //                        launch and one memory latency (M = 1, K = 8192, r = 64: 4.0 us)
 //   mx_decode_kernel     M <= 32: streams the weights; bound by memory (M = 13, 28672
@@ -199,7 +200,10 @@ __global__ __launch_bounds__(kThreads) void mx_dequant_kernel(const uint8_t *__r
 // The scale bytes come with them (8 BM and 8 BN contiguous bytes, 16 a lane).
 // The adapter term bf16(s H) B^T (r <= 64) follows as bf16 MFMAs into the same
 // accumulators, its fragments read from global memory (H is small, B is read
-// once per tile column).  (Reading them a sub-step ahead, or leaving out the
+// once per tile column).  One piece of s H rounds each product by 2^-8 at most, as
+// Y's own rounding does Y: it shows where the adapter's part is most of Y (error
+// against 64 bits at 4096 x 8192 x 8192: 0.0017 of Y's norm, that of a bf16 result
+// formed in fp32); two pieces would double these MFMAs and s H's memory.  (Reading them a sub-step ahead, or leaving out the
 // loads past the last step, changes nothing at 4096 x 8192 x 8192: 136.5 us at
 // best in each form, the clock falls by what the schedule gains.)
 struct MxGemmArgs {
@@ -474,8 +478,10 @@ void mx_gemm_kernel(MxGemmArgs a) {
 
 // ------------------------------------------------------------------ few rows
 // M <= 32, two launches.  The first quantises X and forms partial sums of H = X
-// A^T (in the streaming kernel every workgroup would repeat both: 11.4 + 9.8 us
-// against 5.2 + 8.9 at M = 1, 8192 x 8192, r = 64); the second streams the weights
+// A^T (with both repeated in every workgroup of the streaming kernel 11.4 + 9.8 us
+// against 5.2 + 8.9 at M = 1, 8192 x 8192, r = 64; H is what costs there: a wave needs
+// only its own columns of X^, and quantising those alone in the streaming kernel is
+// not built); the second streams the weights
 // and, when a workgroup's waves cover all of K (up to 8192 columns), finishes Y.
 //
 // Streaming: a wave owns 16 weight rows x 1024 columns at a time, eight
@@ -572,7 +578,7 @@ struct HPieces {
   bf16x8 hi, lo;
 };
 struct AdapterArgs {
-  const uint16_t *sH;  // bf16 s H [M, 64], zero beyond r: used as it is when non-null, else
+  const uint16_t *sH;  // bf16 s H [M, 64], zero beyond r (one piece, as in the tiles): used when non-null, else
   const float *hp;     // [hsplits][M][64] unscaled (columns at or beyond r undefined), or null
   int hsplits;
   const uint16_t *B;   // bf16 [N, r]

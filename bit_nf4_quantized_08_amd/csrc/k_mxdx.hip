@@ -28,6 +28,10 @@
 // 8 / WC): 32 UW consecutive columns of dX.  "Tile column" x of a wave is unit
 // (q, u) = (x / 8 / UW, x / 8 % UW).
 //
+// dH enters in one bf16 piece: its rounding is 2^-8 of each product of the adapter
+// term at most, as the result's is of dX (error against 64 bits at 4096 x 8192 x 8192:
+// 0.0017 of dX's norm, that of a bf16 result formed in fp32).
+//
 // G's stage is swizzled in 16-byte pieces as in the forward: piece k of row r
 // at slot k ^ ((r >> 1) & 7).  Contraction order: in sub-step c of a step, lane
 // half h supplies rows 32 h + 8 c .. + 7 of both operands.

@@ -446,7 +446,8 @@ size_t qlora_mx_workspace_size(int op, int64_t M, int64_t N, int64_t K, int64_t 
  * Shape rules: M >= 1, N % 64 == 0, K % 64 == 0, N * 128 C <= INT32_MAX,
  * N and K <= 2^22, M <= 2^24, M * C <= 2^28, 0 <= r <= QN_MAX_RANK.  A
  * non-finite block of X makes its row of Y NaN.  M <= 32 streams the weights once
- * (both operands on the matrix cores), larger M runs tiles.  The workspace is
+ * (both operands on the matrix cores), larger M runs tiles; the two round s H and
+ * order their sums differently, so a row's last bit may differ with M.  The workspace is
  * written by the call: calls that may run at the same time, captured graphs
  * among them, need one each. */
 int qlora_mx_linear_fwd(const void *X, int64_t M, const qn_mx_matrix *W, const void *A, const void *B, int64_t r,
