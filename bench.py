@@ -72,9 +72,9 @@ KERNEL_SOURCE = {
 # bytes.  Keyed by kernel and workload; `sha256` is source_sha of the kernel when
 # the counters were taken.
 TRAFFIC = {
-    "gemm_fwd_70b": {"bytes": 1562081494, "sha256": "091b33ddf00ec1a8719d9ccce2e16881e6b3be57649edc14f1a051fae19bf93b"},
-    "lowrank_70b": {"bytes": 176677707, "sha256": "8c54093717a28844c54ba54075b907ecf3182c20a214ab02e89c4f95303ed0b6"},
-    "gemv_70b": {"bytes": 114969718, "sha256": "049094bb4d2ded67c182ccae92b4642599c446d89f0aa5685596677bd807dc34"},
+    "gemm_fwd_70b": {"bytes": 1560865210, "sha256": "a8e7cd07a354324bcbc4d71408017d89748ff4935214fc0fcb7720a7e61e2b12"},
+    "lowrank_70b": {"bytes": 176676966, "sha256": "1cd00653d5aea2da6ef5aa6709f227a5a39c36522b3ad9edfb16d318b22f419c"},
+    "gemv_70b": {"bytes": 114969651, "sha256": "fe0c94bf60f1e2551e7a43005ba2185f8709ca6eebdad3f6b54929cd8067b188"},
 }
 
 # The configurations (N, K) of the linear layers.

@@ -13,16 +13,17 @@
 //   mx_dequant_kernel    codes and scales -> fp32 or bf16; bound by memory (the
 //                        same to bf16: 15.7 us, 5.4 TB/s)
 //   mx_gemm_kernel       tiles of mx(X) W^T with the adapter term, optionally over
-//                        a part of K with fp32 partial sums; bound by LDS (a step's
-//                        196 KB of reads and 68 KB of writes, about 2080 cycles) and
-//                        the matrix cores (2048 cycles), which overlap little: 3700
-//                        cycles a step (4096 x 8192 x 8192, r = 64: 134 to 138 us, 4.1
-//                        PFLOP/s; matrix pipes busy 57 % of the cycles at 1.75 GHz)
+//                        a part of K with fp32 partial sums (4096 x 8192 x 8192, r =
+//                        64: 134 to 138 us, 4.1 PFLOP/s at 1.75 GHz).  A step's 3700
+//                        cycles are near the sum of the MFMAs' 2048 (57 % busy) and
+//                        LDS' 196 KB of reads and 68 KB of writes (2080 at 128 bytes a
+//                        cycle; the LDS-active counter, which leaves the direct loads
+//                        out, shows 1070): the two overlap little
 //   mx_prep_kernel       few rows: X^ and the adapter's H partials; bound by its
 //                        launch and one memory latency (M = 1, K = 8192, r = 64: 4.0 us)
 //   mx_decode_kernel     M <= 32: streams the weights; bound by memory (M = 13, 28672
 //                        x 8192: 125 MB, 22 us, 5.7 TB/s; M = 1, 8192 x 8192: 36 MB,
-//                        8.7 us, 4.1 TB/s, a third of it start and end)
+//                        9.0 us, 4.0 TB/s, a third of it start and end)
 //   mx_finish_kernel     adds partial products and the adapter term; bound by its
 //                        launch at the sizes that cut K (about 5 us)
 
