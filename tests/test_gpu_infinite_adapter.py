@@ -90,3 +90,32 @@ def test_adapter_gradients(base, M, r, kind):
         np.testing.assert_array_equal(np.isinf(a) * np.sign(a), np.isinf(b) * np.sign(b), err_msg=name)
         f = np.isfinite(b)
         assert rel_fro(a[f], b[f]) <= 2 * REL_FRO_TOL   # either is within REL_FRO_TOL of the exact one
+
+
+@pytest.mark.parametrize("M, N, K", [(16, 8256, 4160), (5, 16448, 4160), (20, 8256, 4160), (32, 512, 4160)])
+@pytest.mark.parametrize("kind", ["H", "B"])
+@pytest.mark.parametrize("want_H", [True, False])
+def test_mx_forward_row_groups(M, N, K, kind, want_H):
+    """Two and four groups of weight rows per wave, ranks beyond 32, H returned or not."""
+    say(f"mx forward, infinite {kind}, row groups, M={M} N={N} K={K}")
+    r, j0, k0, n0 = 40, 37, 77, N - 10
+    gen = torch.Generator().manual_seed(M)
+    X, A, B, W = (torch.randn(t, generator=gen) for t in ((M, K), (r, K), (N, r), (N, K)))
+    X[:, k0] = torch.where(torch.arange(M) % 3 == 1, -1.0, 1.0)
+    if kind == "B":
+        B[n0, j0] = INF
+    else:
+        A[j0, :] = 0.0
+        A[j0, k0] = INF
+    X, A, B = (t.to(torch.bfloat16).to(dev()) for t in (X, A, B))
+    res = lib.qlora_mx_linear_fwd(X, lib.mxfp4_quantize(W.to(dev())), A, B, float(r), want_H=want_H)
+    got = host(res[0] if want_H else res)
+    H = X.double() @ A.double().t()   # the column's sign; sums of 4160 terms of order 1, far from zero in 64 bits
+    col = host(torch.sign(H[:, j0])).astype(np.float32)
+    if want_H:
+        np.testing.assert_array_equal(np.sign(host(res[1])[:, j0]), col)
+    if kind == "B":
+        np.testing.assert_array_equal(got[:, n0], col * np.float32(INF))
+        assert np.isfinite(np.delete(got, n0, axis=1)).all()
+    else:
+        np.testing.assert_array_equal(got, np.sign(col[:, None] * host(B)[:, j0][None, :]) * np.float32(INF))
